@@ -60,6 +60,11 @@ class MoeArgs(ctypes.Structure):
                 ("out", c_ptr), ("ld_out", c_i64)]
 
 
+class MatrixBank(ctypes.Structure):
+    _fields_ = [("dtype", c_i32), ("num_experts", c_i32), ("n", c_i64), ("k", c_i64), ("ld", c_i64),
+                ("expert_stride", c_i64), ("w", c_ptr)]
+
+
 _LAYOUT_FIELDS = ["x_q", "x_scales", "x_gscale", "counts", "offsets", "dst2src", "route2dst",
                   "rows_q", "rows_scales", "gateup", "gateup_bytes", "act_q", "act_q_bytes",
                   "act_scales", "act_scales_bytes", "act_gscale", "down", "down_bytes", "partials",
@@ -97,6 +102,16 @@ _SIGNATURES = [
     ("ftmoe_forward_workspace_layout", c_i32, [ctypes.POINTER(MoeShape), ctypes.POINTER(WorkspaceLayout)]),
     ("ftmoe_moe_forward", c_i32, [ctypes.POINTER(MoeArgs), c_ptr, c_size, c_ptr]),
     ("ftmoe_moe_forward_noalloc", c_i32, [ctypes.POINTER(MoeArgs), c_ptr]),
+    ("ftmoe_grouped_matmul", c_i32, [c_ptr, c_i64, c_i64, c_ptr, ctypes.POINTER(MatrixBank), c_i32, c_ptr, c_i64,
+                                     c_i32, c_ptr]),
+    ("ftmoe_grouped_matmul_wgrad", c_i32, [c_ptr, c_i64, c_ptr, c_i64, c_i64, c_i32, c_ptr,
+                                           ctypes.POINTER(MatrixBank), c_i32, c_ptr]),
+    ("ftmoe_grouped_matmul_wgrad_saved", c_i32, [c_ptr, c_i64, c_i32, ctypes.POINTER(Act), c_ptr,
+                                                 ctypes.POINTER(MatrixBank), c_i32, c_ptr]),
+    ("ftmoe_silu_mul_save", c_i32, [c_ptr, c_i32, c_i64, c_i64, c_i64, c_ptr, c_ptr, c_i64, c_i32, c_i32, c_ptr,
+                                    c_ptr, c_ptr]),
+    ("ftmoe_silu_mul_backward", c_i32, [c_ptr, c_ptr, c_i32, c_i64, c_i64, c_ptr, c_ptr, c_i64, c_i32, c_ptr, c_ptr,
+                                        c_i64, c_ptr, c_i64, c_ptr, c_ptr]),
     ("ftmoe_selftest_wait_timeout", c_i32, [ctypes.c_uint64, c_ptr, c_ptr]),
     ("ftmoe_selftest_shared_division", c_i32, [c_ptr, c_ptr]),
     ("ftmoe_expert_slots", c_i32, [c_ptr, c_i64, c_ptr, c_ptr, c_i32, c_ptr, c_i32, c_i64, c_i32, c_ptr, c_ptr,
@@ -313,6 +328,129 @@ def ftmoe_expert_slots(expert_ids, slot_expert, slot_usage, expert_slot, step, m
         _p(expert_ids), expert_ids.numel(), _p(slot_expert), _p(slot_usage), slot_expert.numel(),
         _p(expert_slot), expert_slot.numel(), int(step), int(max_fetch), _p(fetch_plan), _p(n_fetch),
         _stream(stream)))
+
+
+def _dtype_code(t, name):
+    if t.dtype not in _OUT_DTYPES:
+        raise ValueError(f"{name} dtype {t.dtype} is not one of bf16, fp16, fp32")
+    return _OUT_DTYPES[t.dtype]
+
+
+def _same(want, **tensors):
+    """Devices, shapes and dtypes that the C entry cannot see: {name: (tensor, shape)} against dtype `want`
+    (None: any). Rows are contiguous."""
+    for name, (t, shape) in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} is not on a CUDA device")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if want is not None and t.dtype != want:
+            raise ValueError(f"{name} is {t.dtype}, expected {want}")
+        if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"the rows of {name} are not contiguous")
+
+
+def _ld(t):
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+
+
+def make_matrix_bank(w):
+    """MatrixBank view of a [E, n, k] tensor of bf16, fp16 or fp32 matrices (any expert and row
+    strides, contiguous rows)."""
+    E, n, k = w.shape
+    _same(None, w=(w, (E, n, k)))
+    ld = w.stride(1) if n > 1 else max(k, w.stride(1))
+    es = w.stride(0) if E > 1 else max((n - 1) * ld + k, w.stride(0))
+    return MatrixBank(_dtype_code(w, "w"), E, n, k, ld, es, _p(w))
+
+
+def _check_offsets(offsets, E):
+    _same(torch.int32, offsets=(offsets, (E + 1,)))
+
+
+def ftmoe_grouped_matmul(a, offsets, w, out, input_grad=False, stream=None):
+    """out rows = a rows times the transposed matrix of their expert (input_grad: times the
+    matrix itself). a [rows, k] (input_grad: [rows, n]), w [E, n, k], both bf16 or fp16; out
+    [rows, n] (input_grad: [rows, k]) bf16, fp16 or fp32; offsets int32 [E + 1]."""
+    E, n, k = w.shape
+    rows = a.shape[0]
+    _check_offsets(offsets, E)
+    _same(w.dtype, a=(a, (rows, n if input_grad else k)))
+    _same(None, out=(out, (rows, k if input_grad else n)))
+    bank = make_matrix_bank(w)
+    _check("ftmoe_grouped_matmul", lib().ftmoe_grouped_matmul(
+        _p(a), rows, _ld(a), _p(offsets), ctypes.byref(bank), int(bool(input_grad)), _p(out), _ld(out),
+        out_dtype_code(out), _stream(stream)))
+
+
+def ftmoe_grouped_matmul_wgrad(dy, x, offsets, dw, accumulate=False, stream=None):
+    """dw[e] = dy_e^T x_e over the rows of expert e (accumulate: added to dw). dy [rows, n] and
+    x [rows, k] bf16 or fp16, dw [E, n, k] bf16, fp16 or fp32."""
+    E, n, k = dw.shape
+    rows = dy.shape[0]
+    _check_offsets(offsets, E)
+    _same(dy.dtype, dy=(dy, (rows, n)), x=(x, (rows, k)))
+    bank = make_matrix_bank(dw)
+    _check("ftmoe_grouped_matmul_wgrad", lib().ftmoe_grouped_matmul_wgrad(
+        _p(dy), _ld(dy), _p(x), _ld(x), rows, _dtype_code(dy, "dy"), _p(offsets), ctypes.byref(bank),
+        int(bool(accumulate)), _stream(stream)))
+
+
+def ftmoe_grouped_matmul_wgrad_saved(dy, q, scales, offsets, dw, fmt=FMT_MXFP8, accumulate=False, stream=None):
+    """The same with x as MXFP8 rows: q uint8 [rows, k], scales uint8 [rows, k / 32]."""
+    E, n, k = dw.shape
+    rows = dy.shape[0]
+    _check_offsets(offsets, E)
+    _same(dy.dtype, dy=(dy, (rows, n)))
+    if fmt == FMT_MXFP8:
+        _same(torch.uint8, q=(q, (rows, k)), scales=(scales, (rows, k // 32)))
+        _dense(q=q, scales=scales)
+    act, bank = Act(fmt, 0, rows, k, _p(q), _p(scales), None), make_matrix_bank(dw)
+    _check("ftmoe_grouped_matmul_wgrad_saved", lib().ftmoe_grouped_matmul_wgrad_saved(
+        _p(dy), _ld(dy), _dtype_code(dy, "dy"), ctypes.byref(act), _p(offsets), ctypes.byref(bank),
+        int(bool(accumulate)), _stream(stream)))
+
+
+def _dense(**tensors):
+    for name, t in tensors.items():
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name} is not contiguous")
+
+
+def _check_saved(q, scales, rows, inter, fmt):
+    """q uint8 [rows, 2 * inter] and scales [rows, 2 * groups] of a saved gate/up row."""
+    _same(torch.uint8, q=(q, (rows, 2 * inter)))
+    if fmt == FMT_FP8:
+        _same(torch.float32, scales=(scales, (rows, 2 * cdiv(inter, 128))))
+    elif fmt == FMT_MXFP8:
+        _same(torch.uint8, scales=(scales, (rows, 2 * (inter // 32))))
+    _dense(q=q, scales=scales)
+
+
+def ftmoe_silu_mul_save(gu, h, q, scales, fmt=FMT_MXFP8, rows_dev=None, stream=None):
+    """h = silu(gate) * up from gu [rows, 2 * inter], and both halves kept in 8 bits: q uint8
+    [rows, 2 * inter], scales [rows, 2 * groups] (FP8: fp32 per 128, MXFP8: uint8 per 32)."""
+    rows, inter = h.shape
+    _same(None, gu=(gu, (rows, 2 * inter)), h=(h, (rows, inter)))
+    _check_saved(q, scales, rows, inter, fmt)
+    _check("ftmoe_silu_mul_save", lib().ftmoe_silu_mul_save(
+        _p(gu), _dtype_code(gu, "gu"), rows, inter, _ld(gu), _p(rows_dev), _p(h), _ld(h), _dtype_code(h, "h"), fmt,
+        _p(q), _p(scales), _stream(stream)))
+
+
+def ftmoe_silu_mul_backward(q, scales, dh, dgu, hw=None, row_weights=None, dweights=None, fmt=FMT_MXFP8,
+                            rows_dev=None, stream=None):
+    """Gradients from the kept gate/up rows: dgu [rows, 2 * inter], hw = weight * h [rows, inter]
+    and dweights fp32 [rows], for the gradient dh [rows, inter] of the unweighted h."""
+    rows, inter = dh.shape
+    _same(dh.dtype, dh=(dh, (rows, inter)), dgu=(dgu, (rows, 2 * inter)), hw=(hw, (rows, inter)))
+    _same(torch.float32, row_weights=(row_weights, (rows,)), dweights=(dweights, (rows,)))
+    _check_saved(q, scales, rows, inter, fmt)
+    _check("ftmoe_silu_mul_backward", lib().ftmoe_silu_mul_backward(
+        _p(q), _p(scales), fmt, rows, inter, _p(rows_dev), _p(dh), _ld(dh), _dtype_code(dh, "dh"), _p(row_weights),
+        _p(dgu), _ld(dgu), _p(hw), 0 if hw is None else _ld(hw), _p(dweights), _stream(stream)))
 
 
 def ftmoe_selftest_wait_timeout(timeout_ns, elapsed_ns=None, stream=None):

@@ -1,0 +1,256 @@
+// SiLU-and-mul that keeps its gate/up rows in 8 bits, and its backward pass from them.
+//
+// Forward, per row: h = silu(g) * u with silu(g) = g * s, s = 1 / (1 + exp(-g)); g and u are
+// kept as e4m3 codes with an fp32 scale per 128 (amax / 448) or a power of two per 32.
+// Backward, with the kept g and u, the gradient dh of the unweighted h and the routing weight w:
+//   d h / d u = g s,   d h / d g = u s (1 + g (1 - s))
+//   dgu = w dh (d h / d g | d h / d u),   hw = w h,   dweight = sum_i dh_i h_i
+// Both passes are elementwise but for the group maxima and dweight: they are bound by memory.
+// The forward moves 8 bytes per intermediate column (4 read, 2 + 2 written) and 1/16 to 1/32 of
+// scales; the backward 10 (2 codes and 2 of dh read, 4 + 2 written). Keeping gate/up in bf16
+// would move 4 more bytes per column and hold twice the memory between the passes.
+#include "common.cuh"
+#include "elem16.cuh"
+#include "internal.h"
+
+namespace ftmoe {
+
+namespace act_train {
+
+__device__ __forceinline__ int64_t valid_rows(int64_t rows, const int32_t* rows_dev) {
+  if (rows_dev == nullptr) return rows;
+  const int64_t d = *rows_dev;
+  return d < 0 ? 0 : (d < rows ? d : rows);
+}
+
+// Codes of 8 values that share a maximum with the lanes around them: 16 lanes (FP8's group of
+// 128) or 4 (MXFP8's 32). Every lane of the warp calls it. sc: the group's fp32 scale, or the
+// E8M0 byte.
+template <bool kMx>
+__device__ __forceinline__ uint2 quantize8(const float (&v)[8], float& sc, uint8_t& byte) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+#pragma unroll
+  for (int o = kMx ? 2 : 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float q[8];
+  if constexpr (kMx) {
+    // floor(log2 m) off the exponent field; a zero or subnormal maximum takes the smallest scale
+    const int ef = (int)((__float_as_uint(m) >> 23) & 0xff);
+    const int shared = ef == 0 || ef < 8 ? -127 : ef - 127 - 8;
+    byte = (uint8_t)(shared + 127);
+    const float f = __uint_as_float((uint32_t)(127 - shared) << 23);  // 2^-shared, exact
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = v[i] * f;
+  } else {
+    sc = div_rn(m, kE4M3Max);
+    if (m > 0.0f) {
+      const SharedDivisor d(sc);  // v / sc as IEEE division rounds it
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] = d.div(v[i]);
+    } else {
+      return make_uint2(0u, 0u);
+    }
+  }
+  return make_uint2((uint32_t)f2_to_e4m3x2(q[0], q[1]) | ((uint32_t)f2_to_e4m3x2(q[2], q[3]) << 16),
+                    (uint32_t)f2_to_e4m3x2(q[4], q[5]) | ((uint32_t)f2_to_e4m3x2(q[6], q[7]) << 16));
+}
+
+__device__ __forceinline__ void store_codes(uint8_t* q, uint2 c, bool vec, int n) {
+  if (vec && n >= 8) {
+    *reinterpret_cast<uint2*>(q) = c;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) q[i] = (uint8_t)((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
+  }
+}
+
+// A half-warp per (row, 128 columns): a lane owns 8 columns of both halves.
+template <typename In, typename Out, bool kMx>
+__global__ void __launch_bounds__(256) silu_save_kernel(
+    const typename In::T* __restrict__ gu, int64_t rows, int64_t inter, int64_t ld_gu,
+    const int32_t* __restrict__ rows_dev, typename Out::T* __restrict__ h, int64_t ld_h, uint8_t* __restrict__ q,
+    void* __restrict__ scales, bool vec_gu, bool vec_h, bool vec_q) {
+  const int64_t ng = (inter + kGroup - 1) / kGroup;
+  const int64_t units = valid_rows(rows, rows_dev) * ng;
+  const int lane = threadIdx.x & 31, hl = lane & 15;
+  const int64_t nwarps = (int64_t)gridDim.x * (blockDim.x >> 5);
+  // the loop bound is uniform over the warp, so every shuffle sees all 32 lanes
+  for (int64_t w = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); 2 * w < units; w += nwarps) {
+    const int64_t unit = 2 * w + (lane >> 4);
+    const bool live = unit < units;
+    const int64_t row = live ? unit / ng : 0, grp = live ? unit - row * ng : 0;
+    const int64_t c0 = grp * kGroup + hl * 8;
+    const int64_t left = live ? inter - c0 : 0;
+    const int n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
+    float g[8], u[8], a[8];
+    elem_load8<In>(gu + row * ld_gu + c0, vec_gu, n, g);
+    elem_load8<In>(gu + row * ld_gu + inter + c0, vec_gu, n, u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = silu_mul_1(g[i], u[i]);
+    float sg, su;
+    uint8_t bg, bu;
+    const uint2 cg = quantize8<kMx>(g, sg, bg), cu = quantize8<kMx>(u, su, bu);
+    if (n > 0) {
+      elem_store8<Out>(h + row * ld_h + c0, vec_h, n, a);
+      uint8_t* qr = q + row * 2 * inter + c0;
+      store_codes(qr, cg, vec_q, n);
+      store_codes(qr + inter, cu, vec_q, n);
+      if constexpr (kMx) {
+        if ((lane & 3) == 0) {
+          const int64_t nb = inter / kMxBlock;
+          uint8_t* s = static_cast<uint8_t*>(scales) + row * 2 * nb + c0 / kMxBlock;
+          s[0] = bg;
+          s[nb] = bu;
+        }
+      } else if (hl == 0) {
+        float* s = static_cast<float*>(scales) + row * 2 * ng + grp;
+        s[0] = sg;
+        s[ng] = su;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void load_codes(const uint8_t* q, bool vec, int n, float (&v)[8]) {
+  uint32_t c[2] = {0u, 0u};
+  if (vec && n >= 8) {
+    const uint2 r = *reinterpret_cast<const uint2*>(q);
+    c[0] = r.x, c[1] = r.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) c[i >> 2] |= (uint32_t)q[i] << (8 * (i & 3));
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = e4m3_to_f((uint8_t)(c[i >> 2] >> (8 * (i & 3))));
+}
+
+// kTpr threads per row, 8 columns each per pass; 256 / kTpr rows per CTA. dweights: a thread
+// adds its columns in ascending order, then a butterfly over the warp and the warps in order.
+template <typename Elem, bool kMx, int kTpr>
+__global__ void __launch_bounds__(256) silu_backward_kernel(
+    const uint8_t* __restrict__ q, const void* __restrict__ scales, int64_t rows, int64_t inter,
+    const int32_t* __restrict__ rows_dev, const typename Elem::T* __restrict__ dh, int64_t ld_dh,
+    const float* __restrict__ row_weights, typename Elem::T* __restrict__ dgu, int64_t ld_dgu,
+    typename Elem::T* __restrict__ hw, int64_t ld_hw, float* __restrict__ dweights, bool vec_q, bool vec_dh,
+    bool vec_dgu, bool vec_hw) {
+  constexpr int kRows = 256 / kTpr, kWarps = kTpr / 32;
+  __shared__ float part[2][8];
+  const int64_t limit = valid_rows(rows, rows_dev);
+  const int sub = threadIdx.x / kTpr, tid = threadIdx.x % kTpr, lane = threadIdx.x & 31;
+  const int64_t nb = kMx ? inter / kMxBlock : (inter + kGroup - 1) / kGroup;
+  int phase = 0;
+  // the loop bound is the same for every thread of the CTA
+  for (int64_t base = (int64_t)blockIdx.x * kRows; base < limit; base += (int64_t)gridDim.x * kRows, phase ^= 1) {
+    const int64_t row = base + sub;
+    const bool live = row < limit;
+    float dot = 0.0f;
+    const float w = live && row_weights != nullptr ? row_weights[row] : 1.0f;
+    for (int64_t c0 = (int64_t)tid * 8; live && c0 < inter; c0 += kTpr * 8) {
+      const int64_t left = inter - c0;
+      const int n = left >= 8 ? 8 : (int)left;
+      float g[8], u[8], d[8], sg, su;
+      load_codes(q + row * 2 * inter + c0, vec_q, n, g);
+      load_codes(q + row * 2 * inter + inter + c0, vec_q, n, u);
+      elem_load8<Elem>(dh + row * ld_dh + c0, vec_dh, n, d);
+      if constexpr (kMx) {
+        const uint8_t* s = static_cast<const uint8_t*>(scales) + row * 2 * nb + c0 / kMxBlock;
+        sg = e8m0_to_f(s[0]);
+        su = e8m0_to_f(s[nb]);
+      } else {
+        const float* s = static_cast<const float*>(scales) + row * 2 * nb + c0 / kGroup;
+        sg = s[0];
+        su = s[nb];
+      }
+      float dg[8], du[8], hv[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float gi = g[i] * sg, ui = u[i] * su;
+        // the product's rounding error r (exact by FMA) would come back multiplied by |g| through
+        // the exponential: exp(-(gi + r)) = exp(-gi) (1 - r) to first order. A scale that is a
+        // power of two leaves none. (e may be infinite: the factor keeps it so.)
+        const float e = expf(-gi);
+        const float s = 1.0f / (1.0f + (kMx ? e : e * (1.0f - fmaf(g[i], sg, -gi))));
+        const float silu = gi * s, h = silu * ui, wd = w * d[i];
+        dot = fmaf(d[i], h, dot);
+        dg[i] = wd * ui * fmaf(silu, 1.0f - s, s);
+        du[i] = wd * silu;
+        hv[i] = w * h;
+      }
+      elem_store8<Elem>(dgu + row * ld_dgu + c0, vec_dgu, n, dg);
+      elem_store8<Elem>(dgu + row * ld_dgu + inter + c0, vec_dgu, n, du);
+      if (hw != nullptr) elem_store8<Elem>(hw + row * ld_hw + c0, vec_hw, n, hv);
+    }
+    if (dweights != nullptr) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      if constexpr (kWarps == 1) {
+        if (live && lane == 0) dweights[row] = dot;
+      } else {
+        // two buffers in turn: a warp may begin the next row's sum while another still reads this one
+        if (lane == 0) part[phase][threadIdx.x >> 5] = dot;
+        __syncthreads();
+        if (live && tid == 0) {
+          float sum = 0.0f;
+#pragma unroll
+          for (int i = 0; i < kWarps; ++i) sum += part[phase][sub * kWarps + i];
+          dweights[row] = sum;
+        }
+      }
+    }
+  }
+}
+
+static int grid_for(int64_t blocks) {
+  const int64_t cap = (int64_t)sm_count() * 32;
+  if (blocks > cap) blocks = cap;
+  return (int)(blocks < 1 ? 1 : blocks);
+}
+
+}  // namespace act_train
+
+cudaError_t launch_silu_save(const SiluSaveArgs& a, cudaStream_t st) {
+  using namespace act_train;
+  const int grid = grid_for(cdiv(a.rows * cdiv(a.inter, kGroup), 16));
+  return with_elem(a.gu_dtype, [&](auto in) {
+    return with_elem(a.h_dtype, [&](auto out) {
+      using In = decltype(in);
+      using Out = decltype(out);
+      // the up half begins at column inter: it has to keep the vectors' alignment
+      const bool vg = elem_vec_ok(a.gu, a.ld_gu, sizeof(typename In::T)) && a.inter % 8 == 0;
+      const bool vh = elem_vec_ok(a.h, a.ld_h, sizeof(typename Out::T));
+      const bool vq = (uintptr_t)a.q % 8 == 0 && a.inter % 8 == 0;
+      auto k = a.mx ? silu_save_kernel<In, Out, true> : silu_save_kernel<In, Out, false>;
+      return launch_kernel(k, dim3(grid), dim3(256), 0, st, false, static_cast<const typename In::T*>(a.gu), a.rows,
+                           a.inter, a.ld_gu, a.rows_dev, static_cast<typename Out::T*>(a.h), a.ld_h, a.q, a.scales, vg,
+                           vh, vq);
+    });
+  });
+}
+
+cudaError_t launch_silu_backward(const SiluBackwardArgs& a, cudaStream_t st) {
+  using namespace act_train;
+  return with_elem(a.dtype, [&](auto elem) {
+    using E = decltype(elem);
+    using T = typename E::T;
+    const bool vq = (uintptr_t)a.q % 8 == 0 && a.inter % 8 == 0;
+    const bool vd = elem_vec_ok(a.dh, a.ld_dh, sizeof(T));
+    const bool vgu = elem_vec_ok(a.dgu, a.ld_dgu, sizeof(T)) && a.inter % 8 == 0;
+    const bool vhw = a.hw == nullptr || elem_vec_ok(a.hw, a.ld_hw, sizeof(T));
+    auto go = [&](auto kernel, int tpr) {
+      return launch_kernel(kernel, dim3(grid_for(cdiv(a.rows, 256 / tpr))), dim3(256), 0, st, false, a.q, a.scales,
+                           a.rows, a.inter, a.rows_dev, static_cast<const T*>(a.dh), a.ld_dh, a.row_weights,
+                           static_cast<T*>(a.dgu), a.ld_dgu, static_cast<T*>(a.hw), a.ld_hw, a.dweights, vq, vd, vgu,
+                           vhw);
+    };
+    // as many threads per row as it has runs of 8 columns, so that a thread makes few passes
+    if (a.inter <= 256) return a.mx ? go(silu_backward_kernel<E, true, 32>, 32) : go(silu_backward_kernel<E, false, 32>, 32);
+    if (a.inter <= 1024)
+      return a.mx ? go(silu_backward_kernel<E, true, 128>, 128) : go(silu_backward_kernel<E, false, 128>, 128);
+    return a.mx ? go(silu_backward_kernel<E, true, 256>, 256) : go(silu_backward_kernel<E, false, 256>, 256);
+  });
+}
+
+}  // namespace ftmoe

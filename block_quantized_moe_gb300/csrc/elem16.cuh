@@ -1,0 +1,87 @@
+// Element access by ftmoe_out_dtype for the training kernels: eight consecutive elements of a
+// bf16, fp16 or fp32 row as fp32 values, in one or two vector accesses where the caller has
+// checked the alignment, else one by one up to a given count.
+#pragma once
+
+#include "common.cuh"
+
+namespace ftmoe {
+
+struct ElemBf16 {
+  using T = uint16_t;
+  static __device__ __forceinline__ float get(uint16_t b) { return bf16_bits_to_f(b); }
+  static __device__ __forceinline__ uint16_t put(float v) { return OutBf16::cvt(v); }
+};
+struct ElemF16 {
+  using T = uint16_t;
+  static __device__ __forceinline__ float get(uint16_t b) { return __half2float(__ushort_as_half(b)); }
+  static __device__ __forceinline__ uint16_t put(float v) { return OutF16::cvt(v); }
+};
+struct ElemF32 {
+  using T = float;
+  static __device__ __forceinline__ float get(float b) { return b; }
+  static __device__ __forceinline__ float put(float v) { return v; }
+};
+
+// n (at most 8) elements at p as fp32, the rest zero
+template <typename Elem>
+__device__ __forceinline__ void elem_load8(const typename Elem::T* p, bool vec, int n, float (&v)[8]) {
+  if (vec && n >= 8) {
+    if constexpr (sizeof(typename Elem::T) == 2) {
+      const uint4 r = *reinterpret_cast<const uint4*>(p);
+      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = Elem::get((uint16_t)(w[i] & 0xffffu));
+        v[2 * i + 1] = Elem::get((uint16_t)(w[i] >> 16));
+      }
+    } else {
+      const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? Elem::get(p[i]) : 0.0f;
+  }
+}
+
+// the first n (at most 8) of v, each rounded once
+template <typename Elem>
+__device__ __forceinline__ void elem_store8(typename Elem::T* p, bool vec, int n, const float (&v)[8]) {
+  if (vec && n >= 8) {
+    if constexpr (sizeof(typename Elem::T) == 2) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = (uint32_t)Elem::put(v[2 * i]) | ((uint32_t)Elem::put(v[2 * i + 1]) << 16);
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = Elem::put(v[i]);
+  }
+}
+
+// whether rows of `elem_bytes`-byte elements at base with stride ld may take 8-element vectors
+// (16-byte accesses)
+inline bool elem_vec_ok(const void* base, int64_t ld, int elem_bytes) {
+  return (uintptr_t)base % 16 == 0 && (ld * elem_bytes) % 16 == 0;
+}
+
+// dtype -> element type, for host dispatch: f(ElemBf16{}) and so on
+template <typename F>
+inline cudaError_t with_elem(int32_t dtype, F f) {
+  if (dtype == FTMOE_OUT_BF16) return f(ElemBf16{});
+  if (dtype == FTMOE_OUT_FP16) return f(ElemF16{});
+  return f(ElemF32{});
+}
+
+// 2^(b - 127) of an E8M0 scale byte (b = 0 gives the subnormal 2^-127; 255 is the format's NaN)
+__device__ __forceinline__ float e8m0_to_f(uint8_t b) {
+  return __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7fc00000u : (uint32_t)b << 23);
+}
+
+}  // namespace ftmoe

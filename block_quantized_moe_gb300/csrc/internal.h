@@ -264,6 +264,59 @@ cudaError_t launch_combine(const float* y, int64_t ld_y, const int32_t* route2ds
                            int64_t hidden, int32_t out_dtype, void* out, int64_t ld_out, cudaStream_t s);
 uint32_t read_err_act();
 
+// act_train.cu: SiLU-and-mul that keeps gate/up in 8 bits, and its backward pass
+struct SiluSaveArgs {
+  const void* gu;
+  int32_t gu_dtype;        // ftmoe_out_dtype
+  int64_t rows, inter, ld_gu;
+  const int32_t* rows_dev;
+  void* h;
+  int64_t ld_h;
+  int32_t h_dtype;
+  bool mx;                 // MXFP8, else FP8
+  uint8_t* q;              // [rows][2][inter]
+  void* scales;
+};
+cudaError_t launch_silu_save(const SiluSaveArgs& a, cudaStream_t s);
+struct SiluBackwardArgs {
+  const uint8_t* q;
+  const void* scales;
+  bool mx;
+  int64_t rows, inter;
+  const int32_t* rows_dev;
+  const void* dh;
+  int64_t ld_dh;
+  int32_t dtype;           // of dh, dgu, hw
+  const float* row_weights;
+  void* dgu;
+  int64_t ld_dgu;
+  void* hw;
+  int64_t ld_hw;
+  float* dweights;
+};
+cudaError_t launch_silu_backward(const SiluBackwardArgs& a, cudaStream_t s);
+
+// matmul16.cu: products grouped by expert in 16 bits (three directions)
+struct Matmul16Args {
+  const void* a;           // rows of the product's input, or dy of the weight gradient
+  int64_t ld_a;
+  int64_t rows;
+  int32_t dtype;           // of a, the weights and x: bf16 or fp16
+  const int32_t* offsets;
+  ftmoe_matrix_bank w;     // weights, or the weight gradient
+  int32_t input_grad;      // 0: out = a w^T, 1: out = a w
+  void* out;
+  int64_t ld_out;
+  int32_t out_dtype;
+  int32_t wgrad;           // 1: w += or = dy^T x per expert
+  const void* x;           // 16-bit rows, or MXFP8 codes where x_scales is set
+  int64_t ld_x;
+  const uint8_t* x_scales;
+  int32_t accumulate;
+};
+cudaError_t launch_matmul16(const Matmul16Args& a, cudaStream_t s);  // picks the kernel
+cudaError_t launch_matmul16_general(const Matmul16Args& a, cudaStream_t s);
+
 // selftest.cu
 uint32_t read_err_selftest();
 

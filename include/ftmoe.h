@@ -419,6 +419,89 @@ ftmoe_status ftmoe_expert_slots(int32_t* expert_ids, int64_t routes, int32_t* sl
                                 int32_t num_slots, int32_t* expert_slot, int32_t num_experts, int64_t step,
                                 int32_t max_fetch, int32_t* fetch_plan, int32_t* n_fetch, void* stream);
 
+/* ------------------------------------------------------------------------------------
+ * Training and 16-bit products (no counterpart in the pages; services of this library for
+ * experts kept in bf16 or fp16). Rows are grouped by expert as in FTMOE_ROUTES_GROUPED: the
+ * rows of expert e are [offsets[e], offsets[e+1]) (device int32 [E+1], from
+ * ftmoe_segment_routes); bounds are clamped to [0, rows], and an expert whose bounds do not
+ * increase has no rows. One training step of the expert FFN: examples/train_experts.py.
+ * ------------------------------------------------------------------------------------ */
+
+/* E matrices of shape [n, k]: element (e, i, j) at w[e * expert_stride + i * ld + j]. dtype is
+ * an ftmoe_out_dtype; the entry points say which they take. ld >= k, expert_stride >=
+ * (n - 1) * ld + k, both in elements. */
+typedef struct ftmoe_matrix_bank {
+  int32_t dtype;
+  int32_t num_experts;
+  int64_t n;
+  int64_t k;
+  int64_t ld;
+  int64_t expert_stride;
+  void* w;
+} ftmoe_matrix_bank;
+
+/* Product grouped by expert, or the gradient of its input:
+ *   input_grad = 0: out[r, i] = sum_j a[r, j] * w[e, i, j]   a [rows][k], out [rows][n]
+ *   input_grad = 1: out[r, j] = sum_i a[r, i] * w[e, i, j]   a [rows][n], out [rows][k]
+ * for the rows r of every expert e. a and w are bf16 or fp16, both w->dtype; out is
+ * out_dtype (that type or any other), rounded to nearest even once from an fp32 sum. Row
+ * strides ld_a, ld_out in elements. Rows at or beyond offsets[E] are neither read nor
+ * written. Any sizes and strides are taken; where every base and row stride of a and w is a
+ * multiple of 16 bytes the tensor cores or, for few rows, the streaming kernel run, else a
+ * slower general kernel. w is only read. rows == 0 launches nothing. */
+ftmoe_status ftmoe_grouped_matmul(const void* a, int64_t rows, int64_t ld_a, const int32_t* offsets,
+                                  const ftmoe_matrix_bank* w, int32_t input_grad, void* out, int64_t ld_out,
+                                  int32_t out_dtype, void* stream);
+
+/* Gradient of the weights:
+ *   dw[e, i, j] = (accumulate ? dw[e, i, j] : 0) + sum over the rows r of expert e of dy[r, i] * x[r, j]
+ * dy [rows][n] and x [rows][k] are bf16 or fp16, both `dtype`; dw->dtype is any
+ * ftmoe_out_dtype. The sum is fp32 and rounded once; an old value is added in fp32 before the
+ * rounding. An expert without rows gets zeros (accumulate: keeps its values). rows == 0 is
+ * no error: every expert is then one without rows. dw must not overlap dy or x. */
+ftmoe_status ftmoe_grouped_matmul_wgrad(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, int64_t rows,
+                                        int32_t dtype, const int32_t* offsets, const ftmoe_matrix_bank* dw,
+                                        int32_t accumulate, void* stream);
+
+/* The same gradient with x kept in 8 bits: x->format is FTMOE_FMT_MXFP8 (rows of k codes and
+ * k/32 scale bytes, as ftmoe_quantize_act and ftmoe_gather_rows_scales write them). Codes are
+ * decoded in front of the multiply; a code times a power of two is exact in bf16 (and in fp16
+ * down to 2^-24), so dw is the gradient for the saved values with no further rounding. FP8
+ * rows (an fp32 scale per group) would have to be rounded to 16 bits first and are refused,
+ * like NVFP4, as FTMOE_UNSUPPORTED. x->rows is the row count of dy too. */
+ftmoe_status ftmoe_grouped_matmul_wgrad_saved(const void* dy, int64_t ld_dy, int32_t dtype, const ftmoe_act* x,
+                                              const int32_t* offsets, const ftmoe_matrix_bank* dw,
+                                              int32_t accumulate, void* stream);
+
+/* SiLU-and-mul that keeps its input in 8 bits for the backward pass: for each row
+ *   h[i] = silu(g[i]) * u[i],  g = gu[row, 0:inter], u = gu[row, inter:2*inter]
+ * (fp32, rounded once to h_dtype) from the values of gu themselves, and both halves quantized
+ * as ftmoe_quantize_act quantizes a row of `inter` elements: q uint8 [rows][2][inter] and, for
+ * FTMOE_FMT_FP8, scales float [rows][2][ceil(inter/128)], for FTMOE_FMT_MXFP8 (inter % 32 ==
+ * 0) scales E8M0 [rows][2][inter/32]; NVFP4 is FTMOE_UNSUPPORTED. gu_dtype and h_dtype are
+ * ftmoe_out_dtype values. rows_dev: optional device int32 count of valid rows (<= rows, e.g.
+ * offsets + E); rows beyond it are neither read nor written. */
+ftmoe_status ftmoe_silu_mul_save(const void* gu, int32_t gu_dtype, int64_t rows, int64_t inter, int64_t ld_gu,
+                                 const int32_t* rows_dev, void* h, int64_t ld_h, int32_t h_dtype, int32_t format,
+                                 uint8_t* q, void* scales, void* stream);
+
+/* Backward pass of SiLU-and-mul and of the routing weight, from the rows that
+ * ftmoe_silu_mul_save kept. With g, u the kept values, s = 1 / (1 + exp(-g)), and w =
+ * row_weights[row] (1 where row_weights is NULL):
+ *   dgu[row, i]         = w * dh[row, i] * u * s * (1 + g * (1 - s))
+ *   dgu[row, inter + i] = w * dh[row, i] * g * s
+ *   hw[row, i]          = w * g * s * u                       (hw may be NULL)
+ *   dweights[row]       = sum_i dh[row, i] * g * s * u        (dweights may be NULL)
+ * dh is the gradient of the unweighted h (the input gradient of the down product for the
+ * output's own gradient): the FFN weights a route's output, so the weight moves to dgu and
+ * to hw, the x of the down product's weight gradient, and the down product's output is not
+ * needed. dh, dgu and hw are `dtype`; row_weights and dweights are float [rows]. The sum of
+ * dweights has a fixed order. rows_dev as above. */
+ftmoe_status ftmoe_silu_mul_backward(const uint8_t* q, const void* scales, int32_t format, int64_t rows,
+                                     int64_t inter, const int32_t* rows_dev, const void* dh, int64_t ld_dh,
+                                     int32_t dtype, const float* row_weights, void* dgu, int64_t ld_dgu, void* hw,
+                                     int64_t ld_hw, float* dweights, void* stream);
+
 /* Self-test of the bounded pipeline waits (failure detection; the pages have no counterpart).
  * Every wait of the TMA/tensor-core pipelines gives up after a time limit (4 s), raises
  * FTMOE_ERR_WAIT_TIMEOUT in the device error word and lets its kernel return normally, so a
