@@ -1,7 +1,9 @@
 // SiLU-and-mul that keeps its gate/up rows in 8 bits, and its backward pass from them.
 //
 // Forward, per row: h = silu(g) * u with silu(g) = g * s, s = 1 / (1 + exp(-g)); g and u are
-// kept as e4m3 codes with an fp32 scale per 128 (amax / 448) or a power of two per 32.
+// kept as e4m3 codes with an fp32 scale per 128 (amax times fp32's 1 / 448: the multiplication
+// may differ from the division in the last bit, which a scale that travels with its codes does
+// not notice) or a power of two per 32.
 // Backward, with the kept g and u, the gradient dh of the unweighted h and the routing weight w:
 //   d h / d u = g s,   d h / d g = u s (1 + g (1 - s))
 //   dgu = w dh (d h / d g | d h / d u),   hw = w h,   dweight = sum_i dh_i h_i
@@ -43,7 +45,7 @@ __device__ __forceinline__ uint2 quantize8(const float (&v)[8], float& sc, uint8
 #pragma unroll
     for (int i = 0; i < 8; ++i) q[i] = v[i] * f;
   } else {
-    sc = div_rn(m, kE4M3Max);
+    sc = m * (1.0f / kE4M3Max);
     if (m > 0.0f) {
       const SharedDivisor d(sc);  // v / sc as IEEE division rounds it
 #pragma unroll

@@ -162,6 +162,10 @@ cudaError_t launch_matmul16_general(const Matmul16Args& a, cudaStream_t st) {
   return mm16::run(p, a.dtype, a.out_dtype, false, (cdiv(a.rows, 64) + w.num_experts) * cdiv(p.n, 64), st);
 }
 
-cudaError_t launch_matmul16(const Matmul16Args& a, cudaStream_t st) { return launch_matmul16_general(a, st); }
+cudaError_t launch_matmul16(const Matmul16Args& a, cudaStream_t st) {
+  int unsupported = 0;
+  const cudaError_t e = launch_tc_matmul16(a, st, &unsupported);
+  return unsupported ? launch_matmul16_general(a, st) : e;
+}
 
 }  // namespace ftmoe

@@ -475,10 +475,13 @@ ftmoe_status ftmoe_grouped_matmul_wgrad_saved(const void* dy, int64_t ld_dy, int
 
 /* SiLU-and-mul that keeps its input in 8 bits for the backward pass: for each row
  *   h[i] = silu(g[i]) * u[i],  g = gu[row, 0:inter], u = gu[row, inter:2*inter]
- * (fp32, rounded once to h_dtype) from the values of gu themselves, and both halves quantized
- * as ftmoe_quantize_act quantizes a row of `inter` elements: q uint8 [rows][2][inter] and, for
- * FTMOE_FMT_FP8, scales float [rows][2][ceil(inter/128)], for FTMOE_FMT_MXFP8 (inter % 32 ==
- * 0) scales E8M0 [rows][2][inter/32]; NVFP4 is FTMOE_UNSUPPORTED. gu_dtype and h_dtype are
+ * (fp32, rounded once to h_dtype) from the values of gu themselves, and both halves kept as
+ * e4m3 codes, q uint8 [rows][2][inter]. FTMOE_FMT_FP8: per 1x128 group s = amax * (1/448) (an
+ * fp32 product; ftmoe_quantize_act divides, which may differ in the last bit), code =
+ * e4m3_rne_satfinite(x / s), s in scales float [rows][2][ceil(inter/128)]; amax = 0 gives s = 0
+ * and zero codes. FTMOE_FMT_MXFP8 (inter % 32 == 0): codes and bytes as ftmoe_quantize_act
+ * writes them for a row of `inter` elements, scales E8M0 [rows][2][inter/32]. NVFP4 is
+ * FTMOE_UNSUPPORTED. gu_dtype and h_dtype are
  * ftmoe_out_dtype values. rows_dev: optional device int32 count of valid rows (<= rows, e.g.
  * offsets + E); rows beyond it are neither read nor written. */
 ftmoe_status ftmoe_silu_mul_save(const void* gu, int32_t gu_dtype, int64_t rows, int64_t inter, int64_t ld_gu,

@@ -362,8 +362,9 @@ def backward_check(g, u, dh, w, dgu, hw, dwt, inter):
 
 
 @pytest.mark.parametrize("fmt", [ft.FMT_FP8, ft.FMT_MXFP8])
-def test_silu_saved_codes_are_the_quantizers(fmt):
-    """Codes and scales bit for bit those of ftmoe_quantize_act on each half."""
+def test_silu_saved_codes_bit_for_bit(fmt):
+    """MXFP8: codes and scales those of ftmoe_quantize_act on each half. FP8: the scale is the fp32
+    product amax * (1/448), the codes those of the IEEE quotients by it."""
     rows, inter = 33, 416
     gu = normal((rows, 2 * inter), 3.0, torch.bfloat16, 33)
     gu[3] = 0.0
@@ -372,7 +373,14 @@ def test_silu_saved_codes_are_the_quantizers(fmt):
     groups = s.shape[1] // 2
     for half in (0, 1):
         part = gu[:, half * inter:(half + 1) * inter].contiguous()
-        want_q, want_s, _ = ft.quantize_act(part, fmt)
+        if fmt == ft.FMT_MXFP8:
+            want_q, want_s, _ = ft.quantize_act(part, fmt)
+        else:
+            x = torch.nn.functional.pad(part.float(), (0, groups * 128 - inter)).view(rows, groups, 128).cpu().numpy()
+            want = np.abs(x).max(2, keepdims=True) * (np.float32(1) / np.float32(448))
+            codes = torch.from_numpy(np.where(want > 0, x / np.where(want > 0, want, np.float32(1)), np.float32(0)))
+            want_q = codes.to(torch.float8_e4m3fn).view(torch.uint8).view(rows, -1)[:, :inter].to(DEV)
+            want_s = torch.from_numpy(want[:, :, 0]).to(DEV)
         assert torch.equal(q[:, half * inter:(half + 1) * inter], want_q)
         assert torch.equal(s[:, half * groups:(half + 1) * groups], want_s)
 
