@@ -28,13 +28,15 @@
 // segment, in A and in B (what is there may be NaN), up to the next multiple of 16, and hands
 // the stage to the MMA issuer, which runs only the 16-row steps that hold rows.
 // From saved rows (MXFP8), A arrives as codes; eight warps decode them into the operand tile,
-// one 32-wide group with its power-of-two scale per thread, exactly.
+// two 32-wide groups with their power-of-two scales per thread, exactly.
 //
-// Roles: warp 0 TMA, warp 1 MMA issue and TMEM, warp 2 segment tails (weight grad), warps 4-11
-// epilogue, warps 12-19 decode (saved rows). Every mbarrier wait is bounded: on timeout the
+// Roles: warp 0 TMA, warp 1 MMA issue and TMEM, warp 2 segment tails (weight grad) or codes
+// (saved rows), warp 3 relay (saved rows), warps 4-11 epilogue, warps 12-19 decode (saved rows). Every mbarrier wait is bounded: on timeout the
 // kernel raises FTMOE_ERR_WAIT_TIMEOUT, stops its roles, waits for its own loads and MMAs,
 // frees its TMEM and returns.
 #include <cuda.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "elem16.cuh"
@@ -51,12 +53,18 @@ constexpr int kBK = 64;                   // elements of l per stage: one 128-by
 constexpr int kM = 256, kN = 256;         // of the pair
 constexpr int kTile = 128 * kBK * 2;      // 16 KiB: this CTA's half of A, and of B at most
 constexpr int kRaw = 128 * kBK;           // saved rows: 8 KiB of codes
+constexpr int kRawSlots = 6;
+constexpr int kOutBuf = 8192;             // an output box: 32 columns of c (16 of fp32) by 128 of m
 constexpr int kEpiWarps = 8, kDecWarps = 8;
 constexpr int kMaxExperts = 4096;
 
 __host__ __device__ constexpr bool is_wgrad(int mode) { return mode >= kWeightGrad; }
-__host__ __device__ constexpr int stage_bytes(int mode) { return 2 * kTile + (mode == kWeightGradSaved ? kRaw : 0); }
-__host__ __device__ constexpr int stages(int mode) { return mode == kWeightGradSaved ? 5 : 6; }
+// 32 KiB a stage (a fill takes about as long as three stages' MMAs; 4, 5 and 6 stages measured
+// the same), two output boxes for each half of the epilogue, and the ring of codes.
+__host__ __device__ constexpr int stages(int mode) { return mode == kWeightGradSaved ? 4 : 5; }
+__host__ __device__ constexpr int smem_bytes(int mode) {
+  return stages(mode) * 2 * kTile + 4 * kOutBuf + (mode == kWeightGradSaved ? kRawSlots * kRaw : 0);
+}
 __host__ __device__ constexpr int threads(int mode) { return 32 * (4 + kEpiWarps + (mode == kWeightGradSaved ? kDecWarps : 0)); }
 
 struct Params {
@@ -69,6 +77,7 @@ struct Params {
   int l_dim;                 // extent of l (product, input grad)
   int c_dim;                 // weight grad: extent of c
   int E, out_dtype, bf16, accumulate;
+  int tma_out;               // whether map_o describes the output
 };
 
 // One MMA of the pair, issued by one lane of a converged warp: with the whole warp in the issue
@@ -175,10 +184,31 @@ struct Unit {
   int l0, len;     // weight grad: first row of the segment and its length; else 0 and l_dim
 };
 
-// Two 16-bit roundings of the values of one lane pair: see store_columns.
+// two values rounded to 16 bits, lo in the low half
 template <typename Elem>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  return (uint32_t)Elem::put(lo) | ((uint32_t)Elem::put(hi) << 16);
+  uint32_t r;
+  if constexpr (sizeof(typename Elem::T) == 4)
+    r = 0;
+  else if constexpr (std::is_same<Elem, ElemBf16>::value)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+// fp32 boxes added to memory, each element once (an fp32 sum rounded to nearest)
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(x), "r"(y), "r"(z)
+               : "memory");
 }
 
 // 32 columns d[0..31] of this lane's m into out[(c0 + j) * ld + m], j < cols, m < m_dim. 16-bit
@@ -220,13 +250,18 @@ template <int MODE>
 __global__ void __launch_bounds__(threads(MODE), 1)
     tc_matmul16_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b0,
                        const __grid_constant__ CUtensorMap map_b1, const __grid_constant__ CUtensorMap map_b2,
-                       const __grid_constant__ CUtensorMap map_b3, Params p) {
+                       const __grid_constant__ CUtensorMap map_b3, const __grid_constant__ CUtensorMap map_o, Params p) {
   constexpr bool kWG = is_wgrad(MODE), kSaved = MODE == kWeightGradSaved;
-  constexpr int S = stages(MODE), kStage = stage_bytes(MODE);
+  constexpr int S = stages(MODE), kStage = 2 * kTile;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  int* cum = reinterpret_cast<int*>(tiles + (size_t)S * kStage);  // [E + 1] units before expert e (not weight grad)
+  uint8_t* outbuf = tiles + (size_t)S * kStage;        // [2 halves of the epilogue][2] output boxes
+  uint8_t* raws = outbuf + 4 * kOutBuf;                // saved rows: [kRawSlots] codes
+  int* cum = reinterpret_cast<int*>(raws);             // else: [E + 1] units before expert e (not weight grad)
   __shared__ __align__(8) uint64_t full[S], empty[S], lfull[S], tfull[2], tempty[2];
+  // saved rows: codes landed / taken; operand tile decoded in this CTA (the second CTA reports it
+  // to the first's full barrier through one thread)
+  __shared__ __align__(8) uint64_t rfull[kRawSlots], rempty[kRawSlots], decoded[S];
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
 
@@ -246,11 +281,16 @@ __global__ void __launch_bounds__(threads(MODE), 1)
   if (threadIdx.x == 0) {
     s_abort = 0;
     for (int i = 0; i < S; ++i) {
-      // saved rows: every decoding warp of both CTAs and the first CTA's producer; weight grad:
-      // two arrivals of the first CTA's producer, or one of each CTA's tail warp; else its one
-      mbar_init(smem_u32(&full[i]), kSaved ? 2 * kDecWarps + 1 : kWG ? 2 : 1);
+      // weight grad: two arrivals of the first CTA's producer, or (a segment's last stage) one
+      // of each CTA's tail warp; saved rows: both CTAs' relays and the first CTA's producer
+      mbar_init(smem_u32(&full[i]), kSaved ? 3 : kWG ? 2 : 1);
       mbar_init(smem_u32(&empty[i]), 1);
       mbar_init(smem_u32(&lfull[i]), 1);
+      mbar_init(smem_u32(&decoded[i]), kDecWarps / 2);
+    }
+    for (int i = 0; i < kRawSlots; ++i) {
+      mbar_init(smem_u32(&rfull[i]), 1);
+      mbar_init(smem_u32(&rempty[i]), kDecWarps / 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&tfull[i]), 1);
@@ -327,7 +367,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
   if (warp == 0) {
     // ------------------------------- TMA producer -------------------------------
     if (lane == 0) {
-      uint32_t it = 0, tails = 0, tail_ph = 0;  // bit st: slot st's last use was a tail; its phase
+      uint32_t it = 0, tails = 0, tail_ph = 0;  // bit st: slot st's last use was a tail; uses of lfull[st], mod 2
       for (int u = u_begin; u < u_end && !s_abort; u += u_step) {
         Unit t;
         decode(u, t);
@@ -338,32 +378,25 @@ __global__ void __launch_bounds__(threads(MODE), 1)
         const int hb = half <= 16 ? 16 : half <= 32 ? 32 : half <= 64 ? 64 : 128;
         const CUtensorMap* mb = half <= 16 ? &map_b3 : half <= 32 ? &map_b2 : half <= 64 ? &map_b1 : &map_b0;
         const uint32_t bytes_b = kWG ? (half > 64 ? kTile : kTile / 2) : (uint32_t)hb * 128;
+        const uint32_t bytes = (kSaved ? 0 : kTile) + bytes_b;
         for (int s = 0; s < steps; ++s, ++it) {
           const int st = it % S;
           if (!mbar_wait(smem_u32(&empty[st]), ((it / S) & 1) ^ 1, &s_abort)) break;
           const uint32_t ta = smem_u32(tiles + (size_t)st * kStage), tb = ta + kTile;
-          const uint32_t fb = mapa_shared(smem_u32(&full[st]), 0);
+          const bool tail = kWG && t.len - s * kBK < kBK;
+          // a tail lands on this CTA's own barrier, everything else on the first CTA's
+          const uint32_t bar = tail ? smem_u32(&lfull[st]) : mapa_shared(smem_u32(&full[st]), 0);
+          tails = tail ? tails | (1u << st) : tails & ~(1u << st);
+          if (tail) {
+            mbar_expect_tx(bar, bytes);
+            tail_ph ^= 1u << st;
+            if (kSaved && crank == 0) mbar_arrive(smem_u32(&full[st]));
+          } else if (crank == 0) {
+            mbar_expect_tx(smem_u32(&full[st]), 2 * bytes);
+            if (kWG && !kSaved) mbar_arrive(smem_u32(&full[st]));
+          }
           if constexpr (kWG) {
-            const bool tail = t.len - s * kBK < kBK;
             const int l = t.l0 + s * kBK;
-            const uint32_t local = smem_u32(&lfull[st]);
-            tails = tail ? tails | (1u << st) : tails & ~(1u << st);
-            if constexpr (kSaved) {
-              mbar_expect_tx(local, kRaw + (tail ? bytes_b : 0));
-              tail_ph ^= 1u << st;
-              tma_pair_2d(tb + kTile, &map_a, local, ma, l);  // 128 codes of 64 rows
-              if (crank == 0) {
-                if (tail) mbar_arrive(smem_u32(&full[st]));
-                else mbar_expect_tx(smem_u32(&full[st]), 2 * bytes_b);
-              }
-            } else if (tail) {
-              mbar_expect_tx(local, kTile + bytes_b);
-              tail_ph ^= 1u << st;
-            } else if (crank == 0) {
-              mbar_expect_tx(smem_u32(&full[st]), 2 * (kTile + bytes_b));
-              mbar_arrive(smem_u32(&full[st]));
-            }
-            const uint32_t bar = tail ? local : fb;
             if constexpr (!kSaved) {
               tma_pair_2d(ta, &map_a, bar, ma, l);
               tma_pair_2d(ta + kTile / 2, &map_a, bar, ma + 64, l);
@@ -371,28 +404,30 @@ __global__ void __launch_bounds__(threads(MODE), 1)
             tma_pair_2d(tb, &map_b0, bar, cb, l);
             if (half > 64) tma_pair_2d(tb + kTile / 2, &map_b0, bar, cb + 64, l);
           } else {
-            if (crank == 0) mbar_expect_tx(smem_u32(&full[st]), 2 * (kTile + bytes_b));
             if constexpr (MODE == kProduct) {
-              tma_pair_3d(ta, &map_a, fb, s * kBK, ma, t.e);
+              tma_pair_3d(ta, &map_a, bar, s * kBK, ma, t.e);
             } else {
-              tma_pair_3d(ta, &map_a, fb, ma, s * kBK, t.e);
-              tma_pair_3d(ta + kTile / 2, &map_a, fb, ma + 64, s * kBK, t.e);
+              tma_pair_3d(ta, &map_a, bar, ma, s * kBK, t.e);
+              tma_pair_3d(ta + kTile / 2, &map_a, bar, ma + 64, s * kBK, t.e);
             }
-            tma_pair_2d(tb, mb, fb, s * kBK, cb);
+            tma_pair_2d(tb, mb, bar, s * kBK, cb);
           }
         }
       }
-      // Loads still in flight after an abort (bounded): tails and codes land on this CTA's
-      // barriers, the rest on the first CTA's, which the second outlives no longer than the
-      // closing cluster barrier.
+      // Loads still in flight after an abort (bounded): tails land on this CTA's barriers, the
+      // rest on the first CTA's, which the second outlives no longer than the closing cluster
+      // barrier.
       for (int st = 0; st < S && (uint32_t)st < it; ++st) {
         const uint32_t last = it - 1 - ((it - 1 - st) % S);
-        const bool on_local = kSaved || (tails >> st & 1);
+        const bool on_local = tails >> st & 1;
         if (!on_local && crank != 0) continue;
         const uint32_t bar = on_local ? smem_u32(&lfull[st]) : smem_u32(&full[st]);
         const uint32_t ph = on_local ? (tail_ph >> st & 1) ^ 1 : (last / S) & 1;
+        // (saved rows: a full barrier whose decoders have left never completes; a millisecond is
+        // ample for the copies themselves)
+        const unsigned long long limit = kSaved && s_abort ? 1000000ull : kTimeoutNs;
         const unsigned long long t0 = globaltimer();
-        while (!mbar_try_wait(bar, ph) && globaltimer() - t0 < kTimeoutNs) {
+        while (!mbar_try_wait(bar, ph) && globaltimer() - t0 < limit) {
         }
       }
     }
@@ -475,11 +510,57 @@ __global__ void __launch_bounds__(threads(MODE), 1)
       }
       it += steps;
     }
+  } else if (kSaved && warp == 2) {
+    // ------------------------ saved rows: codes ------------------------
+    if (lane == 0) {
+      uint32_t it = 0;
+      for (int u = u_begin; u < u_end && !s_abort; u += u_step) {
+        Unit t;
+        decode(u, t);
+        const int steps = (t.len + kBK - 1) / kBK, ma = t.m0 + (int)crank * 128;
+        for (int s = 0; s < steps; ++s, ++it) {
+          const int r = it % kRawSlots;
+          if (!mbar_wait(smem_u32(&rempty[r]), ((it / kRawSlots) & 1) ^ 1, &s_abort)) break;
+          mbar_expect_tx(smem_u32(&rfull[r]), kRaw);
+          tma_pair_2d(smem_u32(raws + r * kRaw), &map_a, smem_u32(&rfull[r]), ma, t.l0 + s * kBK);
+        }
+      }
+      for (int r = 0; r < kRawSlots && (uint32_t)r < it; ++r) {  // in flight after an abort
+        const uint32_t last = it - 1 - ((it - 1 - r) % kRawSlots);
+        const unsigned long long t0 = globaltimer();
+        while (!mbar_try_wait(smem_u32(&rfull[r]), (last / kRawSlots) & 1) && globaltimer() - t0 < kTimeoutNs) {
+        }
+      }
+    }
+  } else if (kSaved && warp == 3) {
+    // ------------------------ saved rows: relay ------------------------
+    // One thread hands this CTA's decoded tiles to the first CTA's full barrier: the release at
+    // cluster scope waits for memory, and eight decoding warps doing it each would wait as often.
+    if (lane == 0) {
+      uint32_t it = 0;
+      for (int u = u_begin; u < u_end && !s_abort; u += u_step) {
+        Unit t;
+        decode(u, t);
+        const int steps = (t.len + kBK - 1) / kBK;
+        for (int s = 0; s < steps; ++s, ++it) {
+          const int st = it % S;
+          if (!mbar_wait(smem_u32(&decoded[st]), (it / S) & 1, &s_abort)) break;
+          arrive_release_cluster(mapa_shared(smem_u32(&full[st]), 0));
+        }
+      }
+    }
   } else if (warp >= 4 && warp < 4 + kEpiWarps) {
     // --------------------------------- epilogue ---------------------------------
+    // Two groups of four warps take chunks of 32 columns in turn. A chunk goes through shared
+    // memory and leaves as TMA boxes of 128 m by 32 c (16 of fp32), 256 or 512 contiguous bytes
+    // a row. (Stored from registers, 64 bytes a row and warp, the weight gradient of 64 experts
+    // of 128 rows, 2048 x 4096, took 477 us for 1.07 GB.) A chunk that ends inside the tile of
+    // an expert's rows, an unaligned output and a 16-bit accumulation are stored from registers.
     const int ew = warp - 4, quarter = warp & 3, half = ew >> 2;
-    uint32_t acc = 0;
+    const bool leader = quarter == 0 && lane == 0;
+    uint32_t acc = 0, box = 0;
     const bool words = p.ld_out % 2 == 0 && p.out_expert % 2 == 0 && reinterpret_cast<uintptr_t>(p.out) % 4 == 0;
+    const bool tma_out = p.tma_out && (!p.accumulate || p.out_dtype == FTMOE_OUT_FP32);
     for (int u = u_begin; u < u_end; u += u_step) {
       Unit t;
       decode(u, t);
@@ -488,14 +569,15 @@ __global__ void __launch_bounds__(threads(MODE), 1)
       const int buf = (int)(acc & 1);
       if (!none) {
         const int got = mbar_wait(smem_u32(&tfull[buf]), (acc >> 1) & 1, &s_abort) ? 1 : 0;
-        if (__all_sync(0xffffffffu, got) == 0) break;
+        // the group's warps share barriers below: they leave together
+        if (named_bar_or(1 + half, 128, got == 0)) break;
         fence_after();
         ++acc;
       }
       const uint32_t taddr = tmem_base + ((uint32_t)(32 * quarter) << 16) + buf * kN;
-      const int m = t.m0 + (int)crank * 128 + 32 * quarter + lane;
+      const int mc = t.m0 + (int)crank * 128, ml = 32 * quarter + lane, m = mc + ml;
       const int64_t first = (int64_t)t.e * p.out_expert + (int64_t)t.c0 * p.ld_out;
-      // chunks of 32 columns, the two groups of four warps in turn
+      bool held = !none;
       for (int c = 32 * half; c < t.cols; c += 64) {
         float d[32];
         if (none) {
@@ -504,86 +586,159 @@ __global__ void __launch_bounds__(threads(MODE), 1)
         } else {
           tmem_ld<32>(taddr + c, d);
           tmem_ld_wait();
+          if (c + 64 >= t.cols) {  // this warp's last read: the accumulator goes back to the MMAs
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[buf]), 0));
+            held = false;
+          }
         }
-        const int64_t o = first + (int64_t)c * p.ld_out;
         const int cols = t.cols - c;
-        if (p.out_dtype == FTMOE_OUT_FP32)
-          store_columns<ElemF32>(static_cast<float*>(p.out) + o, p.ld_out, d, cols, m, p.m_dim, lane, words, p.accumulate);
-        else if (p.out_dtype == FTMOE_OUT_BF16)
-          store_columns<ElemBf16>(static_cast<uint16_t*>(p.out) + o, p.ld_out, d, cols, m, p.m_dim, lane, words, p.accumulate);
-        else
-          store_columns<ElemF16>(static_cast<uint16_t*>(p.out) + o, p.ld_out, d, cols, m, p.m_dim, lane, words, p.accumulate);
+        if (tma_out && (kWG || cols >= 32)) {  // (a weight gradient's edge is clipped by its tensor map)
+          const int per = p.out_dtype == FTMOE_OUT_FP32 ? 16 : 32;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (h == 1 && per == 32) break;
+            uint8_t* ob = outbuf + (2 * half + (box & 1)) * kOutBuf;
+            // the store that used this buffer two boxes ago has read it
+            if (leader) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            named_bar(1 + half, 128);
+            if (p.out_dtype == FTMOE_OUT_FP32) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) reinterpret_cast<float*>(ob)[j * 128 + ml] = d[16 * h + j];
+            } else if (p.out_dtype == FTMOE_OUT_BF16) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 2) {
+                const uint32_t w = pack2<ElemBf16>(d[j], d[j + 1]);
+                reinterpret_cast<uint16_t*>(ob)[j * 128 + ml] = (uint16_t)w;
+                reinterpret_cast<uint16_t*>(ob)[(j + 1) * 128 + ml] = (uint16_t)(w >> 16);
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; j += 2) {
+                const uint32_t w = pack2<ElemF16>(d[j], d[j + 1]);
+                reinterpret_cast<uint16_t*>(ob)[j * 128 + ml] = (uint16_t)w;
+                reinterpret_cast<uint16_t*>(ob)[(j + 1) * 128 + ml] = (uint16_t)(w >> 16);
+              }
+            }
+            fence_async_shared();
+            named_bar(1 + half, 128);
+            if (leader) {
+              const int y = t.c0 + c + 16 * h;
+              if (mc < p.m_dim && (!kWG || y < p.c_dim)) {
+                if (p.accumulate)
+                  tma_add_3d(&map_o, smem_u32(ob), mc, y, kWG ? t.e : 0);
+                else
+                  tma_store_3d(&map_o, smem_u32(ob), mc, y, kWG ? t.e : 0);
+              }
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+            ++box;
+          }
+        } else {
+          const int64_t o = first + (int64_t)c * p.ld_out;
+          if (p.out_dtype == FTMOE_OUT_FP32)
+            store_columns<ElemF32>(static_cast<float*>(p.out) + o, p.ld_out, d, cols, m, p.m_dim, lane, words, p.accumulate);
+          else if (p.out_dtype == FTMOE_OUT_BF16)
+            store_columns<ElemBf16>(static_cast<uint16_t*>(p.out) + o, p.ld_out, d, cols, m, p.m_dim, lane, words, p.accumulate);
+          else
+            store_columns<ElemF16>(static_cast<uint16_t*>(p.out) + o, p.ld_out, d, cols, m, p.m_dim, lane, words, p.accumulate);
+        }
       }
-      if (!none) {
+      if (held) {  // no column of this unit was this warp's
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[buf]), 0));
       }
     }
+    if (leader) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   } else if (kSaved && warp >= 4 + kEpiWarps) {
     // ------------------------ saved rows: decode ------------------------
-    // Thread (warp dw, lane): line r = 8 dw + lane % 8 of the stage's 64, 32-wide group lane / 8
-    // of its 128 codes. Eight lanes with consecutive lines touch eight different 16-byte columns
-    // of the swizzled lines, reading and writing.
-    const int dw = warp - 4 - kEpiWarps, r = 8 * dw + (lane & 7), grp = lane >> 3;
+    // Two groups of four warps take stages in turn, so that one decodes while the other waits
+    // for its stores to be visible. Thread (warp dw, lane): lines r and r + 32 of the stage's
+    // 64, r = 8 dw + lane % 8, and the 32-wide group lane / 8 of their 128 codes. Eight lanes
+    // with consecutive lines touch eight different 16-byte columns of the swizzled lines,
+    // reading and writing.
+    const int dw = (warp - 4 - kEpiWarps) & 3, team = (warp - 4 - kEpiWarps) >> 2;
+    const int r0 = 8 * dw + (lane & 7), grp = lane >> 3;
     const int kg = p.m_dim / kMxBlock;
-    uint32_t it = 0, ph = 0;
+    uint32_t it = 0, tph = 0;  // bit st: uses of lfull[st], mod 2 (both teams count them all)
     bool ok = true;
     for (int u = u_begin; u < u_end && ok; u += u_step) {
       Unit t;
       decode(u, t);
       const int steps = (t.len + kBK - 1) / kBK;
       const int g = (t.m0 + (int)crank * 128) / kMxBlock + grp;
-      // scale bytes are fetched a step ahead of their codes
-      auto scale_at = [&](int s) {
-        const int l = s * kBK + r;
-        return g < kg && l < t.len ? (int)__ldg(p.x_scales + (int64_t)(t.l0 + l) * kg + g) : 0;
-      };
-      int next = steps > 0 ? scale_at(0) : 0;
-      for (int s = 0; s < steps; ++s, ++it) {
-        const int st = it % S;
-        const float sc = e8m0_to_f((uint8_t)next);
-        if (s + 1 < steps) next = scale_at(s + 1);
-        ok = mbar_wait(smem_u32(&lfull[st]), ph >> st & 1, &s_abort);
+      auto scale_at = [&](int l) { return g < kg && l < t.len ? (int)__ldg(p.x_scales + (int64_t)(t.l0 + l) * kg + g) : 0; };
+      // scale bytes are fetched one of the team's stages ahead of their codes
+      int s = (int)((it ^ (uint32_t)team) & 1u);
+      int next[2] = {scale_at(s * kBK + r0), scale_at(s * kBK + r0 + 32)};
+      const bool ragged = t.len % kBK != 0;
+      for (; s < steps; s += 2) {
+        const uint32_t i = it + s;
+        const int st = i % S, raw_slot = i % kRawSlots;
+        const float sc[2] = {e8m0_to_f((uint8_t)next[0]), e8m0_to_f((uint8_t)next[1])};
+        next[0] = scale_at((s + 2) * kBK + r0);
+        next[1] = scale_at((s + 2) * kBK + r0 + 32);
+        const bool tail = ragged && s == steps - 1;
+        const int left = t.len - s * kBK;
+        ok = mbar_wait(smem_u32(&rfull[raw_slot]), (i / kRawSlots) & 1, &s_abort);
+        // the operand slot is free (its last MMAs have read it)
+        ok = ok && mbar_wait(smem_u32(&empty[st]), ((i / S) & 1) ^ 1, &s_abort);
+        // and dy's rows of a last stage are in place, to be cut off below
+        if (tail) ok = ok && mbar_wait(smem_u32(&lfull[st]), tph >> st & 1, &s_abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        ph ^= 1u << st;
-        const uint32_t ta = smem_u32(tiles + (size_t)st * kStage), raw = ta + 2 * kTile;
-        const int left = t.len - s * kBK;
-        const bool live = r < left;
+        const uint32_t ta = smem_u32(tiles + (size_t)st * kStage), raw = smem_u32(raws + raw_slot * kRaw);
+        uint4 c[2][2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 c = ld_shared_16(raw + r * 128 + (((2 * grp + h) ^ (r & 7)) << 4));
-          const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
-          uint32_t o[8];
+        for (int v = 0; v < 2; ++v)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t two = (cw[i >> 1] >> (16 * (i & 1))) & 0xffffu;
-            const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-            const float2 f = __half22float2(__half2(hr));
-            const float lo = f.x * sc, hi = f.y * sc;
-            o[i] = !live ? 0u : p.bf16 ? pack2<ElemBf16>(lo, hi) : pack2<ElemF16>(lo, hi);
+          for (int h = 0; h < 2; ++h) {
+            const int r = r0 + 32 * v;
+            c[v][h] = ld_shared_16(raw + r * 128 + (((2 * grp + h) ^ (r & 7)) << 4));
           }
-          // columns 32 grp + 16 h .. + 15: two 16-byte columns of the line in box grp / 2
-          const uint32_t line = ta + (grp >> 1) * (kTile / 2) + r * 128;
-          const int col = (grp & 1) * 4 + 2 * h;
-          st_shared_16(line + ((col ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
-          st_shared_16(line + (((col + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
-        }
-        if (left < kBK && r >= left) {
-          // the segment's last step: dy's lines past its end (both 64-column boxes, this
-          // thread's quarter of each)
-          const uint32_t line = ta + kTile + r * 128;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int chunk = grp * 4 + i;
-            st_shared_16(line + (chunk >> 3) * (kTile / 2) + ((chunk & 7) << 4), 0, 0, 0, 0);
+        for (int v = 0; v < 2; ++v) {
+          const int r = r0 + 32 * v;
+          const bool live = r < left;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t cw[4] = {c[v][h].x, c[v][h].y, c[v][h].z, c[v][h].w};
+            uint32_t o[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t two = (cw[k >> 1] >> (16 * (k & 1))) & 0xffffu;
+              const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+              const float2 f = __half22float2(__half2(hr));
+              const float lo = f.x * sc[v], hi = f.y * sc[v];
+              o[k] = !live ? 0u : p.bf16 ? pack2<ElemBf16>(lo, hi) : pack2<ElemF16>(lo, hi);
+            }
+            // columns 32 grp + 16 h .. + 15: two 16-byte columns of the line in box grp / 2
+            const uint32_t line = ta + (grp >> 1) * (kTile / 2) + r * 128;
+            const int col = (grp & 1) * 4 + 2 * h;
+            st_shared_16(line + ((col ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
+            st_shared_16(line + (((col + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
+          }
+          if (tail && !live) {
+            // dy's line past the segment's end: this thread's quarter of both 64-column boxes
+            const uint32_t line = ta + kTile + r * 128;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int chunk = grp * 4 + k;
+              st_shared_16(line + (chunk >> 3) * (kTile / 2) + ((chunk & 7) << 4), 0, 0, 0, 0);
+            }
           }
         }
         fence_async_shared();
         __syncwarp();
-        if (lane == 0) arrive_release_cluster(mapa_shared(smem_u32(&full[st]), 0));
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&decoded[st]));
+          mbar_arrive(smem_u32(&rempty[raw_slot]));
+        }
       }
+      if (ragged) tph ^= 1u << ((it + steps - 1) % S);
+      it += steps;
     }
   }
 
@@ -599,22 +754,39 @@ __global__ void __launch_bounds__(threads(MODE), 1)
   }
 }
 
-static bool encode16(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
-                     const uint32_t* box) {
+static bool encode(CUtensorMap* map, const void* base, CUtensorMapDataType type, int rank, const uint64_t* dims,
+                   const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   cuuint64_t d[3], st[2];
   cuuint32_t b[3], es[3] = {1, 1, 1};
   for (int i = 0; i < rank; ++i) d[i] = dims[i], b[i] = box[i];
   for (int i = 0; i + 1 < rank; ++i) st[i] = strides[i];
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, (cuuint32_t)rank, const_cast<void*>(base), d, st, b, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return enc(map, type, (cuuint32_t)rank, const_cast<void*>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// operand tiles of 2-byte elements
+static bool encode16(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                     const uint32_t* box) {
+  return encode(map, base, CU_TENSOR_MAP_DATA_TYPE_UINT16, rank, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Output boxes; false (and an unused map) where rows do not start on 16-byte boundaries.
+static bool encode_out(CUtensorMap* map, void* base, int32_t dtype, uint64_t m, uint64_t rows, uint64_t E, int64_t ld,
+                       int64_t expert) {
+  const bool f32 = dtype == FTMOE_OUT_FP32;
+  const int64_t b = f32 ? 4 : 2;
+  if ((uintptr_t)base % 16 != 0 || ld * b % 16 != 0 || (E > 1 && expert * b % 16 != 0)) return false;
+  const uint64_t dims[3] = {m, rows, E}, st[2] = {(uint64_t)(ld * b), (uint64_t)(E > 1 ? expert * b : ld * b)};
+  const uint32_t box[3] = {128, f32 ? 16u : 32u, 1};
+  return encode(map, base, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, dims, st, box,
+                CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 template <int MODE>
 static cudaError_t launch(const CUtensorMap* maps, const Params& p, cudaStream_t st, int* unsupported) {
-  const size_t smem = 1024 + (size_t)stages(MODE) * stage_bytes(MODE) + (is_wgrad(MODE) ? 0 : ((size_t)p.E + 1) * 4);
+  const size_t smem = 1024 + (size_t)smem_bytes(MODE) + (is_wgrad(MODE) ? 0 : ((size_t)p.E + 1) * 4);
   int dev = 0;
   cudaGetDevice(&dev);
   // per device: CTA pairs that can be resident at once, with the largest shared memory this
@@ -622,7 +794,7 @@ static cudaError_t launch(const CUtensorMap* maps, const Params& p, cudaStream_t
   static int pairs[64] = {};
   int np = dev >= 0 && dev < 64 ? pairs[dev] : 0;
   if (np == 0) {
-    const size_t most = 1024 + (size_t)stages(MODE) * stage_bytes(MODE) + (is_wgrad(MODE) ? 0 : (kMaxExperts + 1) * 4);
+    const size_t most = 1024 + (size_t)smem_bytes(MODE) + (is_wgrad(MODE) ? 0 : (kMaxExperts + 1) * 4);
     const cudaError_t e =
         cudaFuncSetAttribute(tc_matmul16_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (e != cudaSuccess) return e;
@@ -635,7 +807,7 @@ static cudaError_t launch(const CUtensorMap* maps, const Params& p, cudaStream_t
     return cudaSuccess;
   }
   return launch_kernel_cluster(tc_matmul16_kernel<MODE>, dim3(2 * np), dim3(threads(MODE)), smem, st, false, 2, maps[0],
-                               maps[1], maps[2], maps[3], maps[4], p);
+                               maps[1], maps[2], maps[3], maps[4], maps[5], p);
 }
 
 }  // namespace tc16
@@ -649,7 +821,7 @@ cudaError_t launch_tc_matmul16(const Matmul16Args& a, cudaStream_t st, int* unsu
   const ftmoe_matrix_bank& w = a.w;
   const int64_t E = w.num_experts;
   if (E > kMaxExperts || a.rows < 1) return cudaSuccess;
-  CUtensorMap maps[5];
+  CUtensorMap maps[6];
   Params p = {};
   p.offsets = a.offsets;
   p.rows = a.rows;
@@ -676,6 +848,8 @@ cudaError_t launch_tc_matmul16(const Matmul16Args& a, cudaStream_t st, int* unsu
     p.m_dim = (int)m;
     p.l_dim = (int)l;
     p.out_dtype = a.out_dtype;
+    p.tma_out = encode_out(&maps[5], a.out, a.out_dtype, (uint64_t)m, R, 1, a.ld_out, 0);
+    if (!p.tma_out) maps[5] = maps[0];
     *unsupported = 0;
     return a.input_grad ? launch<kInputGrad>(maps, p, st, unsupported) : launch<kProduct>(maps, p, st, unsupported);
   }
@@ -703,6 +877,8 @@ cudaError_t launch_tc_matmul16(const Matmul16Args& a, cudaStream_t st, int* unsu
   p.c_dim = (int)w.n;
   p.out_dtype = w.dtype;
   p.accumulate = a.accumulate;
+  p.tma_out = encode_out(&maps[5], w.w, w.dtype, (uint64_t)w.k, (uint64_t)w.n, (uint64_t)E, w.ld, w.expert_stride);
+  if (!p.tma_out) maps[5] = maps[0];
   *unsupported = 0;
   return a.x_scales ? launch<kWeightGradSaved>(maps, p, st, unsupported) : launch<kWeightGrad>(maps, p, st, unsupported);
 }
