@@ -28,10 +28,10 @@
 // segment, in A and in B (what is there may be NaN), up to the next multiple of 16, and hands
 // the stage to the MMA issuer, which runs only the 16-row steps that hold rows.
 // From saved rows (MXFP8), A arrives as codes; eight warps decode them into the operand tile,
-// two 32-wide groups with their power-of-two scales per thread, exactly.
+// a 32-wide group with its power-of-two scale at a time, exactly.
 //
 // Roles: warp 0 TMA, warp 1 MMA issue and TMEM, warp 2 segment tails (weight grad) or codes
-// (saved rows), warp 3 relay (saved rows), warps 4-11 epilogue, warps 12-19 decode (saved rows). Every mbarrier wait is bounded: on timeout the
+// (saved rows), warps 4-11 epilogue, warps 12-19 decode (saved rows). Every mbarrier wait is bounded: on timeout the
 // kernel raises FTMOE_ERR_WAIT_TIMEOUT, stops its roles, waits for its own loads and MMAs,
 // frees its TMEM and returns.
 #include <cuda.h>
@@ -53,17 +53,18 @@ constexpr int kBK = 64;                   // elements of l per stage: one 128-by
 constexpr int kM = 256, kN = 256;         // of the pair
 constexpr int kTile = 128 * kBK * 2;      // 16 KiB: this CTA's half of A, and of B at most
 constexpr int kRaw = 128 * kBK;           // saved rows: 8 KiB of codes
-constexpr int kRawSlots = 6;
+constexpr int kRawSlots = 4;
 constexpr int kOutBuf = 8192;             // an output box: 32 columns of c (16 of fp32) by 128 of m
-constexpr int kEpiWarps = 8, kDecWarps = 8;
+constexpr int kOutBufs = 3;               // boxes in flight for each half of the epilogue
+constexpr int kEpiWarps = 8, kDecWarps = 8, kDecTeams = 4, kTeamWarps = kDecWarps / kDecTeams;
 constexpr int kMaxExperts = 4096;
 
 __host__ __device__ constexpr bool is_wgrad(int mode) { return mode >= kWeightGrad; }
 // 32 KiB a stage (a fill takes about as long as three stages' MMAs; 4, 5 and 6 stages measured
-// the same), two output boxes for each half of the epilogue, and the ring of codes.
+// the same), the output boxes of both halves of the epilogue, and the ring of codes.
 __host__ __device__ constexpr int stages(int mode) { return mode == kWeightGradSaved ? 4 : 5; }
 __host__ __device__ constexpr int smem_bytes(int mode) {
-  return stages(mode) * 2 * kTile + 4 * kOutBuf + (mode == kWeightGradSaved ? kRawSlots * kRaw : 0);
+  return stages(mode) * 2 * kTile + 2 * kOutBufs * kOutBuf + (mode == kWeightGradSaved ? kRawSlots * kRaw : 0);
 }
 __host__ __device__ constexpr int threads(int mode) { return 32 * (4 + kEpiWarps + (mode == kWeightGradSaved ? kDecWarps : 0)); }
 
@@ -138,10 +139,18 @@ __device__ __forceinline__ void tma_pair_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// arrive on a barrier of the pair's first CTA, releasing this CTA's shared-memory writes (fenced
-// into the async proxy before) to the thread that issues the pair's MMAs
-__device__ __forceinline__ void arrive_release_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// Handing operand tiles that ordinary stores have touched (decoded codes, zeroed lines) to the
+// pair's MMA issuer: every writing thread fences its stores into the async proxy, which waits
+// until they are performed in this SM's shared memory, the warp converges, and one lane arrives
+// on the first CTA's barrier. Each SM's tensor core reads its operands from its own shared
+// memory, so nothing has to become visible in the other SM but the arrival, and the arrival
+// needs no cluster-scope release. That release waits for global memory: with it the decode of
+// 24,576 rows over 32 experts, 4096 x 7168, took 2,007 us instead of 1,342.
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void hand_over(uint64_t* full, int lane) {
+  fence_async_shared();
+  __syncwarp();
+  if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(full), 0));
 }
 __device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -166,7 +175,6 @@ __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, vola
   }
   return true;
 }
-__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void st_shared_16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -255,13 +263,11 @@ __global__ void __launch_bounds__(threads(MODE), 1)
   constexpr int S = stages(MODE), kStage = 2 * kTile;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  uint8_t* outbuf = tiles + (size_t)S * kStage;        // [2 halves of the epilogue][2] output boxes
-  uint8_t* raws = outbuf + 4 * kOutBuf;                // saved rows: [kRawSlots] codes
+  uint8_t* outbuf = tiles + (size_t)S * kStage;        // [2 halves of the epilogue][kOutBufs] output boxes
+  uint8_t* raws = outbuf + 2 * kOutBufs * kOutBuf;     // saved rows: [kRawSlots] codes
   int* cum = reinterpret_cast<int*>(raws);             // else: [E + 1] units before expert e (not weight grad)
   __shared__ __align__(8) uint64_t full[S], empty[S], lfull[S], tfull[2], tempty[2];
-  // saved rows: codes landed / taken; operand tile decoded in this CTA (the second CTA reports it
-  // to the first's full barrier through one thread)
-  __shared__ __align__(8) uint64_t rfull[kRawSlots], rempty[kRawSlots], decoded[S];
+  __shared__ __align__(8) uint64_t rfull[kRawSlots], rempty[kRawSlots];  // saved rows: codes landed, codes taken
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
 
@@ -282,15 +288,15 @@ __global__ void __launch_bounds__(threads(MODE), 1)
     s_abort = 0;
     for (int i = 0; i < S; ++i) {
       // weight grad: two arrivals of the first CTA's producer, or (a segment's last stage) one
-      // of each CTA's tail warp; saved rows: both CTAs' relays and the first CTA's producer
-      mbar_init(smem_u32(&full[i]), kSaved ? 3 : kWG ? 2 : 1);
+      // of each CTA's tail warp; saved rows: the decoding warps of both CTAs and the first
+      // CTA's producer
+      mbar_init(smem_u32(&full[i]), kSaved ? 2 * kTeamWarps + 1 : kWG ? 2 : 1);
       mbar_init(smem_u32(&empty[i]), 1);
       mbar_init(smem_u32(&lfull[i]), 1);
-      mbar_init(smem_u32(&decoded[i]), kDecWarps / 2);
     }
     for (int i = 0; i < kRawSlots; ++i) {
       mbar_init(smem_u32(&rfull[i]), 1);
-      mbar_init(smem_u32(&rempty[i]), kDecWarps / 2);
+      mbar_init(smem_u32(&rempty[i]), kTeamWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&tfull[i]), 1);
@@ -504,9 +510,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
         // lines v .. vr - 1 of the four 64-column boxes (A and B), 8 chunks of 16 bytes each
         for (int i = lane; i < (vr - v) * 32; i += 32)
           st_shared_16(ta + (i / 8 % 4) * (kTile / 2) + (v + i / 32) * 128 + (i % 8) * 16, 0, 0, 0, 0);
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0) arrive_release_cluster(mapa_shared(smem_u32(&full[st]), 0));
+        hand_over(&full[st], lane);
       }
       it += steps;
     }
@@ -532,23 +536,6 @@ __global__ void __launch_bounds__(threads(MODE), 1)
         }
       }
     }
-  } else if (kSaved && warp == 3) {
-    // ------------------------ saved rows: relay ------------------------
-    // One thread hands this CTA's decoded tiles to the first CTA's full barrier: the release at
-    // cluster scope waits for memory, and eight decoding warps doing it each would wait as often.
-    if (lane == 0) {
-      uint32_t it = 0;
-      for (int u = u_begin; u < u_end && !s_abort; u += u_step) {
-        Unit t;
-        decode(u, t);
-        const int steps = (t.len + kBK - 1) / kBK;
-        for (int s = 0; s < steps; ++s, ++it) {
-          const int st = it % S;
-          if (!mbar_wait(smem_u32(&decoded[st]), (it / S) & 1, &s_abort)) break;
-          arrive_release_cluster(mapa_shared(smem_u32(&full[st]), 0));
-        }
-      }
-    }
   } else if (warp >= 4 && warp < 4 + kEpiWarps) {
     // --------------------------------- epilogue ---------------------------------
     // Two groups of four warps take chunks of 32 columns in turn. A chunk goes through shared
@@ -558,7 +545,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
     // an expert's rows, an unaligned output and a 16-bit accumulation are stored from registers.
     const int ew = warp - 4, quarter = warp & 3, half = ew >> 2;
     const bool leader = quarter == 0 && lane == 0;
-    uint32_t acc = 0, box = 0;
+    uint32_t acc = 0, box = 0;  // units, output boxes so far
     const bool words = p.ld_out % 2 == 0 && p.out_expert % 2 == 0 && reinterpret_cast<uintptr_t>(p.out) % 4 == 0;
     const bool tma_out = p.tma_out && (!p.accumulate || p.out_dtype == FTMOE_OUT_FP32);
     for (int u = u_begin; u < u_end; u += u_step) {
@@ -599,10 +586,9 @@ __global__ void __launch_bounds__(threads(MODE), 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (h == 1 && per == 32) break;
-            uint8_t* ob = outbuf + (2 * half + (box & 1)) * kOutBuf;
-            // the store that used this buffer two boxes ago has read it
-            if (leader) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-            named_bar(1 + half, 128);
+            // free: the barrier of the box before this one followed the leader's wait for the
+            // store that last used this buffer
+            uint8_t* ob = outbuf + (kOutBufs * half + box % kOutBufs) * kOutBuf;
             if (p.out_dtype == FTMOE_OUT_FP32) {
 #pragma unroll
               for (int j = 0; j < 16; ++j) reinterpret_cast<float*>(ob)[j * 128 + ml] = d[16 * h + j];
@@ -622,6 +608,8 @@ __global__ void __launch_bounds__(threads(MODE), 1)
               }
             }
             fence_async_shared();
+            // all stores but the latest have read their buffers, the next box's among them
+            if (leader) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kOutBufs - 2) : "memory");
             named_bar(1 + half, 128);
             if (leader) {
               const int y = t.c0 + c + 16 * h;
@@ -654,32 +642,40 @@ __global__ void __launch_bounds__(threads(MODE), 1)
     if (leader) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   } else if (kSaved && warp >= 4 + kEpiWarps) {
     // ------------------------ saved rows: decode ------------------------
-    // Two groups of four warps take stages in turn, so that one decodes while the other waits
-    // for its stores to be visible. Thread (warp dw, lane): lines r and r + 32 of the stage's
-    // 64, r = 8 dw + lane % 8, and the 32-wide group lane / 8 of their 128 codes. Eight lanes
-    // with consecutive lines touch eight different 16-byte columns of the swizzled lines,
-    // reading and writing.
-    const int dw = (warp - 4 - kEpiWarps) & 3, team = (warp - 4 - kEpiWarps) >> 2;
+    // Four teams of two warps take stages in turn, so that some decode while others wait for
+    // codes, for a free operand slot or for their stores to be visible. Thread (warp dw of the
+    // team, lane): lines r0 + 16 v of the stage's 64, r0 = 8 dw + lane % 8, and the 32-wide group
+    // lane / 8 of their 128 codes. Eight lanes with consecutive lines touch eight different
+    // 16-byte columns of the swizzled lines, reading and writing.
+    const int dw = (warp - 4 - kEpiWarps) % kTeamWarps, team = (warp - 4 - kEpiWarps) / kTeamWarps;
     const int r0 = 8 * dw + (lane & 7), grp = lane >> 3;
+    constexpr int kLines = 64 / (8 * kTeamWarps);
     const int kg = p.m_dim / kMxBlock;
-    uint32_t it = 0, tph = 0;  // bit st: uses of lfull[st], mod 2 (both teams count them all)
+    uint32_t it = 0, tph = 0;  // tph, bit st: uses of lfull[st], mod 2 (every team counts them all)
     bool ok = true;
     for (int u = u_begin; u < u_end && ok; u += u_step) {
       Unit t;
       decode(u, t);
       const int steps = (t.len + kBK - 1) / kBK;
       const int g = (t.m0 + (int)crank * 128) / kMxBlock + grp;
-      auto scale_at = [&](int l) { return g < kg && l < t.len ? (int)__ldg(p.x_scales + (int64_t)(t.l0 + l) * kg + g) : 0; };
-      // scale bytes are fetched one of the team's stages ahead of their codes
-      int s = (int)((it ^ (uint32_t)team) & 1u);
-      int next[2] = {scale_at(s * kBK + r0), scale_at(s * kBK + r0 + 32)};
+      // scale bytes, fetched one of the team's stages ahead of their codes
+      uint32_t next = 0;
+      auto fetch = [&](int s) {
+        next = 0;
+#pragma unroll
+        for (int v = 0; v < kLines; ++v) {
+          const int l = s * kBK + r0 + 8 * kTeamWarps * v;
+          const uint32_t b = g < kg && l < t.len ? (uint32_t)__ldg(p.x_scales + (int64_t)(t.l0 + l) * kg + g) : 0u;
+          next |= b << (8 * v);
+        }
+      };
+      int s = (int)(((uint32_t)team - it) % kDecTeams);
+      fetch(s);
       const bool ragged = t.len % kBK != 0;
-      for (; s < steps; s += 2) {
-        const uint32_t i = it + s;
+      for (; s < steps; s += kDecTeams) {
+        const uint32_t i = it + s, scales = next;
         const int st = i % S, raw_slot = i % kRawSlots;
-        const float sc[2] = {e8m0_to_f((uint8_t)next[0]), e8m0_to_f((uint8_t)next[1])};
-        next[0] = scale_at((s + 2) * kBK + r0);
-        next[1] = scale_at((s + 2) * kBK + r0 + 32);
+        fetch(s + kDecTeams);
         const bool tail = ragged && s == steps - 1;
         const int left = t.len - s * kBK;
         ok = mbar_wait(smem_u32(&rfull[raw_slot]), (i / kRawSlots) & 1, &s_abort);
@@ -690,28 +686,24 @@ __global__ void __launch_bounds__(threads(MODE), 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t ta = smem_u32(tiles + (size_t)st * kStage), raw = smem_u32(raws + raw_slot * kRaw);
-        uint4 c[2][2];
-#pragma unroll
-        for (int v = 0; v < 2; ++v)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int r = r0 + 32 * v;
-            c[v][h] = ld_shared_16(raw + r * 128 + (((2 * grp + h) ^ (r & 7)) << 4));
-          }
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const int r = r0 + 32 * v;
+#pragma unroll 2
+        for (int v = 0; v < kLines; ++v) {
+          const int r = r0 + 8 * kTeamWarps * v;
           const bool live = r < left;
+          const float sc = e8m0_to_f((uint8_t)(scales >> (8 * v)));
+          uint4 c[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) c[h] = ld_shared_16(raw + r * 128 + (((2 * grp + h) ^ (r & 7)) << 4));
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t cw[4] = {c[v][h].x, c[v][h].y, c[v][h].z, c[v][h].w};
+            const uint32_t cw[4] = {c[h].x, c[h].y, c[h].z, c[h].w};
             uint32_t o[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const uint32_t two = (cw[k >> 1] >> (16 * (k & 1))) & 0xffffu;
               const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
               const float2 f = __half22float2(__half2(hr));
-              const float lo = f.x * sc[v], hi = f.y * sc[v];
+              const float lo = f.x * sc, hi = f.y * sc;
               o[k] = !live ? 0u : p.bf16 ? pack2<ElemBf16>(lo, hi) : pack2<ElemF16>(lo, hi);
             }
             // columns 32 grp + 16 h .. + 15: two 16-byte columns of the line in box grp / 2
@@ -730,12 +722,8 @@ __global__ void __launch_bounds__(threads(MODE), 1)
             }
           }
         }
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(smem_u32(&decoded[st]));
-          mbar_arrive(smem_u32(&rempty[raw_slot]));
-        }
+        hand_over(&full[st], lane);
+        if (lane == 0) mbar_arrive(smem_u32(&rempty[raw_slot]));
       }
       if (ragged) tph ^= 1u << ((it + steps - 1) % S);
       it += steps;
