@@ -686,33 +686,48 @@ __global__ void __launch_bounds__(threads(MODE), 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t ta = smem_u32(tiles + (size_t)st * kStage), raw = smem_u32(raws + raw_slot * kRaw);
+        // (the element type is chosen outside the loops)
+        auto lines = [&](auto elem) {
+          using Elem = decltype(elem);
 #pragma unroll 2
-        for (int v = 0; v < kLines; ++v) {
-          const int r = r0 + 8 * kTeamWarps * v;
-          const bool live = r < left;
-          const float sc = e8m0_to_f((uint8_t)(scales >> (8 * v)));
-          uint4 c[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) c[h] = ld_shared_16(raw + r * 128 + (((2 * grp + h) ^ (r & 7)) << 4));
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t cw[4] = {c[h].x, c[h].y, c[h].z, c[h].w};
-            uint32_t o[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const uint32_t two = (cw[k >> 1] >> (16 * (k & 1))) & 0xffffu;
-              const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-              const float2 f = __half22float2(__half2(hr));
-              const float lo = f.x * sc, hi = f.y * sc;
-              o[k] = !live ? 0u : p.bf16 ? pack2<ElemBf16>(lo, hi) : pack2<ElemF16>(lo, hi);
-            }
+          for (int v = 0; v < kLines; ++v) {
+            const int r = r0 + 8 * kTeamWarps * v;
+            const bool live = r < left;
+            const float sc = e8m0_to_f((uint8_t)(scales >> (8 * v)));
             // columns 32 grp + 16 h .. + 15: two 16-byte columns of the line in box grp / 2
             const uint32_t line = ta + (grp >> 1) * (kTile / 2) + r * 128;
-            const int col = (grp & 1) * 4 + 2 * h;
-            st_shared_16(line + ((col ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
-            st_shared_16(line + (((col + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
+            uint4 c[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              c[h] = ld_shared_16(raw + r * 128 + (((2 * grp + h) ^ (r & 7)) << 4));
+              if (!live) c[h] = make_uint4(0u, 0u, 0u, 0u);  // (a code past the segment may be NaN)
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t cw[4] = {c[h].x, c[h].y, c[h].z, c[h].w};
+              uint32_t o[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const uint32_t two = (cw[k >> 1] >> (16 * (k & 1))) & 0xffffu;
+                const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+                const float2 f = __half22float2(__half2(hr));
+                o[k] = pack2<Elem>(f.x * sc, f.y * sc);
+              }
+              const int col = (grp & 1) * 4 + 2 * h;
+              st_shared_16(line + ((col ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
+              st_shared_16(line + (((col + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
+            }
           }
-          if (tail && !live) {
+        };
+        if (p.bf16)
+          lines(ElemBf16{});
+        else
+          lines(ElemF16{});
+        if (tail) {
+#pragma unroll
+          for (int v = 0; v < kLines; ++v) {
+            const int r = r0 + 8 * kTeamWarps * v;
+            if (r < left) continue;
             // dy's line past the segment's end: this thread's quarter of both 64-column boxes
             const uint32_t line = ta + kTile + r * 128;
 #pragma unroll
