@@ -330,114 +330,138 @@ def ftmoe_expert_slots(expert_ids, slot_expert, slot_usage, expert_slot, step, m
         _stream(stream)))
 
 
+# The training entry points check what the C entry cannot see (devices, shapes, dtypes, contiguous
+# rows) in as few tensor queries as that takes: at decode sizes the binding costs more than the
+# kernel, and each query of a tensor costs about as much as a Python call.
+
 def _dtype_code(t, name):
-    if t.dtype not in _OUT_DTYPES:
+    code = _OUT_DTYPES.get(t.dtype)
+    if code is None:
         raise ValueError(f"{name} dtype {t.dtype} is not one of bf16, fp16, fp32")
-    return _OUT_DTYPES[t.dtype]
+    return code
 
 
-def _same(want, **tensors):
-    """Devices, shapes and dtypes that the C entry cannot see: {name: (tensor, shape)} against dtype `want`
-    (None: any). Rows are contiguous."""
-    for name, (t, shape) in tensors.items():
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} is not on a CUDA device")
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        if want is not None and t.dtype != want:
-            raise ValueError(f"{name} is {t.dtype}, expected {want}")
-        if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
-            raise ValueError(f"the rows of {name} are not contiguous")
+def _refuse(t, name, shape, dtype):
+    """Says what is wrong with a tensor that failed a check."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} is not on a CUDA device")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
+    raise ValueError(f"the rows of {name} are not contiguous")
 
 
-def _ld(t):
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+def _rows_of(t, name, rows, cols, dtype=None):
+    """Row stride of a [rows, cols] tensor with contiguous rows (any stride where there is one row)."""
+    if not t.is_cuda or t.shape != (rows, cols) or (dtype is not None and t.dtype != dtype):
+        _refuse(t, name, (rows, cols), dtype)
+    ld, one = t.stride()
+    if one != 1 and cols > 1 and rows:
+        _refuse(t, name, (rows, cols), dtype)
+    return ld if rows > 1 else max(cols, ld)
+
+
+def _dense_of(t, name, shape, dtype):
+    """Address of a contiguous tensor of this shape."""
+    if not t.is_cuda or t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        _refuse(t, name, shape, dtype)
+    return t.data_ptr()
+
+
+def _raw_stream(stream, t):
+    """The stream handle as an int: the given one, or the current one of the tensor's device."""
+    if stream is None:
+        return _current_raw_stream(t.get_device())
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+try:
+    _current_raw_stream = torch._C._cuda_getCurrentRawStream
+except AttributeError:  # a torch without CUDA
+    def _current_raw_stream(device):
+        return torch.cuda.current_stream(device).cuda_stream
 
 
 def make_matrix_bank(w):
     """MatrixBank view of a [E, n, k] tensor of bf16, fp16 or fp32 matrices (any expert and row
     strides, contiguous rows)."""
     E, n, k = w.shape
-    _same(None, w=(w, (E, n, k)))
-    ld = w.stride(1) if n > 1 else max(k, w.stride(1))
-    es = w.stride(0) if E > 1 else max((n - 1) * ld + k, w.stride(0))
-    return MatrixBank(_dtype_code(w, "w"), E, n, k, ld, es, _p(w))
-
-
-def _check_offsets(offsets, E):
-    _same(torch.int32, offsets=(offsets, (E + 1,)))
+    es, ld, one = w.stride()
+    if not w.is_cuda or (one != 1 and k > 1):
+        _refuse(w, "w", (E, n, k), None)
+    if n <= 1:
+        ld = max(k, ld)
+    if E <= 1:
+        es = max((n - 1) * ld + k, es)
+    return MatrixBank(_dtype_code(w, "w"), E, n, k, ld, es, w.data_ptr())
 
 
 def ftmoe_grouped_matmul(a, offsets, w, out, input_grad=False, stream=None):
     """out rows = a rows times the transposed matrix of their expert (input_grad: times the
     matrix itself). a [rows, k] (input_grad: [rows, n]), w [E, n, k], both bf16 or fp16; out
     [rows, n] (input_grad: [rows, k]) bf16, fp16 or fp32; offsets int32 [E + 1]."""
-    E, n, k = w.shape
-    rows = a.shape[0]
-    _check_offsets(offsets, E)
-    _same(w.dtype, a=(a, (rows, n if input_grad else k)))
-    _same(None, out=(out, (rows, k if input_grad else n)))
     bank = make_matrix_bank(w)
-    _check("ftmoe_grouped_matmul", lib().ftmoe_grouped_matmul(
-        _p(a), rows, _ld(a), _p(offsets), ctypes.byref(bank), int(bool(input_grad)), _p(out), _ld(out),
-        out_dtype_code(out), _stream(stream)))
+    rows, wide_in, wide_out = a.shape[0], bank.k, bank.n
+    if input_grad:
+        wide_in, wide_out = wide_out, wide_in
+    off = _dense_of(offsets, "offsets", (bank.num_experts + 1,), torch.int32)
+    ld_a, ld_out = _rows_of(a, "a", rows, wide_in, w.dtype), _rows_of(out, "out", rows, wide_out)
+    st = lib().ftmoe_grouped_matmul(a.data_ptr(), rows, ld_a, off, bank, 1 if input_grad else 0, out.data_ptr(), ld_out,
+                                    _dtype_code(out, "out"), _raw_stream(stream, a))
+    if st:
+        raise FtmoeError("ftmoe_grouped_matmul", st)
 
 
 def ftmoe_grouped_matmul_wgrad(dy, x, offsets, dw, accumulate=False, stream=None):
     """dw[e] = dy_e^T x_e over the rows of expert e (accumulate: added to dw). dy [rows, n] and
     x [rows, k] bf16 or fp16, dw [E, n, k] bf16, fp16 or fp32."""
-    E, n, k = dw.shape
-    rows = dy.shape[0]
-    _check_offsets(offsets, E)
-    _same(dy.dtype, dy=(dy, (rows, n)), x=(x, (rows, k)))
     bank = make_matrix_bank(dw)
-    _check("ftmoe_grouped_matmul_wgrad", lib().ftmoe_grouped_matmul_wgrad(
-        _p(dy), _ld(dy), _p(x), _ld(x), rows, _dtype_code(dy, "dy"), _p(offsets), ctypes.byref(bank),
-        int(bool(accumulate)), _stream(stream)))
+    rows, dt = dy.shape[0], dy.dtype
+    off = _dense_of(offsets, "offsets", (bank.num_experts + 1,), torch.int32)
+    ld_dy, ld_x = _rows_of(dy, "dy", rows, bank.n), _rows_of(x, "x", rows, bank.k, dt)
+    st = lib().ftmoe_grouped_matmul_wgrad(dy.data_ptr(), ld_dy, x.data_ptr(), ld_x, rows, _dtype_code(dy, "dy"), off,
+                                          bank, 1 if accumulate else 0, _raw_stream(stream, dw))
+    if st:
+        raise FtmoeError("ftmoe_grouped_matmul_wgrad", st)
 
 
 def ftmoe_grouped_matmul_wgrad_saved(dy, q, scales, offsets, dw, fmt=FMT_MXFP8, accumulate=False, stream=None):
     """The same with x as MXFP8 rows: q uint8 [rows, k], scales uint8 [rows, k / 32]."""
-    E, n, k = dw.shape
-    rows = dy.shape[0]
-    _check_offsets(offsets, E)
-    _same(dy.dtype, dy=(dy, (rows, n)))
-    if fmt == FMT_MXFP8:
-        _same(torch.uint8, q=(q, (rows, k)), scales=(scales, (rows, k // 32)))
-        _dense(q=q, scales=scales)
-    act, bank = Act(fmt, 0, rows, k, _p(q), _p(scales), None), make_matrix_bank(dw)
-    _check("ftmoe_grouped_matmul_wgrad_saved", lib().ftmoe_grouped_matmul_wgrad_saved(
-        _p(dy), _ld(dy), _dtype_code(dy, "dy"), ctypes.byref(act), _p(offsets), ctypes.byref(bank),
-        int(bool(accumulate)), _stream(stream)))
+    bank = make_matrix_bank(dw)
+    rows, k = dy.shape[0], bank.k
+    off = _dense_of(offsets, "offsets", (bank.num_experts + 1,), torch.int32)
+    ld_dy = _rows_of(dy, "dy", rows, bank.n)
+    qp = _dense_of(q, "q", (rows, k), torch.uint8)
+    sp = _dense_of(scales, "scales", (rows, k // 32), torch.uint8) if fmt == FMT_MXFP8 else scales.data_ptr()
+    act = Act(fmt, 0, rows, k, qp, sp, None)
+    st = lib().ftmoe_grouped_matmul_wgrad_saved(dy.data_ptr(), ld_dy, _dtype_code(dy, "dy"), act, off, bank,
+                                                1 if accumulate else 0, _raw_stream(stream, dw))
+    if st:
+        raise FtmoeError("ftmoe_grouped_matmul_wgrad_saved", st)
 
 
-def _dense(**tensors):
-    for name, t in tensors.items():
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"{name} is not contiguous")
-
-
-def _check_saved(q, scales, rows, inter, fmt):
-    """q uint8 [rows, 2 * inter] and scales [rows, 2 * groups] of a saved gate/up row."""
-    _same(torch.uint8, q=(q, (rows, 2 * inter)))
+def _saved_of(q, scales, rows, inter, fmt):
+    """Addresses of q uint8 [rows, 2 * inter] and scales [rows, 2 * groups] of kept gate/up rows."""
+    qp = _dense_of(q, "q", (rows, 2 * inter), torch.uint8)
     if fmt == FMT_FP8:
-        _same(torch.float32, scales=(scales, (rows, 2 * cdiv(inter, 128))))
-    elif fmt == FMT_MXFP8:
-        _same(torch.uint8, scales=(scales, (rows, 2 * (inter // 32))))
-    _dense(q=q, scales=scales)
+        return qp, _dense_of(scales, "scales", (rows, 2 * cdiv(inter, 128)), torch.float32)
+    if fmt == FMT_MXFP8:
+        return qp, _dense_of(scales, "scales", (rows, 2 * (inter // 32)), torch.uint8)
+    return qp, scales.data_ptr()
 
 
 def ftmoe_silu_mul_save(gu, h, q, scales, fmt=FMT_MXFP8, rows_dev=None, stream=None):
     """h = silu(gate) * up from gu [rows, 2 * inter], and both halves kept in 8 bits: q uint8
     [rows, 2 * inter], scales [rows, 2 * groups] (FP8: fp32 per 128, MXFP8: uint8 per 32)."""
     rows, inter = h.shape
-    _same(None, gu=(gu, (rows, 2 * inter)), h=(h, (rows, inter)))
-    _check_saved(q, scales, rows, inter, fmt)
-    _check("ftmoe_silu_mul_save", lib().ftmoe_silu_mul_save(
-        _p(gu), _dtype_code(gu, "gu"), rows, inter, _ld(gu), _p(rows_dev), _p(h), _ld(h), _dtype_code(h, "h"), fmt,
-        _p(q), _p(scales), _stream(stream)))
+    ld_gu, ld_h = _rows_of(gu, "gu", rows, 2 * inter), _rows_of(h, "h", rows, inter)
+    qp, sp = _saved_of(q, scales, rows, inter, fmt)
+    st = lib().ftmoe_silu_mul_save(gu.data_ptr(), _dtype_code(gu, "gu"), rows, inter, ld_gu,
+                                   None if rows_dev is None else rows_dev.data_ptr(), h.data_ptr(), ld_h,
+                                   _dtype_code(h, "h"), fmt, qp, sp, _raw_stream(stream, h))
+    if st:
+        raise FtmoeError("ftmoe_silu_mul_save", st)
 
 
 def ftmoe_silu_mul_backward(q, scales, dh, dgu, hw=None, row_weights=None, dweights=None, fmt=FMT_MXFP8,
@@ -445,12 +469,17 @@ def ftmoe_silu_mul_backward(q, scales, dh, dgu, hw=None, row_weights=None, dweig
     """Gradients from the kept gate/up rows: dgu [rows, 2 * inter], hw = weight * h [rows, inter]
     and dweights fp32 [rows], for the gradient dh [rows, inter] of the unweighted h."""
     rows, inter = dh.shape
-    _same(dh.dtype, dh=(dh, (rows, inter)), dgu=(dgu, (rows, 2 * inter)), hw=(hw, (rows, inter)))
-    _same(torch.float32, row_weights=(row_weights, (rows,)), dweights=(dweights, (rows,)))
-    _check_saved(q, scales, rows, inter, fmt)
-    _check("ftmoe_silu_mul_backward", lib().ftmoe_silu_mul_backward(
-        _p(q), _p(scales), fmt, rows, inter, _p(rows_dev), _p(dh), _ld(dh), _dtype_code(dh, "dh"), _p(row_weights),
-        _p(dgu), _ld(dgu), _p(hw), 0 if hw is None else _ld(hw), _p(dweights), _stream(stream)))
+    dt = dh.dtype
+    ld_dh, ld_dgu = _rows_of(dh, "dh", rows, inter), _rows_of(dgu, "dgu", rows, 2 * inter, dt)
+    hp, ld_hw = (None, 0) if hw is None else (hw.data_ptr(), _rows_of(hw, "hw", rows, inter, dt))
+    wp = None if row_weights is None else _dense_of(row_weights, "row_weights", (rows,), torch.float32)
+    dp = None if dweights is None else _dense_of(dweights, "dweights", (rows,), torch.float32)
+    qp, sp = _saved_of(q, scales, rows, inter, fmt)
+    st = lib().ftmoe_silu_mul_backward(qp, sp, fmt, rows, inter, None if rows_dev is None else rows_dev.data_ptr(),
+                                       dh.data_ptr(), ld_dh, _dtype_code(dh, "dh"), wp, dgu.data_ptr(), ld_dgu, hp,
+                                       ld_hw, dp, _raw_stream(stream, dh))
+    if st:
+        raise FtmoeError("ftmoe_silu_mul_backward", st)
 
 
 def ftmoe_selftest_wait_timeout(timeout_ns, elapsed_ns=None, stream=None):

@@ -11,6 +11,8 @@
 // The forward moves 8 bytes per intermediate column (4 read, 2 + 2 written) and 1/16 to 1/32 of
 // scales; the backward 10 (2 codes and 2 of dh read, 4 + 2 written). Keeping gate/up in bf16
 // would move 4 more bytes per column and hold twice the memory between the passes.
+#include <type_traits>
+
 #include "common.cuh"
 #include "elem16.cuh"
 #include "internal.h"
@@ -23,6 +25,15 @@ __device__ __forceinline__ int64_t valid_rows(int64_t rows, const int32_t* rows_
   if (rows_dev == nullptr) return rows;
   const int64_t d = *rows_dev;
   return d < 0 ? 0 : (d < rows ? d : rows);
+}
+
+// 1 / (1 + e) for e = exp(-g) >= 0 or infinite, to one unit in the last place (an IEEE division
+// costs about ten instructions, and these kernels run at the issue rate): silu and its slope are
+// rounded to 16 bits or carried at a few units of fp32 either way.
+__device__ __forceinline__ float sigmoid_of(float e) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return r;
 }
 
 // Codes of 8 values that share a maximum with the lanes around them: 16 lanes (FP8's group of
@@ -68,48 +79,49 @@ __device__ __forceinline__ void store_codes(uint8_t* q, uint2 c, bool vec, int n
   }
 }
 
-// A half-warp per (row, 128 columns): a lane owns 8 columns of both halves.
-template <typename In, typename Out, bool kMx>
+// kTpr threads per row, 8 columns of both halves each per pass; 256 / kTpr rows per CTA. The 16
+// lanes of a half-warp hold one group of 128. (A half-warp per group on a grid-stride loop with a
+// 64-bit division per group ran at half this speed.)
+template <typename In, typename Out, bool kMx, int kTpr>
 __global__ void __launch_bounds__(256) silu_save_kernel(
     const typename In::T* __restrict__ gu, int64_t rows, int64_t inter, int64_t ld_gu,
     const int32_t* __restrict__ rows_dev, typename Out::T* __restrict__ h, int64_t ld_h, uint8_t* __restrict__ q,
     void* __restrict__ scales, bool vec_gu, bool vec_h, bool vec_q) {
-  const int64_t ng = (inter + kGroup - 1) / kGroup;
-  const int64_t units = valid_rows(rows, rows_dev) * ng;
-  const int lane = threadIdx.x & 31, hl = lane & 15;
-  const int64_t nwarps = (int64_t)gridDim.x * (blockDim.x >> 5);
-  // the loop bound is uniform over the warp, so every shuffle sees all 32 lanes
-  for (int64_t w = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); 2 * w < units; w += nwarps) {
-    const int64_t unit = 2 * w + (lane >> 4);
-    const bool live = unit < units;
-    const int64_t row = live ? unit / ng : 0, grp = live ? unit - row * ng : 0;
-    const int64_t c0 = grp * kGroup + hl * 8;
-    const int64_t left = live ? inter - c0 : 0;
-    const int n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
-    float g[8], u[8], a[8];
-    elem_load8<In>(gu + row * ld_gu + c0, vec_gu, n, g);
-    elem_load8<In>(gu + row * ld_gu + inter + c0, vec_gu, n, u);
+  constexpr int kRows = 256 / kTpr;
+  const int64_t limit = valid_rows(rows, rows_dev);
+  const int sub = threadIdx.x / kTpr, tid = threadIdx.x % kTpr;
+  const int64_t nb = kMx ? inter / kMxBlock : (inter + kGroup - 1) / kGroup;
+  for (int64_t base = (int64_t)blockIdx.x * kRows; base < limit; base += (int64_t)gridDim.x * kRows) {
+    const int64_t row = base + sub;
+    const typename In::T* gr = gu + row * ld_gu;
+    // the bound is uniform over the CTA, so every shuffle sees all lanes
+    for (int64_t p0 = 0; p0 < inter; p0 += kTpr * 8) {
+      const int64_t c0 = p0 + tid * 8, left = row < limit ? inter - c0 : 0;
+      const int n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
+      float g[8], u[8], a[8];
+      elem_load8<In>(gr + c0, vec_gu, n, g);
+      elem_load8<In>(gr + inter + c0, vec_gu, n, u);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = silu_mul_1(g[i], u[i]);
-    float sg, su;
-    uint8_t bg, bu;
-    const uint2 cg = quantize8<kMx>(g, sg, bg), cu = quantize8<kMx>(u, su, bu);
-    if (n > 0) {
-      elem_store8<Out>(h + row * ld_h + c0, vec_h, n, a);
-      uint8_t* qr = q + row * 2 * inter + c0;
-      store_codes(qr, cg, vec_q, n);
-      store_codes(qr + inter, cu, vec_q, n);
-      if constexpr (kMx) {
-        if ((lane & 3) == 0) {
-          const int64_t nb = inter / kMxBlock;
-          uint8_t* s = static_cast<uint8_t*>(scales) + row * 2 * nb + c0 / kMxBlock;
-          s[0] = bg;
-          s[nb] = bu;
+      for (int i = 0; i < 8; ++i) a[i] = g[i] * sigmoid_of(expf(-g[i])) * u[i];
+      float sg, su;
+      uint8_t bg, bu;
+      const uint2 cg = quantize8<kMx>(g, sg, bg), cu = quantize8<kMx>(u, su, bu);
+      if (n > 0) {
+        elem_store8<Out>(h + row * ld_h + c0, vec_h, n, a);
+        uint8_t* qr = q + row * 2 * inter + c0;
+        store_codes(qr, cg, vec_q, n);
+        store_codes(qr + inter, cu, vec_q, n);
+        if constexpr (kMx) {
+          if ((tid & 3) == 0) {
+            uint8_t* s = static_cast<uint8_t*>(scales) + row * 2 * nb + c0 / kMxBlock;
+            s[0] = bg;
+            s[nb] = bu;
+          }
+        } else if ((tid & 15) == 0) {
+          float* s = static_cast<float*>(scales) + row * 2 * nb + c0 / kGroup;
+          s[0] = sg;
+          s[nb] = su;
         }
-      } else if (hl == 0) {
-        float* s = static_cast<float*>(scales) + row * 2 * ng + grp;
-        s[0] = sg;
-        s[ng] = su;
       }
     }
   }
@@ -126,7 +138,12 @@ __device__ __forceinline__ void load_codes(const uint8_t* q, bool vec, int n, fl
       if (i < n) c[i >> 2] |= (uint32_t)q[i] << (8 * (i & 3));
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = e4m3_to_f((uint8_t)(c[i >> 2] >> (8 * (i & 3))));
+  for (int i = 0; i < 4; ++i) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
+    const float2 f = __half22float2(__half2(h));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
 }
 
 // kTpr threads per row, 8 columns each per pass; 256 / kTpr rows per CTA. dweights: a thread
@@ -174,7 +191,7 @@ __global__ void __launch_bounds__(256) silu_backward_kernel(
         // the exponential: exp(-(gi + r)) = exp(-gi) (1 - r) to first order. A scale that is a
         // power of two leaves none. (e may be infinite: the factor keeps it so.)
         const float e = expf(-gi);
-        const float s = 1.0f / (1.0f + (kMx ? e : e * (1.0f - fmaf(g[i], sg, -gi))));
+        const float s = sigmoid_of(kMx ? e : e * (1.0f - fmaf(g[i], sg, -gi)));
         const float silu = gi * s, h = silu * ui, wd = w * d[i];
         dot = fmaf(d[i], h, dot);
         dg[i] = wd * ui * fmaf(silu, 1.0f - s, s);
@@ -205,29 +222,40 @@ __global__ void __launch_bounds__(256) silu_backward_kernel(
   }
 }
 
-static int grid_for(int64_t blocks) {
-  const int64_t cap = (int64_t)sm_count() * 32;
-  if (blocks > cap) blocks = cap;
-  return (int)(blocks < 1 ? 1 : blocks);
+// One CTA per rows' worth of threads (a few rows at most each), so that the loads of rows waiting
+// for a place on an SM overlap the arithmetic of others.
+static int grid_for(int64_t rows, int tpr) {
+  const int64_t blocks = cdiv(rows, 256 / tpr), cap = 1 << 20;
+  return (int)(blocks < cap ? blocks : cap);
+}
+
+// as many threads per row as it has runs of 8 columns, so that a thread makes few passes
+template <typename F>
+static cudaError_t with_threads_per_row(int64_t inter, F f) {
+  if (inter <= 256) return f(std::integral_constant<int, 32>{});
+  if (inter <= 1024) return f(std::integral_constant<int, 128>{});
+  return f(std::integral_constant<int, 256>{});
 }
 
 }  // namespace act_train
 
 cudaError_t launch_silu_save(const SiluSaveArgs& a, cudaStream_t st) {
   using namespace act_train;
-  const int grid = grid_for(cdiv(a.rows * cdiv(a.inter, kGroup), 16));
   return with_elem(a.gu_dtype, [&](auto in) {
     return with_elem(a.h_dtype, [&](auto out) {
-      using In = decltype(in);
-      using Out = decltype(out);
-      // the up half begins at column inter: it has to keep the vectors' alignment
-      const bool vg = elem_vec_ok(a.gu, a.ld_gu, sizeof(typename In::T)) && a.inter % 8 == 0;
-      const bool vh = elem_vec_ok(a.h, a.ld_h, sizeof(typename Out::T));
-      const bool vq = (uintptr_t)a.q % 8 == 0 && a.inter % 8 == 0;
-      auto k = a.mx ? silu_save_kernel<In, Out, true> : silu_save_kernel<In, Out, false>;
-      return launch_kernel(k, dim3(grid), dim3(256), 0, st, false, static_cast<const typename In::T*>(a.gu), a.rows,
-                           a.inter, a.ld_gu, a.rows_dev, static_cast<typename Out::T*>(a.h), a.ld_h, a.q, a.scales, vg,
-                           vh, vq);
+      return with_threads_per_row(a.inter, [&](auto t) {
+        using In = decltype(in);
+        using Out = decltype(out);
+        constexpr int kTpr = decltype(t)::value;
+        // the up half begins at column inter: it has to keep the vectors' alignment
+        const bool vg = elem_vec_ok(a.gu, a.ld_gu, sizeof(typename In::T)) && a.inter % 8 == 0;
+        const bool vh = elem_vec_ok(a.h, a.ld_h, sizeof(typename Out::T));
+        const bool vq = (uintptr_t)a.q % 8 == 0 && a.inter % 8 == 0;
+        auto k = a.mx ? silu_save_kernel<In, Out, true, kTpr> : silu_save_kernel<In, Out, false, kTpr>;
+        return launch_kernel(k, dim3(grid_for(a.rows, kTpr)), dim3(256), 0, st, false,
+                             static_cast<const typename In::T*>(a.gu), a.rows, a.inter, a.ld_gu, a.rows_dev,
+                             static_cast<typename Out::T*>(a.h), a.ld_h, a.q, a.scales, vg, vh, vq);
+      });
     });
   });
 }
@@ -241,17 +269,13 @@ cudaError_t launch_silu_backward(const SiluBackwardArgs& a, cudaStream_t st) {
     const bool vd = elem_vec_ok(a.dh, a.ld_dh, sizeof(T));
     const bool vgu = elem_vec_ok(a.dgu, a.ld_dgu, sizeof(T)) && a.inter % 8 == 0;
     const bool vhw = a.hw == nullptr || elem_vec_ok(a.hw, a.ld_hw, sizeof(T));
-    auto go = [&](auto kernel, int tpr) {
-      return launch_kernel(kernel, dim3(grid_for(cdiv(a.rows, 256 / tpr))), dim3(256), 0, st, false, a.q, a.scales,
-                           a.rows, a.inter, a.rows_dev, static_cast<const T*>(a.dh), a.ld_dh, a.row_weights,
-                           static_cast<T*>(a.dgu), a.ld_dgu, static_cast<T*>(a.hw), a.ld_hw, a.dweights, vq, vd, vgu,
-                           vhw);
-    };
-    // as many threads per row as it has runs of 8 columns, so that a thread makes few passes
-    if (a.inter <= 256) return a.mx ? go(silu_backward_kernel<E, true, 32>, 32) : go(silu_backward_kernel<E, false, 32>, 32);
-    if (a.inter <= 1024)
-      return a.mx ? go(silu_backward_kernel<E, true, 128>, 128) : go(silu_backward_kernel<E, false, 128>, 128);
-    return a.mx ? go(silu_backward_kernel<E, true, 256>, 256) : go(silu_backward_kernel<E, false, 256>, 256);
+    return with_threads_per_row(a.inter, [&](auto t) {
+      constexpr int kTpr = decltype(t)::value;
+      auto k = a.mx ? silu_backward_kernel<E, true, kTpr> : silu_backward_kernel<E, false, kTpr>;
+      return launch_kernel(k, dim3(grid_for(a.rows, kTpr)), dim3(256), 0, st, false, a.q, a.scales, a.rows, a.inter,
+                           a.rows_dev, static_cast<const T*>(a.dh), a.ld_dh, a.row_weights, static_cast<T*>(a.dgu),
+                           a.ld_dgu, static_cast<T*>(a.hw), a.ld_hw, a.dweights, vq, vd, vgu, vhw);
+    });
   });
 }
 
