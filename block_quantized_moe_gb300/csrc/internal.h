@@ -316,6 +316,9 @@ struct Matmul16Args {
 };
 cudaError_t launch_matmul16(const Matmul16Args& a, cudaStream_t s);  // picks the kernel
 cudaError_t launch_matmul16_general(const Matmul16Args& a, cudaStream_t s);
+// stream_matmul16.cu: the product for a handful of rows
+bool stream_matmul16_ok(const Matmul16Args& a);
+cudaError_t launch_stream_matmul16(const Matmul16Args& a, cudaStream_t s);
 // tc_matmul16.cu: the tcgen05 kernel; *unsupported where TMA cannot read the operands
 cudaError_t launch_tc_matmul16(const Matmul16Args& a, cudaStream_t s, int* unsupported);
 uint32_t read_err_tc_matmul16();

@@ -162,7 +162,18 @@ cudaError_t launch_matmul16_general(const Matmul16Args& a, cudaStream_t st) {
   return mm16::run(p, a.dtype, a.out_dtype, false, (cdiv(a.rows, 64) + w.num_experts) * cdiv(p.n, 64), st);
 }
 
+// The streaming kernel where the tensor-core kernel would have at most 38 units of 256 weight
+// rows, half of what fills the GPU. Measured on GB300 (streaming, tensor cores, microseconds):
+// two rows over two experts, 1536 x 2048 (12 units) 5.5, 12.9; one row, 4096 x 7168 (16 units)
+// 19, 33; from there on the units suffice: eight rows over eight experts, 1536 x 2048 (48) 14.3,
+// 14.4; over eight experts, 2048 x 4096 (64) 33, 30; four rows of one expert, 4096 x 7168 46, 33.
+static bool prefer_stream(const Matmul16Args& a) {
+  const int64_t hit = a.rows < a.w.num_experts ? a.rows : a.w.num_experts;
+  return a.rows <= 16 && hit * cdiv(a.w.n, 256) <= 38 && stream_matmul16_ok(a);
+}
+
 cudaError_t launch_matmul16(const Matmul16Args& a, cudaStream_t st) {
+  if (prefer_stream(a)) return launch_stream_matmul16(a, st);
   int unsupported = 0;
   const cudaError_t e = launch_tc_matmul16(a, st, &unsupported);
   return unsupported ? launch_matmul16_general(a, st) : e;

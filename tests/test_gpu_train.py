@@ -99,6 +99,22 @@ def test_product(counts, n, k, dtype, out, input_grad):
     assert ft.ftmoe_read_error_flags() == 0
 
 
+@pytest.mark.parametrize("counts", [[1], [1, 0, 1], [0, 0, 4], [5, 0, 0], [0] * 300 + [1, 0, 2] + [0] * 250, [16]])
+@pytest.mark.parametrize("n,k", [(8, 8), (24, 2056), (264, 768), (1000, 4104)])
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("fp16", "fp32"), ("bf16", "fp16")])
+def test_product_of_a_handful_of_rows(counts, n, k, dtype, out):
+    """Decode sizes: rows of one expert and of several, experts without rows around them, weight
+    rows that end inside a lane's pieces; rows past the last segment are not written."""
+    R, E = sum(counts), len(counts)
+    a = normal((R + 1, k), 1.0, DT[dtype], 61)
+    w = normal((E, n, k), 0.1, DT[dtype], 62)
+    o = torch.full((R + 1, n), float("nan"), dtype=DT[out], device=DEV)
+    ft.ftmoe_grouped_matmul(a, offsets_of(counts), w, o)
+    ref, mag = product_ref(a[:R], w, counts, False)
+    check(o[:R], ref, mag, k, "product")
+    assert torch.isnan(o[R]).all()
+
+
 @pytest.mark.parametrize("pad,shift", [(8, 0), (8, 8), (3, 0), (1, 5), (64, 24)])
 @pytest.mark.parametrize("input_grad", [False, True])
 def test_product_strides_and_rows_past_the_end(pad, shift, input_grad):
