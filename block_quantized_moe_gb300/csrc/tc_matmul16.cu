@@ -30,6 +30,14 @@
 // From saved rows (MXFP8), A arrives as codes; eight warps decode them into the operand tile,
 // a 32-wide group with its power-of-two scale at a time, exactly.
 //
+// Long sums. The tensor core cuts low bits off as it adds a product to its fp32 accumulator: the
+// error is a bias that grows with the number of additions (measured: 4.4e-6 of the result's norm
+// over 4,096 terms, where fp32 sums rounded to nearest have 6e-7). A 16-bit output hides that, an
+// fp32 output does not. For fp32 outputs an accumulator takes 8 stages (512 terms) and the
+// epilogue adds the accumulators up in registers, 128 per thread, the control warps giving up
+// theirs; from saved rows, whose decoding warps need the registers, it takes 32 stages and the
+// parts are added in memory by TMA.
+//
 // Roles: warp 0 TMA, warp 1 MMA issue and TMEM, warp 2 segment tails (weight grad) or codes
 // (saved rows), warps 4-11 epilogue, warps 12-19 decode (saved rows). Every mbarrier wait is bounded: on timeout the
 // kernel raises FTMOE_ERR_WAIT_TIMEOUT, stops its roles, waits for its own loads and MMAs,
@@ -79,6 +87,7 @@ struct Params {
   int c_dim;                 // weight grad: extent of c
   int E, out_dtype, bf16, accumulate;
   int tma_out;               // whether map_o describes the output
+  int chunk;                 // stages that one accumulator adds up (see "Long sums")
 };
 
 // One MMA of the pair, issued by one lane of a converged warp: with the whole warp in the issue
@@ -243,18 +252,27 @@ __device__ __forceinline__ void store_columns(typename Elem::T* out, int64_t ld,
     }
   } else if (m < m_dim) {
     T* o = out + m;
-    float old[32];
-    if (accumulate) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) old[j] = j < cols ? Elem::get(o[j * ld]) : 0.0f;
+    for (int j0 = 0; j0 < 32; j0 += 8) {
+      float old[8] = {};
+      if (accumulate) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) old[j] = j0 + j < cols ? Elem::get(o[(j0 + j) * ld]) : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j0 + j < cols) o[(j0 + j) * ld] = Elem::put(accumulate ? old[j] + d[j0 + j] : d[j0 + j]);
     }
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j < cols) o[j * ld] = Elem::put(accumulate ? old[j] + d[j] : d[j]);
   }
 }
 
-template <int MODE>
+// Registers with kSum: 384 threads launch with 168 each; the control warpgroup keeps 80, the two
+// epilogue warpgroups take 208.
+constexpr int kCtlRegs = 80, kSumRegs = 208;
+constexpr int kSumRegsNeeded = 128 * kCtlRegs + 256 * kSumRegs;
+constexpr int kSumStages = 8, kAddStages = 32, kNoChunk = 0x3fffffff;
+
+template <int MODE, bool kSum>
 __global__ void __launch_bounds__(threads(MODE), 1)
     tc_matmul16_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b0,
                        const __grid_constant__ CUtensorMap map_b1, const __grid_constant__ CUtensorMap map_b2,
@@ -370,6 +388,8 @@ __global__ void __launch_bounds__(threads(MODE), 1)
     t.n = (t.cols + 31) & ~31;
   };
 
+  if (warp < 4) {
+  if constexpr (kSum) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtlRegs));
   if (warp == 0) {
     // ------------------------------- TMA producer -------------------------------
     if (lane == 0) {
@@ -449,14 +469,16 @@ __global__ void __launch_bounds__(threads(MODE), 1)
         const uint32_t idesc = (1u << 4) | ((uint32_t)p.bf16 << 7) | ((uint32_t)p.bf16 << 10) |
                                (MODE == kProduct ? 0u : 1u << 15) | (kWG ? 1u << 16 : 0u) |
                                ((uint32_t)(t.n >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);
-        const int buf = (int)(acc & 1);
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&tempty[buf]), ((acc >> 1) & 1) ^ 1, &s_abort))) break;
-        fence_after();
-        const uint32_t d = tmem_base + buf * kN;
         const int steps = (t.len + kBK - 1) / kBK;
         bool ok = true;
-        for (int s = 0; s < steps; ++s, ++it) {
+        uint32_t d = 0;
+        for (int s = 0, part = 0; s < steps; ++s, ++it) {
           const int st = it % S;
+          if (part == 0) {  // a free accumulator
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&tempty[acc & 1]), ((acc >> 1) & 1) ^ 1, &s_abort));
+            if (!ok) break;
+            d = tmem_base + (acc & 1) * kN;
+          }
           ok = kWG ? wait_cluster(smem_u32(&full[st]), (it / S) & 1, &s_abort)
                    : mbar_wait(smem_u32(&full[st]), (it / S) & 1, &s_abort);
           ok = __all_sync(0xffffffffu, ok);
@@ -469,7 +491,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
           const int left = t.len - s * kBK;
 #pragma unroll
           for (int j = 0; j < kBK / 16; ++j) {
-            const uint32_t acc_on = s > 0 || j > 0 ? 1u : 0u;
+            const uint32_t acc_on = part > 0 || j > 0 ? 1u : 0u;
             if constexpr (kWG)
               mma_f16_pair_if(d, smem_desc_mn_sw128(ta + 2048 * j), smem_desc_mn_sw128(tb + 2048 * j), idesc, acc_on,
                               16 * j < left);
@@ -478,10 +500,13 @@ __global__ void __launch_bounds__(threads(MODE), 1)
                            smem_desc_sw128(tb + 32 * j), idesc, acc_on);
           }
           commit_pair_elected(smem_u32(&empty[st]));
+          if (++part == p.chunk || s == steps - 1) {
+            commit_pair_elected(smem_u32(&tfull[acc & 1]));
+            ++acc;
+            part = 0;
+          }
         }
         if (!ok) break;
-        commit_pair_elected(smem_u32(&tfull[buf]));
-        ++acc;
       }
       // MMAs still running write TMEM: wait (bounded) for the last commit of each accumulator
       for (uint32_t b = 0; b < 2 && b < acc; ++b) {
@@ -536,8 +561,10 @@ __global__ void __launch_bounds__(threads(MODE), 1)
         }
       }
     }
-  } else if (warp >= 4 && warp < 4 + kEpiWarps) {
+  }
+  } else if (warp < 4 + kEpiWarps) {
     // --------------------------------- epilogue ---------------------------------
+    if constexpr (kSum) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
     // Two groups of four warps take chunks of 32 columns in turn. A chunk goes through shared
     // memory and leaves as TMA boxes of 128 m by 32 c (16 of fp32), 256 or 512 contiguous bytes
     // a row. (Stored from registers, 64 bytes a row and warp, the weight gradient of 64 experts
@@ -545,51 +572,29 @@ __global__ void __launch_bounds__(threads(MODE), 1)
     // an expert's rows, an unaligned output and a 16-bit accumulation are stored from registers.
     const int ew = warp - 4, quarter = warp & 3, half = ew >> 2;
     const bool leader = quarter == 0 && lane == 0;
-    uint32_t acc = 0, box = 0;  // units, output boxes so far
+    uint32_t acc = 0, box = 0;  // accumulators, output boxes so far
     const bool words = p.ld_out % 2 == 0 && p.out_expert % 2 == 0 && reinterpret_cast<uintptr_t>(p.out) % 4 == 0;
+    const bool f32 = kSum || p.out_dtype == FTMOE_OUT_FP32;
     const bool tma_out = p.tma_out && (!p.accumulate || p.out_dtype == FTMOE_OUT_FP32);
     for (int u = u_begin; u < u_end; u += u_step) {
       Unit t;
       decode(u, t);
       const bool none = kWG && t.len == 0;  // an expert without rows: zeros, or nothing to add
       if (none && p.accumulate) continue;
-      const int buf = (int)(acc & 1);
-      if (!none) {
-        const int got = mbar_wait(smem_u32(&tfull[buf]), (acc >> 1) & 1, &s_abort) ? 1 : 0;
-        // the group's warps share barriers below: they leave together
-        if (named_bar_or(1 + half, 128, got == 0)) break;
-        fence_after();
-        ++acc;
-      }
-      const uint32_t taddr = tmem_base + ((uint32_t)(32 * quarter) << 16) + buf * kN;
       const int mc = t.m0 + (int)crank * 128, ml = 32 * quarter + lane, m = mc + ml;
       const int64_t first = (int64_t)t.e * p.out_expert + (int64_t)t.c0 * p.ld_out;
-      bool held = !none;
-      for (int c = 32 * half; c < t.cols; c += 64) {
-        float d[32];
-        if (none) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) d[j] = 0.0f;
-        } else {
-          tmem_ld<32>(taddr + c, d);
-          tmem_ld_wait();
-          if (c + 64 >= t.cols) {  // this warp's last read: the accumulator goes back to the MMAs
-            fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[buf]), 0));
-            held = false;
-          }
-        }
+      // 32 columns from c on, added to what memory holds or in place of it
+      auto emit = [&](int c, const float (&d)[32], bool add) {
         const int cols = t.cols - c;
         if (tma_out && (kWG || cols >= 32)) {  // (a weight gradient's edge is clipped by its tensor map)
-          const int per = p.out_dtype == FTMOE_OUT_FP32 ? 16 : 32;
+          const int per = f32 ? 16 : 32;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (h == 1 && per == 32) break;
             // free: the barrier of the box before this one followed the leader's wait for the
             // store that last used this buffer
             uint8_t* ob = outbuf + (kOutBufs * half + box % kOutBufs) * kOutBuf;
-            if (p.out_dtype == FTMOE_OUT_FP32) {
+            if (f32) {
 #pragma unroll
               for (int j = 0; j < 16; ++j) reinterpret_cast<float*>(ob)[j * 128 + ml] = d[16 * h + j];
             } else if (p.out_dtype == FTMOE_OUT_BF16) {
@@ -614,7 +619,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
             if (leader) {
               const int y = t.c0 + c + 16 * h;
               if (mc < p.m_dim && (!kWG || y < p.c_dim)) {
-                if (p.accumulate)
+                if (add)
                   tma_add_3d(&map_o, smem_u32(ob), mc, y, kWG ? t.e : 0);
                 else
                   tma_store_3d(&map_o, smem_u32(ob), mc, y, kWG ? t.e : 0);
@@ -625,22 +630,91 @@ __global__ void __launch_bounds__(threads(MODE), 1)
           }
         } else {
           const int64_t o = first + (int64_t)c * p.ld_out;
-          if (p.out_dtype == FTMOE_OUT_FP32)
-            store_columns<ElemF32>(static_cast<float*>(p.out) + o, p.ld_out, d, cols, m, p.m_dim, lane, words, p.accumulate);
+          if (f32)
+            store_columns<ElemF32>(static_cast<float*>(p.out) + o, p.ld_out, d, cols, m, p.m_dim, lane, words, add);
           else if (p.out_dtype == FTMOE_OUT_BF16)
-            store_columns<ElemBf16>(static_cast<uint16_t*>(p.out) + o, p.ld_out, d, cols, m, p.m_dim, lane, words, p.accumulate);
+            store_columns<ElemBf16>(static_cast<uint16_t*>(p.out) + o, p.ld_out, d, cols, m, p.m_dim, lane, words, add);
           else
-            store_columns<ElemF16>(static_cast<uint16_t*>(p.out) + o, p.ld_out, d, cols, m, p.m_dim, lane, words, p.accumulate);
+            store_columns<ElemF16>(static_cast<uint16_t*>(p.out) + o, p.ld_out, d, cols, m, p.m_dim, lane, words, add);
         }
-      }
-      if (held) {  // no column of this unit was this warp's
+      };
+      auto wait_acc = [&]() {
+        const int got = mbar_wait(smem_u32(&tfull[acc & 1]), (acc >> 1) & 1, &s_abort) ? 1 : 0;
+        // the group's warps share barriers in emit: they leave together
+        const bool left = named_bar_or(1 + half, 128, got == 0);
+        fence_after();
+        return !left;
+      };
+      auto release_acc = [&]() {  // this warp's last read of the accumulator: it goes back to the MMAs
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[buf]), 0));
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc & 1]), 0));
+      };
+      const uint32_t lanes = tmem_base + ((uint32_t)(32 * quarter) << 16);
+      const int parts = none ? 1 : ((t.len + kBK - 1) / kBK + p.chunk - 1) / p.chunk;
+      if constexpr (kSum) {
+        float sum[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sum[i][j] = 0.0f;
+        bool ok = true;
+        for (int q = 0; q < parts && !none; ++q, ++acc) {
+          ok = wait_acc();
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = 32 * half + 64 * i;
+            if (c < t.cols) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float d[16];
+                tmem_ld<16>(lanes + (acc & 1) * kN + c + 16 * h, d);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) sum[i][16 * h + j] += d[j];
+              }
+            }
+          }
+          release_acc();
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (32 * half + 64 * i < t.cols) emit(32 * half + 64 * i, sum[i], p.accumulate != 0);
+      } else {
+        bool ok = true;
+        for (int q = 0; q < parts; ++q) {
+          if (!none) {
+            ok = wait_acc();
+            if (!ok) break;
+          }
+          // a part is added to what the parts before it have left in memory
+          if (q > 0 && leader) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+          bool held = !none;
+          for (int c = 32 * half; c < t.cols; c += 64) {
+            float d[32];
+            if (none) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) d[j] = 0.0f;
+            } else {
+              tmem_ld<32>(lanes + (acc & 1) * kN + c, d);
+              tmem_ld_wait();
+              if (c + 64 >= t.cols) {
+                release_acc();
+                held = false;
+              }
+            }
+            emit(c, d, p.accumulate != 0 || q > 0);
+          }
+          if (held) release_acc();  // no column of this unit was this warp's
+          if (!none) ++acc;
+        }
+        if (!ok) break;
       }
     }
     if (leader) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-  } else if (kSaved && warp >= 4 + kEpiWarps) {
+  } else if constexpr (kSaved) {
     // ------------------------ saved rows: decode ------------------------
     // Four teams of two warps take stages in turn, so that some decode while others wait for
     // codes, for a free operand slot or for their stores to be visible. Thread (warp dw of the
@@ -787,7 +861,7 @@ static bool encode_out(CUtensorMap* map, void* base, int32_t dtype, uint64_t m, 
                 CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-template <int MODE>
+template <int MODE, bool kSum>
 static cudaError_t launch(const CUtensorMap* maps, const Params& p, cudaStream_t st, int* unsupported) {
   const size_t smem = 1024 + (size_t)smem_bytes(MODE) + (is_wgrad(MODE) ? 0 : ((size_t)p.E + 1) * 4);
   int dev = 0;
@@ -799,17 +873,24 @@ static cudaError_t launch(const CUtensorMap* maps, const Params& p, cudaStream_t
   if (np == 0) {
     const size_t most = 1024 + (size_t)smem_bytes(MODE) + (is_wgrad(MODE) ? 0 : (kMaxExperts + 1) * 4);
     const cudaError_t e =
-        cudaFuncSetAttribute(tc_matmul16_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+        cudaFuncSetAttribute(tc_matmul16_kernel<MODE, kSum>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (e != cudaSuccess) return e;
-    np = max_active_clusters(tc_matmul16_kernel<MODE>, dim3(threads(MODE)), most, 2, 2 * (sm_count() / 2));
+    np = max_active_clusters(tc_matmul16_kernel<MODE, kSum>, dim3(threads(MODE)), most, 2, 2 * (sm_count() / 2));
     if (np > sm_count() / 2) np = sm_count() / 2;
+    if constexpr (kSum) {
+      // the register split has to fit what the block is launched with
+      cudaFuncAttributes fa;
+      const cudaError_t ea = cudaFuncGetAttributes(&fa, tc_matmul16_kernel<MODE, kSum>);
+      if (ea != cudaSuccess) return ea;
+      if (fa.numRegs * threads(MODE) < kSumRegsNeeded) np = 0;
+    }
     if (dev >= 0 && dev < 64) pairs[dev] = np;
   }
   if (np < 1) {
     *unsupported = 1;
     return cudaSuccess;
   }
-  return launch_kernel_cluster(tc_matmul16_kernel<MODE>, dim3(2 * np), dim3(threads(MODE)), smem, st, false, 2, maps[0],
+  return launch_kernel_cluster(tc_matmul16_kernel<MODE, kSum>, dim3(2 * np), dim3(threads(MODE)), smem, st, false, 2, maps[0],
                                maps[1], maps[2], maps[3], maps[4], maps[5], p);
 }
 
@@ -854,7 +935,12 @@ cudaError_t launch_tc_matmul16(const Matmul16Args& a, cudaStream_t st, int* unsu
     p.tma_out = encode_out(&maps[5], a.out, a.out_dtype, (uint64_t)m, R, 1, a.ld_out, 0);
     if (!p.tma_out) maps[5] = maps[0];
     *unsupported = 0;
-    return a.input_grad ? launch<kInputGrad>(maps, p, st, unsupported) : launch<kProduct>(maps, p, st, unsupported);
+    p.chunk = kNoChunk;
+    if (a.out_dtype == FTMOE_OUT_FP32 && l > kSumStages * kBK) {
+      p.chunk = kSumStages;
+      return a.input_grad ? launch<kInputGrad, true>(maps, p, st, unsupported) : launch<kProduct, true>(maps, p, st, unsupported);
+    }
+    return a.input_grad ? launch<kInputGrad, false>(maps, p, st, unsupported) : launch<kProduct, false>(maps, p, st, unsupported);
   }
   if (!tma16(a.a, a.ld_a) || E * cdiv(w.k, kM) * cdiv(w.n, kN) > 0x7fffffff) return cudaSuccess;
   const uint64_t dd[2] = {(uint64_t)w.n, R}, ds[1] = {2 * (uint64_t)a.ld_a};
@@ -883,7 +969,18 @@ cudaError_t launch_tc_matmul16(const Matmul16Args& a, cudaStream_t st, int* unsu
   p.tma_out = encode_out(&maps[5], w.w, w.dtype, (uint64_t)w.k, (uint64_t)w.n, (uint64_t)E, w.ld, w.expert_stride);
   if (!p.tma_out) maps[5] = maps[0];
   *unsupported = 0;
-  return a.x_scales ? launch<kWeightGradSaved>(maps, p, st, unsupported) : launch<kWeightGrad>(maps, p, st, unsupported);
+  // (the longest segment is known on the device only: at most all rows)
+  const bool f32 = w.dtype == FTMOE_OUT_FP32;
+  p.chunk = kNoChunk;
+  if (a.x_scales) {
+    if (f32) p.chunk = kAddStages;
+    return launch<kWeightGradSaved, false>(maps, p, st, unsupported);
+  }
+  if (f32 && a.rows > kSumStages * kBK) {
+    p.chunk = kSumStages;
+    return launch<kWeightGrad, true>(maps, p, st, unsupported);
+  }
+  return launch<kWeightGrad, false>(maps, p, st, unsupported);
 }
 
 FTMOE_DEFINE_ERR_READER(read_err_tc_matmul16)

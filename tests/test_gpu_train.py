@@ -285,6 +285,40 @@ def test_weight_gradient_strides(pad, shift):
     assert int((~torch.isnan(base)).sum()) == E * n * k
 
 
+@pytest.mark.parametrize("kind", ["product", "input_grad", "weight_grad", "saved"])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_long_sums_keep_fp32(kind, accumulate):
+    """fp32 outputs of long contractions. An accumulator takes 512 terms in 32 additions (2,048 in
+    128 from saved rows), each losing at most 2^-23 of the partial sum, and the partial sums are
+    of the result's size (independent terms): the error's norm is below 32 (128) 2^-23 of it."""
+    if accumulate and kind in ("product", "input_grad"):
+        pytest.skip("only weight gradients accumulate")
+    counts, long, m = [1, 9000, 300], 16384, 136
+    off = offsets_of(counts)
+    if kind in ("product", "input_grad"):
+        counts = [70, 0, 40]
+        n, k = (m, long) if kind == "product" else (long, m)
+        a, w = normal((110, long), 1.0, torch.bfloat16, 63), normal((3, n, k), 0.1, torch.bfloat16, 64)
+        got = torch.empty(110, m, device=DEV)
+        ft.ftmoe_grouped_matmul(a, offsets_of(counts), w, got, input_grad=kind == "input_grad")
+        ref, mag = product_ref(a, w, counts, kind == "input_grad")
+    else:
+        R = sum(counts)
+        dy, x = normal((R, m), 0.5, torch.bfloat16, 65), normal((R, 160), 1.0, torch.bfloat16, 66)
+        got = normal((3, m, 160), 1.0, torch.float32, 67)
+        old = got.double() if accumulate else 0.0
+        if kind == "saved":
+            q, s, x = saved(x)
+            ft.ftmoe_grouped_matmul_wgrad_saved(dy, q, s, off, got, accumulate=accumulate)
+        else:
+            ft.ftmoe_grouped_matmul_wgrad(dy, x, off, got, accumulate=accumulate)
+        ref, mag = wgrad_ref(dy, x, counts)
+        ref = ref + old
+    check(got, ref, mag + ref.abs(), long, kind)
+    rel = float((got.double() - ref).norm() / ref.norm())
+    assert rel <= (128 if kind == "saved" else 32) * 2.0 ** -23, rel
+
+
 def test_gradients_agree_with_differences():
     """L = <c, product>: L's change along random directions of a and w against the two gradients
     (the product is linear in each, so the difference is exact up to rounding)."""
