@@ -90,34 +90,56 @@ struct Params {
   int chunk;                 // stages that one accumulator adds up (see "Long sums")
 };
 
-// One MMA of the pair, issued by one lane of a converged warp: with the whole warp in the issue
-// loop the descriptors stay in uniform registers. (A loop run by lane 0 alone moved each of them
-// over for every MMA: measured on GB300, 830 clocks a stage of four MMAs, with no loads at all,
-// against the 512 that the tensor cores take.)
-__device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
-      " @q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
+// A stage's four MMAs (16 of l each) and the commit that frees its slot, issued by the lane with
+// lead != 0 of a converged warp: with the whole warp in the issue loop the descriptors stay in
+// uniform registers, and with predicates instead of branches nothing stands between the MMAs.
+// (The loop is what bounds the kernel where it is longer than the MMAs it issues. Measured on
+// GB300 without any loads, clocks a stage: run by lane 0 alone, which moves every descriptor
+// over, 830; whole warp, a branch in front of each MMA, 900; predicates, 590; this form is what
+// is in use.) acc: whether the first MMA adds to the accumulator; left: rows of l that count, the
+// MMAs past them are off (kTail).
+template <bool kTail>
+__device__ __forceinline__ void mma_stage(uint32_t d, const uint64_t (&a)[4], const uint64_t (&b)[4], uint32_t idesc,
+                                          uint32_t acc, int left, uint32_t lead, uint32_t empty_bar) {
+  if constexpr (kTail) {
+    asm volatile(
+        "{\n .reg .pred p, q, q1, q2, q3;\n setp.ne.b32 p, %10, 0;\n setp.ne.b32 q, %12, 0;\n"
+        " setp.gt.and.s32 q1, %11, 16, q;\n setp.gt.and.s32 q2, %11, 32, q;\n setp.gt.and.s32 q3, %11, 48, q;\n"
+        " @q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %5, %9, p;\n"
+        " setp.eq.b32 p, 0, 0;\n"
+        " @q1 tcgen05.mma.cta_group::2.kind::f16 [%0], %2, %6, %9, p;\n"
+        " @q2 tcgen05.mma.cta_group::2.kind::f16 [%0], %3, %7, %9, p;\n"
+        " @q3 tcgen05.mma.cta_group::2.kind::f16 [%0], %4, %8, %9, p;\n"
+        " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%13], %14;\n}" ::"r"(d),
+        "l"(a[0]), "l"(a[1]), "l"(a[2]), "l"(a[3]), "l"(b[0]), "l"(b[1]), "l"(b[2]), "l"(b[3]), "r"(idesc), "r"(acc),
+        "r"(left), "r"(lead), "r"(empty_bar), "h"((uint16_t)0x3)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %10, 0;\n setp.ne.b32 q, %11, 0;\n"
+        " @q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %5, %9, p;\n"
+        " setp.eq.b32 p, 0, 0;\n"
+        " @q tcgen05.mma.cta_group::2.kind::f16 [%0], %2, %6, %9, p;\n"
+        " @q tcgen05.mma.cta_group::2.kind::f16 [%0], %3, %7, %9, p;\n"
+        " @q tcgen05.mma.cta_group::2.kind::f16 [%0], %4, %8, %9, p;\n"
+        " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%12], %13;\n}" ::"r"(d),
+        "l"(a[0]), "l"(a[1]), "l"(a[2]), "l"(a[3]), "l"(b[0]), "l"(b[1]), "l"(b[2]), "l"(b[3]), "r"(idesc), "r"(acc),
+        "r"(lead), "r"(empty_bar), "h"((uint16_t)0x3)
+        : "memory");
+  }
 }
-// the same where `on`: a predicate, no branch
-__device__ __forceinline__ void mma_f16_pair_if(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc,
-                                                bool on) {
+__device__ __forceinline__ void commit_pair_lead(uint32_t bar, uint32_t lead) {
   asm volatile(
-      "{\n .reg .pred p, q, r;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 r, %5, 0;\n elect.sync _|q, 0xffffffff;\n"
-      " and.pred q, q, r;\n @q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"((uint32_t)on)
-      : "memory");
-}
-// mma_commit_pair by the lane that issued the MMAs (elect.sync names the same one each time)
-__device__ __forceinline__ void commit_pair_elected(uint32_t bar) {
-  asm volatile(
-      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      "{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n"
       " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}" ::"r"(
           bar),
-      "h"((uint16_t)0x3)
+      "h"((uint16_t)0x3), "r"(lead)
       : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}" : "=r"(r));
+  return r;
 }
 
 // Operand tile whose m (or c) axis is contiguous: 64-element columns of 128-byte lines, one line
@@ -461,52 +483,51 @@ __global__ void __launch_bounds__(threads(MODE), 1)
     // -------------------------------- MMA issuer --------------------------------
     // (the whole warp runs the loop, one elected lane issues)
     if (crank == 0) {
-      uint32_t it = 0, acc = 0;
-      for (int u = u_begin; u < u_end; u += u_step) {
+      const uint32_t lead = elect_one();
+      uint32_t acc = 0, st = 0, ph = 0;  // accumulators so far; the ring's slot and its phase
+      // low words of the operands' descriptors for slot 0; a slot and 16 of l further on
+      const uint64_t a0 = MODE == kProduct ? smem_desc_sw128(smem_u32(tiles)) : smem_desc_mn_sw128(smem_u32(tiles));
+      const uint64_t b0 = kWG ? smem_desc_mn_sw128(smem_u32(tiles) + kTile) : smem_desc_sw128(smem_u32(tiles) + kTile);
+      constexpr uint32_t kSlot = kStage >> 4, kStepA = (MODE == kProduct ? 32 : 2048) >> 4, kStepB = (kWG ? 2048 : 32) >> 4;
+      const uint32_t full0 = smem_u32(&full[0]), empty0 = smem_u32(&empty[0]);
+      bool ok = true;
+      for (int u = u_begin; u < u_end && ok; u += u_step) {
         Unit t;
         decode(u, t);
-        if (t.len == 0) continue;
         const uint32_t idesc = (1u << 4) | ((uint32_t)p.bf16 << 7) | ((uint32_t)p.bf16 << 10) |
                                (MODE == kProduct ? 0u : 1u << 15) | (kWG ? 1u << 16 : 0u) |
                                ((uint32_t)(t.n >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);
-        const int steps = (t.len + kBK - 1) / kBK;
-        bool ok = true;
+        int left = t.len, part = 0;
         uint32_t d = 0;
-        for (int s = 0, part = 0; s < steps; ++s, ++it) {
-          const int st = it % S;
+        while (left > 0) {
           if (part == 0) {  // a free accumulator
             ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&tempty[acc & 1]), ((acc >> 1) & 1) ^ 1, &s_abort));
             if (!ok) break;
             d = tmem_base + (acc & 1) * kN;
           }
-          ok = kWG ? wait_cluster(smem_u32(&full[st]), (it / S) & 1, &s_abort)
-                   : mbar_wait(smem_u32(&full[st]), (it / S) & 1, &s_abort);
+          const uint32_t bar = full0 + 8 * st;
+          ok = kWG ? wait_cluster(bar, ph, &s_abort) : mbar_wait(bar, ph, &s_abort);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           fence_after();
-          const uint32_t ta = smem_u32(tiles + (size_t)st * kStage), tb = ta + kTile;
-          // No branch between the MMAs of a stage: one in front of each took the stage from 512
-          // clocks to 900. Past l_dim TMA has filled in zeros; a segment's last stage turns off
-          // the MMAs past its rows by predicate.
-          const int left = t.len - s * kBK;
+          uint64_t da[4], db[4];
 #pragma unroll
-          for (int j = 0; j < kBK / 16; ++j) {
-            const uint32_t acc_on = part > 0 || j > 0 ? 1u : 0u;
-            if constexpr (kWG)
-              mma_f16_pair_if(d, smem_desc_mn_sw128(ta + 2048 * j), smem_desc_mn_sw128(tb + 2048 * j), idesc, acc_on,
-                              16 * j < left);
-            else
-              mma_f16_pair(d, MODE == kProduct ? smem_desc_sw128(ta + 32 * j) : smem_desc_mn_sw128(ta + 2048 * j),
-                           smem_desc_sw128(tb + 32 * j), idesc, acc_on);
+          for (int j = 0; j < 4; ++j) {
+            da[j] = a0 + st * kSlot + j * kStepA;
+            db[j] = b0 + st * kSlot + j * kStepB;
           }
-          commit_pair_elected(smem_u32(&empty[st]));
-          if (++part == p.chunk || s == steps - 1) {
-            commit_pair_elected(smem_u32(&tfull[acc & 1]));
+          mma_stage<kWG>(d, da, db, idesc, (uint32_t)part, left, lead, empty0 + 8 * st);
+          left -= kBK;
+          if (++st == S) {
+            st = 0;
+            ph ^= 1;
+          }
+          if (++part == p.chunk || left <= 0) {
+            commit_pair_lead(smem_u32(&tfull[acc & 1]), lead);
             ++acc;
             part = 0;
           }
         }
-        if (!ok) break;
       }
       // MMAs still running write TMEM: wait (bounded) for the last commit of each accumulator
       for (uint32_t b = 0; b < 2 && b < acc; ++b) {
