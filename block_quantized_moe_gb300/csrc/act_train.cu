@@ -36,6 +36,26 @@ __device__ __forceinline__ float sigmoid_of(float e) {
   return r;
 }
 
+// Pairs of fp32 values in one instruction (Blackwell's packed fp32 pipe): these kernels run at the
+// issue rate, and this halves their products and sums.
+struct Pair {
+  unsigned long long v;
+  __device__ __forceinline__ Pair() {}
+  __device__ __forceinline__ Pair(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
+  __device__ __forceinline__ explicit Pair(float both) : Pair(both, both) {}
+  __device__ __forceinline__ void get(float& lo, float& hi) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+};
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
 // Codes of 8 values that share a maximum with the lanes around them: 16 lanes (FP8's group of
 // 128) or 4 (MXFP8's 32). Every lane of the warp calls it. sc: the group's fp32 scale, or the
 // E8M0 byte.
@@ -54,15 +74,23 @@ __device__ __forceinline__ uint2 quantize8(const float (&v)[8], float& sc, uint8
     byte = (uint8_t)(shared + 127);
     const float f = __uint_as_float((uint32_t)(127 - shared) << 23);  // 2^-shared, exact
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = v[i] * f;
+    for (int i = 0; i < 8; i += 2) (Pair(v[i], v[i + 1]) * Pair(f)).get(q[i], q[i + 1]);
   } else {
     sc = m * (1.0f / kE4M3Max);
-    if (m > 0.0f) {
-      const SharedDivisor d(sc);  // v / sc as IEEE division rounds it
+    if (!(m > 0.0f)) return make_uint2(0u, 0u);
+    if (sc >= 0x1p-100f && sc <= 0x1p100f) {
+      // v / sc as IEEE division rounds it, by one reciprocal and Markstein's correction (see
+      // SharedDivisor). The residual is taken with the sign that leaves a zero quotient its own:
+      // q0 sc - v is +0 for v = -0, and q0 - (+0) y stays -0.
+      const Pair y(__fdiv_rn(1.0f, sc)), ny(-__fdiv_rn(1.0f, sc)), d(sc), minus(-1.0f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = d.div(v[i]);
+      for (int i = 0; i < 8; i += 2) {
+        const Pair x(v[i], v[i + 1]), q0 = x * y;
+        fma2(fma2(q0, d, x * minus), ny, q0).get(q[i], q[i + 1]);
+      }
     } else {
-      return make_uint2(0u, 0u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] = div_rn(v[i], sc);
     }
   }
   return make_uint2((uint32_t)f2_to_e4m3x2(q[0], q[1]) | ((uint32_t)f2_to_e4m3x2(q[2], q[3]) << 16),
@@ -102,7 +130,10 @@ __global__ void __launch_bounds__(256) silu_save_kernel(
       elem_load8<In>(gr + c0, vec_gu, n, g);
       elem_load8<In>(gr + inter + c0, vec_gu, n, u);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) a[i] = g[i] * sigmoid_of(expf(-g[i])) * u[i];
+      for (int i = 0; i < 8; i += 2) {
+        const Pair sg2(sigmoid_of(expf(-g[i])), sigmoid_of(expf(-g[i + 1])));
+        (Pair(g[i], g[i + 1]) * sg2 * Pair(u[i], u[i + 1])).get(a[i], a[i + 1]);
+      }
       float sg, su;
       uint8_t bg, bu;
       const uint2 cg = quantize8<kMx>(g, sg, bg), cu = quantize8<kMx>(u, su, bu);
@@ -147,7 +178,8 @@ __device__ __forceinline__ void load_codes(const uint8_t* q, bool vec, int n, fl
 }
 
 // kTpr threads per row, 8 columns each per pass; 256 / kTpr rows per CTA. dweights: a thread
-// adds its columns in ascending order, then a butterfly over the warp and the warps in order.
+// adds its even and its odd columns in ascending order, then both, a butterfly over the warp and
+// the warps in order.
 template <typename Elem, bool kMx, int kTpr>
 __global__ void __launch_bounds__(256) silu_backward_kernel(
     const uint8_t* __restrict__ q, const void* __restrict__ scales, int64_t rows, int64_t inter,
@@ -165,7 +197,7 @@ __global__ void __launch_bounds__(256) silu_backward_kernel(
   for (int64_t base = (int64_t)blockIdx.x * kRows; base < limit; base += (int64_t)gridDim.x * kRows, phase ^= 1) {
     const int64_t row = base + sub;
     const bool live = row < limit;
-    float dot = 0.0f;
+    Pair dot2(0.0f);  // columns of even and of odd index
     const float w = live && row_weights != nullptr ? row_weights[row] : 1.0f;
     for (int64_t c0 = (int64_t)tid * 8; live && c0 < inter; c0 += kTpr * 8) {
       const int64_t left = inter - c0;
@@ -184,25 +216,34 @@ __global__ void __launch_bounds__(256) silu_backward_kernel(
         su = s[nb];
       }
       float dg[8], du[8], hv[8];
+      const Pair w2(w), one(1.0f), minus(-1.0f), sg2(sg), su2(su);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float gi = g[i] * sg, ui = u[i] * su;
-        // the product's rounding error r (exact by FMA) would come back multiplied by |g| through
-        // the exponential: exp(-(gi + r)) = exp(-gi) (1 - r) to first order. A scale that is a
-        // power of two leaves none. (e may be infinite: the factor keeps it so.)
-        const float e = expf(-gi);
-        const float s = sigmoid_of(kMx ? e : e * (1.0f - fmaf(g[i], sg, -gi)));
-        const float silu = gi * s, h = silu * ui, wd = w * d[i];
-        dot = fmaf(d[i], h, dot);
-        dg[i] = wd * ui * fmaf(silu, 1.0f - s, s);
-        du[i] = wd * silu;
-        hv[i] = w * h;
+      for (int i = 0; i < 8; i += 2) {
+        const Pair gc(g[i], g[i + 1]), g2 = gc * sg2, u2 = Pair(u[i], u[i + 1]) * su2, d2(d[i], d[i + 1]);
+        float g_lo, g_hi;
+        g2.get(g_lo, g_hi);
+        Pair e(expf(-g_lo), expf(-g_hi));
+        // the rounding error r of code * scale (exact by FMA) would come back multiplied by |g|
+        // through the exponential: exp(-(g + r)) = exp(-g) (1 - r) to first order, and the factor
+        // leaves an infinite exp(-g) infinite. A scale that is a power of two leaves no r.
+        if constexpr (!kMx) e = e * fma2(fma2(gc, sg2, g2 * minus), minus, one);
+        float e_lo, e_hi;
+        e.get(e_lo, e_hi);
+        const Pair s(sigmoid_of(e_lo), sigmoid_of(e_hi));
+        const Pair silu = g2 * s, h = silu * u2, wd = w2 * d2;
+        dot2 = fma2(d2, h, dot2);
+        (wd * u2 * fma2(silu, fma2(s, minus, one), s)).get(dg[i], dg[i + 1]);
+        (wd * silu).get(du[i], du[i + 1]);
+        (w2 * h).get(hv[i], hv[i + 1]);
       }
       elem_store8<Elem>(dgu + row * ld_dgu + c0, vec_dgu, n, dg);
       elem_store8<Elem>(dgu + row * ld_dgu + inter + c0, vec_dgu, n, du);
       if (hw != nullptr) elem_store8<Elem>(hw + row * ld_hw + c0, vec_hw, n, hv);
     }
     if (dweights != nullptr) {
+      float dot, odd;
+      dot2.get(dot, odd);
+      dot += odd;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
       if constexpr (kWarps == 1) {

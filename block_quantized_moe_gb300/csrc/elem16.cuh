@@ -3,6 +3,8 @@
 // checked the alignment, else one by one up to a given count.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace ftmoe {
@@ -45,15 +47,24 @@ __device__ __forceinline__ void elem_load8(const typename Elem::T* p, bool vec, 
   }
 }
 
+// two values rounded to 16 bits, lo in the low half
+template <typename Elem>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r = 0;
+  if constexpr (std::is_same<Elem, ElemBf16>::value)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else if constexpr (std::is_same<Elem, ElemF16>::value)
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // the first n (at most 8) of v, each rounded once
 template <typename Elem>
 __device__ __forceinline__ void elem_store8(typename Elem::T* p, bool vec, int n, const float (&v)[8]) {
   if (vec && n >= 8) {
     if constexpr (sizeof(typename Elem::T) == 2) {
-      uint32_t w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = (uint32_t)Elem::put(v[2 * i]) | ((uint32_t)Elem::put(v[2 * i + 1]) << 16);
-      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(p) =
+          make_uint4(pack2<Elem>(v[0], v[1]), pack2<Elem>(v[2], v[3]), pack2<Elem>(v[4], v[5]), pack2<Elem>(v[6], v[7]));
     } else {
       *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
       *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);

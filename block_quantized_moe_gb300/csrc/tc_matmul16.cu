@@ -44,8 +44,6 @@
 // frees its TMEM and returns.
 #include <cuda.h>
 
-#include <type_traits>
-
 #include "common.cuh"
 #include "elem16.cuh"
 #include "internal.h"
@@ -222,19 +220,6 @@ struct Unit {
   int n;           // N of the MMA: cols rounded up to 32
   int l0, len;     // weight grad: first row of the segment and its length; else 0 and l_dim
 };
-
-// two values rounded to 16 bits, lo in the low half
-template <typename Elem>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t r;
-  if constexpr (sizeof(typename Elem::T) == 4)
-    r = 0;
-  else if constexpr (std::is_same<Elem, ElemBf16>::value)
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  else
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
