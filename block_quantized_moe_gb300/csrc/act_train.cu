@@ -27,15 +27,6 @@ __device__ __forceinline__ int64_t valid_rows(int64_t rows, const int32_t* rows_
   return d < 0 ? 0 : (d < rows ? d : rows);
 }
 
-// 1 / (1 + e) for e = exp(-g) >= 0 or infinite, to one unit in the last place (an IEEE division
-// costs about ten instructions, and these kernels run at the issue rate): silu and its slope are
-// rounded to 16 bits or carried at a few units of fp32 either way.
-__device__ __forceinline__ float sigmoid_of(float e) {
-  float r;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-  return r;
-}
-
 // Pairs of fp32 values in one instruction (Blackwell's packed fp32 pipe): these kernels run at the
 // issue rate, and this halves their products and sums.
 struct Pair {
@@ -54,6 +45,30 @@ __device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
   Pair r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
   return r;
+}
+
+// The sigmoids 1 / (1 + exp(-x)) of two values x = g + r, r a residual far below g's rounding.
+// exp(-x) = 2^t (1 + ln2 (T - t)) with T = -x log2(e) and t its fp32 rounding: the difference T - t,
+// from the residual of the product, log2(e)'s low part and r, keeps the exponential to a few units
+// in the last place however large |g| is (the rounding of t alone would cost |g| of them). The
+// factor is applied as a factor, so that an infinite 2^t stays infinite. 1 + e is scaled by 2^-24
+// before the reciprocal, which would flush to zero from 2^126 on, and its result again.
+constexpr float kLog2e = 1.44269502f, kLog2eLow = 1.92596303e-8f, kLn2 = 0.693147182f, kDown = 0x1p-24f;
+template <bool kResidual>
+__device__ __forceinline__ Pair sigmoid(Pair g, Pair r) {
+  const Pair l(-kLog2e), t = g * l, minus(-1.0f);
+  Pair rest = fma2(g, Pair(-kLog2eLow), fma2(g, l, t * minus));
+  if constexpr (kResidual) rest = fma2(r, l, rest);
+  float t_lo, t_hi;
+  t.get(t_lo, t_hi);
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(t_lo));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(t_hi));
+  const Pair e = Pair(t_lo, t_hi) * fma2(rest, Pair(kLn2), Pair(1.0f));
+  float y_lo, y_hi;
+  fma2(e, Pair(kDown), Pair(kDown)).get(y_lo, y_hi);
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(y_lo));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(y_hi));
+  return Pair(y_lo, y_hi) * Pair(kDown);
 }
 
 // Codes of 8 values that share a maximum with the lanes around them: 16 lanes (FP8's group of
@@ -111,7 +126,7 @@ __device__ __forceinline__ void store_codes(uint8_t* q, uint2 c, bool vec, int n
 // lanes of a half-warp hold one group of 128. (A half-warp per group on a grid-stride loop with a
 // 64-bit division per group ran at half this speed.)
 template <typename In, typename Out, bool kMx, int kTpr>
-__global__ void __launch_bounds__(256) silu_save_kernel(
+__global__ void __launch_bounds__(256, 5) silu_save_kernel(
     const typename In::T* __restrict__ gu, int64_t rows, int64_t inter, int64_t ld_gu,
     const int32_t* __restrict__ rows_dev, typename Out::T* __restrict__ h, int64_t ld_h, uint8_t* __restrict__ q,
     void* __restrict__ scales, bool vec_gu, bool vec_h, bool vec_q) {
@@ -131,8 +146,8 @@ __global__ void __launch_bounds__(256) silu_save_kernel(
       elem_load8<In>(gr + inter + c0, vec_gu, n, u);
 #pragma unroll
       for (int i = 0; i < 8; i += 2) {
-        const Pair sg2(sigmoid_of(expf(-g[i])), sigmoid_of(expf(-g[i + 1])));
-        (Pair(g[i], g[i + 1]) * sg2 * Pair(u[i], u[i + 1])).get(a[i], a[i + 1]);
+        const Pair g2(g[i], g[i + 1]);
+        (g2 * sigmoid<false>(g2, g2) * Pair(u[i], u[i + 1])).get(a[i], a[i + 1]);
       }
       float sg, su;
       uint8_t bg, bu;
@@ -181,7 +196,7 @@ __device__ __forceinline__ void load_codes(const uint8_t* q, bool vec, int n, fl
 // adds its even and its odd columns in ascending order, then both, a butterfly over the warp and
 // the warps in order.
 template <typename Elem, bool kMx, int kTpr>
-__global__ void __launch_bounds__(256) silu_backward_kernel(
+__global__ void __launch_bounds__(256, 5) silu_backward_kernel(
     const uint8_t* __restrict__ q, const void* __restrict__ scales, int64_t rows, int64_t inter,
     const int32_t* __restrict__ rows_dev, const typename Elem::T* __restrict__ dh, int64_t ld_dh,
     const float* __restrict__ row_weights, typename Elem::T* __restrict__ dgu, int64_t ld_dgu,
@@ -220,16 +235,8 @@ __global__ void __launch_bounds__(256) silu_backward_kernel(
 #pragma unroll
       for (int i = 0; i < 8; i += 2) {
         const Pair gc(g[i], g[i + 1]), g2 = gc * sg2, u2 = Pair(u[i], u[i + 1]) * su2, d2(d[i], d[i + 1]);
-        float g_lo, g_hi;
-        g2.get(g_lo, g_hi);
-        Pair e(expf(-g_lo), expf(-g_hi));
-        // the rounding error r of code * scale (exact by FMA) would come back multiplied by |g|
-        // through the exponential: exp(-(g + r)) = exp(-g) (1 - r) to first order, and the factor
-        // leaves an infinite exp(-g) infinite. A scale that is a power of two leaves no r.
-        if constexpr (!kMx) e = e * fma2(fma2(gc, sg2, g2 * minus), minus, one);
-        float e_lo, e_hi;
-        e.get(e_lo, e_hi);
-        const Pair s(sigmoid_of(e_lo), sigmoid_of(e_hi));
+        // (the rounding error of code * scale, exact by FMA; a power of two makes none)
+        const Pair s = sigmoid<!kMx>(g2, fma2(gc, sg2, g2 * minus));
         const Pair silu = g2 * s, h = silu * u2, wd = w2 * d2;
         dot2 = fma2(d2, h, dot2);
         (wd * u2 * fma2(silu, fma2(s, minus, one), s)).get(dg[i], dg[i + 1]);
