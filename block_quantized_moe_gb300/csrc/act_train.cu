@@ -122,137 +122,181 @@ __device__ __forceinline__ void store_codes(uint8_t* q, uint2 c, bool vec, int n
   }
 }
 
-// kTpr threads per row, 8 columns of both halves each per pass; 256 / kTpr rows per CTA. The 16
-// lanes of a half-warp hold one group of 128. (A half-warp per group on a grid-stride loop with a
-// 64-bit division per group ran at half this speed.)
+// The walk of a thread over its (row, pass of 8 columns) pairs: kTpr threads per row, 256 / kTpr
+// rows per CTA at a time, CTAs over the rows in a grid stride. Each kernel loads the next pair's
+// operands before it works on the current one: at these kernels' arithmetic per byte the loads of
+// one pair per thread do not cover the memory's latency.
+template <int kTpr>
+struct Walk {
+  static constexpr int kRows = 256 / kTpr;
+  int64_t row, limit, step;
+  int inter, c0, n;  // first column of this thread's eight, and how many of them exist (0: nothing to do)
+  __device__ __forceinline__ Walk(int64_t limit_, int64_t inter_)
+      : row((int64_t)blockIdx.x * kRows + threadIdx.x / kTpr), limit(limit_), step((int64_t)gridDim.x * kRows),
+        inter((int)inter_), c0((int)(threadIdx.x % kTpr) * 8) {
+    count();
+  }
+  __device__ __forceinline__ void count() {
+    const int left = row < limit ? inter - c0 : 0;
+    n = left >= 8 ? 8 : left > 0 ? left : 0;
+  }
+  // whether the CTA has anything left: the same for all of its threads
+  __device__ __forceinline__ bool any() const { return row - threadIdx.x / kTpr < limit; }
+  __device__ __forceinline__ bool last_pass() const { return c0 - (int)(threadIdx.x % kTpr) * 8 + kTpr * 8 >= inter; }
+  __device__ __forceinline__ void next() {
+    if (last_pass()) {
+      row += step;
+      c0 = (int)(threadIdx.x % kTpr) * 8;
+    } else {
+      c0 += kTpr * 8;
+    }
+    count();
+  }
+};
+
 template <typename In, typename Out, bool kMx, int kTpr>
-__global__ void __launch_bounds__(256, 5) silu_save_kernel(
+__global__ void __launch_bounds__(256, 4) silu_save_kernel(
     const typename In::T* __restrict__ gu, int64_t rows, int64_t inter, int64_t ld_gu,
     const int32_t* __restrict__ rows_dev, typename Out::T* __restrict__ h, int64_t ld_h, uint8_t* __restrict__ q,
     void* __restrict__ scales, bool vec_gu, bool vec_h, bool vec_q) {
-  constexpr int kRows = 256 / kTpr;
-  const int64_t limit = valid_rows(rows, rows_dev);
-  const int sub = threadIdx.x / kTpr, tid = threadIdx.x % kTpr;
-  const int64_t nb = kMx ? inter / kMxBlock : (inter + kGroup - 1) / kGroup;
-  for (int64_t base = (int64_t)blockIdx.x * kRows; base < limit; base += (int64_t)gridDim.x * kRows) {
-    const int64_t row = base + sub;
-    const typename In::T* gr = gu + row * ld_gu;
-    // the bound is uniform over the CTA, so every shuffle sees all lanes
-    for (int64_t p0 = 0; p0 < inter; p0 += kTpr * 8) {
-      const int64_t c0 = p0 + tid * 8, left = row < limit ? inter - c0 : 0;
-      const int n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
-      float g[8], u[8], a[8];
-      elem_load8<In>(gr + c0, vec_gu, n, g);
-      elem_load8<In>(gr + inter + c0, vec_gu, n, u);
+  const int nb = (int)(kMx ? inter / kMxBlock : (inter + kGroup - 1) / kGroup);
+  Walk<kTpr> at(valid_rows(rows, rows_dev), inter);
+  auto load = [&](Raw8<In>& g, Raw8<In>& u) {
+    const typename In::T* gr = gu + at.row * ld_gu + at.c0;
+    g = raw_load8<In>(gr, vec_gu, at.n);
+    u = raw_load8<In>(gr + inter, vec_gu, at.n);
+  };
+  Raw8<In> g_next, u_next;
+  load(g_next, u_next);
+  while (at.any()) {  // (the same for the whole CTA, so every shuffle sees all lanes)
+    float g[8], u[8], a[8];
+    raw_get8<In>(g_next, g);
+    raw_get8<In>(u_next, u);
+    const int64_t row = at.row;
+    const int c0 = at.c0, n = at.n;
+    at.next();
+    load(g_next, u_next);
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const Pair g2(g[i], g[i + 1]);
-        (g2 * sigmoid<false>(g2, g2) * Pair(u[i], u[i + 1])).get(a[i], a[i + 1]);
-      }
-      float sg, su;
-      uint8_t bg, bu;
-      const uint2 cg = quantize8<kMx>(g, sg, bg), cu = quantize8<kMx>(u, su, bu);
-      if (n > 0) {
-        elem_store8<Out>(h + row * ld_h + c0, vec_h, n, a);
-        uint8_t* qr = q + row * 2 * inter + c0;
-        store_codes(qr, cg, vec_q, n);
-        store_codes(qr + inter, cu, vec_q, n);
-        if constexpr (kMx) {
-          if ((tid & 3) == 0) {
-            uint8_t* s = static_cast<uint8_t*>(scales) + row * 2 * nb + c0 / kMxBlock;
-            s[0] = bg;
-            s[nb] = bu;
-          }
-        } else if ((tid & 15) == 0) {
-          float* s = static_cast<float*>(scales) + row * 2 * nb + c0 / kGroup;
-          s[0] = sg;
-          s[nb] = su;
+    for (int i = 0; i < 8; i += 2) {
+      const Pair g2(g[i], g[i + 1]);
+      (g2 * sigmoid<false>(g2, g2) * Pair(u[i], u[i + 1])).get(a[i], a[i + 1]);
+    }
+    float sg, su;
+    uint8_t bg, bu;
+    const uint2 cg = quantize8<kMx>(g, sg, bg), cu = quantize8<kMx>(u, su, bu);
+    if (n > 0) {
+      elem_store8<Out>(h + row * ld_h + c0, vec_h, n, a);
+      uint8_t* qr = q + row * 2 * inter + c0;
+      store_codes(qr, cg, vec_q, n);
+      store_codes(qr + inter, cu, vec_q, n);
+      if constexpr (kMx) {
+        if ((threadIdx.x & 3) == 0) {
+          uint8_t* s = static_cast<uint8_t*>(scales) + row * 2 * nb + c0 / kMxBlock;
+          s[0] = bg;
+          s[nb] = bu;
         }
+      } else if ((threadIdx.x & 15) == 0) {
+        float* s = static_cast<float*>(scales) + row * 2 * nb + c0 / kGroup;
+        s[0] = sg;
+        s[nb] = su;
       }
     }
   }
 }
 
-__device__ __forceinline__ void load_codes(const uint8_t* q, bool vec, int n, float (&v)[8]) {
+// n (at most 8) codes at q, the rest zero
+__device__ __forceinline__ uint2 load_codes(const uint8_t* q, bool vec, int n) {
+  if (vec && n >= 8) return *reinterpret_cast<const uint2*>(q);
   uint32_t c[2] = {0u, 0u};
-  if (vec && n >= 8) {
-    const uint2 r = *reinterpret_cast<const uint2*>(q);
-    c[0] = r.x, c[1] = r.y;
-  } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) c[i >> 2] |= (uint32_t)q[i] << (8 * (i & 3));
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
-    const float2 f = __half22float2(__half2(h));
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
-  }
+  for (int i = 0; i < 8; ++i)
+    if (i < n) c[i >> 2] |= (uint32_t)q[i] << (8 * (i & 3));
+  return make_uint2(c[0], c[1]);
+}
+__device__ __forceinline__ Pair code_pair(uint2 c, int i) {  // codes i and i + 1, i even
+  const uint32_t w = i < 4 ? c.x : c.y;
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (8 * (i & 3))), __NV_E4M3);
+  const float2 f = __half22float2(__half2(h));
+  return Pair(f.x, f.y);
 }
 
-// kTpr threads per row, 8 columns each per pass; 256 / kTpr rows per CTA. dweights: a thread
-// adds its even and its odd columns in ascending order, then both, a butterfly over the warp and
-// the warps in order.
+// dweights: a thread adds its even and its odd columns in ascending order, then both, a butterfly
+// over the warp and the warps in order.
 template <typename Elem, bool kMx, int kTpr>
-__global__ void __launch_bounds__(256, 5) silu_backward_kernel(
+__global__ void __launch_bounds__(256, 4) silu_backward_kernel(
     const uint8_t* __restrict__ q, const void* __restrict__ scales, int64_t rows, int64_t inter,
     const int32_t* __restrict__ rows_dev, const typename Elem::T* __restrict__ dh, int64_t ld_dh,
     const float* __restrict__ row_weights, typename Elem::T* __restrict__ dgu, int64_t ld_dgu,
     typename Elem::T* __restrict__ hw, int64_t ld_hw, float* __restrict__ dweights, bool vec_q, bool vec_dh,
     bool vec_dgu, bool vec_hw) {
-  constexpr int kRows = 256 / kTpr, kWarps = kTpr / 32;
+  constexpr int kWarps = kTpr / 32;
   __shared__ float part[2][8];
-  const int64_t limit = valid_rows(rows, rows_dev);
   const int sub = threadIdx.x / kTpr, tid = threadIdx.x % kTpr, lane = threadIdx.x & 31;
-  const int64_t nb = kMx ? inter / kMxBlock : (inter + kGroup - 1) / kGroup;
-  int phase = 0;
-  // the loop bound is the same for every thread of the CTA
-  for (int64_t base = (int64_t)blockIdx.x * kRows; base < limit; base += (int64_t)gridDim.x * kRows, phase ^= 1) {
-    const int64_t row = base + sub;
-    const bool live = row < limit;
-    Pair dot2(0.0f);  // columns of even and of odd index
-    const float w = live && row_weights != nullptr ? row_weights[row] : 1.0f;
-    for (int64_t c0 = (int64_t)tid * 8; live && c0 < inter; c0 += kTpr * 8) {
-      const int64_t left = inter - c0;
-      const int n = left >= 8 ? 8 : (int)left;
-      float g[8], u[8], d[8], sg, su;
-      load_codes(q + row * 2 * inter + c0, vec_q, n, g);
-      load_codes(q + row * 2 * inter + inter + c0, vec_q, n, u);
-      elem_load8<Elem>(dh + row * ld_dh + c0, vec_dh, n, d);
+  const int nb = (int)(kMx ? inter / kMxBlock : (inter + kGroup - 1) / kGroup);
+  Walk<kTpr> at(valid_rows(rows, rows_dev), inter);
+  struct Operands {
+    uint2 g, u;
+    Raw8<Elem> d;
+    float sg, su, w;
+  };
+  auto load = [&](Operands& o) {
+    const uint8_t* qr = q + at.row * 2 * inter + at.c0;
+    o.g = load_codes(qr, vec_q, at.n);
+    o.u = load_codes(qr + inter, vec_q, at.n);
+    o.d = raw_load8<Elem>(dh + at.row * ld_dh + at.c0, vec_dh, at.n);
+    o.sg = o.su = 0.0f;
+    o.w = 1.0f;
+    if (at.n > 0) {
       if constexpr (kMx) {
-        const uint8_t* s = static_cast<const uint8_t*>(scales) + row * 2 * nb + c0 / kMxBlock;
-        sg = e8m0_to_f(s[0]);
-        su = e8m0_to_f(s[nb]);
+        const uint8_t* s = static_cast<const uint8_t*>(scales) + at.row * 2 * nb + at.c0 / kMxBlock;
+        o.sg = e8m0_to_f(s[0]);
+        o.su = e8m0_to_f(s[nb]);
       } else {
-        const float* s = static_cast<const float*>(scales) + row * 2 * nb + c0 / kGroup;
-        sg = s[0];
-        su = s[nb];
+        const float* s = static_cast<const float*>(scales) + at.row * 2 * nb + at.c0 / kGroup;
+        o.sg = s[0];
+        o.su = s[nb];
       }
-      float dg[8], du[8], hv[8];
-      const Pair w2(w), one(1.0f), minus(-1.0f), sg2(sg), su2(su);
+      if (row_weights != nullptr) o.w = row_weights[at.row];
+    }
+  };
+  const Pair one(1.0f), minus(-1.0f);
+  Pair dot2(0.0f);  // columns of even and of odd index
+  int phase = 0;
+  Operands next;
+  load(next);
+  while (at.any()) {
+    const Operands o = next;
+    const int64_t row = at.row;
+    const int c0 = at.c0, n = at.n;
+    const bool last = at.last_pass(), live = row < at.limit;
+    at.next();
+    load(next);
+    float dg[8], du[8], hv[8], d[8];
+    raw_get8<Elem>(o.d, d);
+    const Pair w2(o.w), sg2(o.sg), su2(o.su);
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const Pair gc(g[i], g[i + 1]), g2 = gc * sg2, u2 = Pair(u[i], u[i + 1]) * su2, d2(d[i], d[i + 1]);
-        // (the rounding error of code * scale, exact by FMA; a power of two makes none)
-        const Pair s = sigmoid<!kMx>(g2, fma2(gc, sg2, g2 * minus));
-        const Pair silu = g2 * s, h = silu * u2, wd = w2 * d2;
-        dot2 = fma2(d2, h, dot2);
-        (wd * u2 * fma2(silu, fma2(s, minus, one), s)).get(dg[i], dg[i + 1]);
-        (wd * silu).get(du[i], du[i + 1]);
-        (w2 * h).get(hv[i], hv[i + 1]);
-      }
+    for (int i = 0; i < 8; i += 2) {
+      const Pair gc = code_pair(o.g, i), g2 = gc * sg2, u2 = code_pair(o.u, i) * su2, d2(d[i], d[i + 1]);
+      // (the rounding error of code * scale, exact by FMA; a power of two makes none)
+      const Pair s = sigmoid<!kMx>(g2, fma2(gc, sg2, g2 * minus));
+      const Pair silu = g2 * s, h = silu * u2, wd = w2 * d2;
+      dot2 = fma2(d2, h, dot2);
+      (wd * u2 * fma2(silu, fma2(s, minus, one), s)).get(dg[i], dg[i + 1]);
+      (wd * silu).get(du[i], du[i + 1]);
+      (w2 * h).get(hv[i], hv[i + 1]);
+    }
+    if (n > 0) {
       elem_store8<Elem>(dgu + row * ld_dgu + c0, vec_dgu, n, dg);
       elem_store8<Elem>(dgu + row * ld_dgu + inter + c0, vec_dgu, n, du);
       if (hw != nullptr) elem_store8<Elem>(hw + row * ld_hw + c0, vec_hw, n, hv);
     }
-    if (dweights != nullptr) {
+    if (last && dweights != nullptr) {  // (uniform over the CTA)
       float dot, odd;
       dot2.get(dot, odd);
       dot += odd;
+      dot2 = Pair(0.0f);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      for (int x = 16; x > 0; x >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, x);
       if constexpr (kWarps == 1) {
         if (live && lane == 0) dweights[row] = dot;
       } else {
@@ -265,15 +309,15 @@ __global__ void __launch_bounds__(256, 5) silu_backward_kernel(
           for (int i = 0; i < kWarps; ++i) sum += part[phase][sub * kWarps + i];
           dweights[row] = sum;
         }
+        phase ^= 1;
       }
     }
   }
 }
 
-// One CTA per rows' worth of threads (a few rows at most each), so that the loads of rows waiting
-// for a place on an SM overlap the arithmetic of others.
+// Four CTAs per SM (64 registers a thread), each walking its share of the rows.
 static int grid_for(int64_t rows, int tpr) {
-  const int64_t blocks = cdiv(rows, 256 / tpr), cap = 1 << 20;
+  const int64_t blocks = cdiv(rows, 256 / tpr), cap = (int64_t)sm_count() * 4;
   return (int)(blocks < cap ? blocks : cap);
 }
 

@@ -25,25 +25,49 @@ struct ElemF32 {
   static __device__ __forceinline__ float put(float v) { return v; }
 };
 
-// n (at most 8) elements at p as fp32, the rest zero
+// eight elements as they lie in memory
 template <typename Elem>
-__device__ __forceinline__ void elem_load8(const typename Elem::T* p, bool vec, int n, float (&v)[8]) {
+struct Raw8 {
+  uint4 w[sizeof(typename Elem::T) / 2];
+};
+
+// n (at most 8) elements at p, the rest zero
+template <typename Elem>
+__device__ __forceinline__ Raw8<Elem> raw_load8(const typename Elem::T* p, bool vec, int n) {
+  Raw8<Elem> r;
+  constexpr int kV = sizeof(typename Elem::T) / 2;
   if (vec && n >= 8) {
-    if constexpr (sizeof(typename Elem::T) == 2) {
-      const uint4 r = *reinterpret_cast<const uint4*>(p);
-      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = Elem::get((uint16_t)(w[i] & 0xffffu));
-        v[2 * i + 1] = Elem::get((uint16_t)(w[i] >> 16));
-      }
-    } else {
-      const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    for (int i = 0; i < kV; ++i) r.w[i] = reinterpret_cast<const uint4*>(p)[i];
+  } else if constexpr (kV == 1) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = (2 * i < n ? (uint32_t)p[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)p[2 * i + 1] << 16 : 0u);
+    r.w[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = i < n ? __float_as_uint(p[i]) : 0u;
+    r.w[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    r.w[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+  return r;
+}
+
+template <typename Elem>
+__device__ __forceinline__ void raw_get8(const Raw8<Elem>& r, float (&v)[8]) {
+  if constexpr (sizeof(typename Elem::T) == 2) {
+    const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = Elem::get((uint16_t)(w[i] & 0xffffu));
+      v[2 * i + 1] = Elem::get((uint16_t)(w[i] >> 16));
     }
   } else {
+    const uint32_t w[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w, r.w[1].x, r.w[1].y, r.w[1].z, r.w[1].w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? Elem::get(p[i]) : 0.0f;
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
   }
 }
 
