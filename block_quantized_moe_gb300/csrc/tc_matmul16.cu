@@ -331,25 +331,26 @@ __global__ void __launch_bounds__(threads(MODE), 1)
   }
   if constexpr (!kWG) {
     if (warp == 0) {
-      int run = 0;
+      // (64-bit, and cut off at the largest int: overlapping segments can count rows many times)
+      long long run = 0;
       for (int base = 0; base < p.E; base += 32) {
         const int e = base + lane;
-        int u = 0;
+        long long u = 0;
         if (e < p.E) {
           int lo, hi;
           bounds(e, lo, hi);
-          u = (hi - lo + kN - 1) / kN * MB;
+          u = (long long)((hi - lo + kN - 1) / kN) * MB;
         }
-        int inc = u;
+        long long inc = u;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const int t = __shfl_up_sync(0xffffffffu, inc, o);
+          const long long t = __shfl_up_sync(0xffffffffu, inc, o);
           if (lane >= o) inc += t;
         }
-        if (e < p.E) cum[e] = run + inc - u;
+        if (e < p.E) cum[e] = (int)min(run + inc - u, (long long)0x7fffffff);
         run += __shfl_sync(0xffffffffu, inc, 31);
       }
-      if (lane == 0) cum[p.E] = run;
+      if (lane == 0) cum[p.E] = (int)min(run, (long long)0x7fffffff);
     }
   }
   if (warp == 1) {
@@ -382,9 +383,9 @@ __global__ void __launch_bounds__(threads(MODE), 1)
         if (cum[mid] <= u) a = mid; else b = mid - 1;
       }
       t.e = a;
-      const int units = cum[a + 1] - cum[a], nt = units / MB, local = u - cum[a];
       int lo, hi;
       bounds(a, lo, hi);
+      const int nt = (hi - lo + kN - 1) / kN, local = u - cum[a];
       const int per = ((hi - lo + nt - 1) / nt + 31) & ~31;
       t.m0 = local / nt * kM;
       t.c0 = lo + local % nt * per;
@@ -401,9 +402,9 @@ __global__ void __launch_bounds__(threads(MODE), 1)
     // ------------------------------- TMA producer -------------------------------
     if (lane == 0) {
       uint32_t it = 0, tails = 0, tail_ph = 0;  // bit st: slot st's last use was a tail; uses of lfull[st], mod 2
-      for (int u = u_begin; u < u_end && !s_abort; u += u_step) {
+      for (int64_t u = u_begin; u < u_end && !s_abort; u += u_step) {
         Unit t;
-        decode(u, t);
+        decode((int)u, t);
         const int half = t.n >> 1;  // of c in each CTA
         const int steps = (t.len + kBK - 1) / kBK;
         const int cb = t.c0 + (int)crank * half, ma = t.m0 + (int)crank * 128;
@@ -476,9 +477,9 @@ __global__ void __launch_bounds__(threads(MODE), 1)
       constexpr uint32_t kSlot = kStage >> 4, kStepA = (MODE == kProduct ? 32 : 2048) >> 4, kStepB = (kWG ? 2048 : 32) >> 4;
       const uint32_t full0 = smem_u32(&full[0]), empty0 = smem_u32(&empty[0]);
       bool ok = true;
-      for (int u = u_begin; u < u_end && ok; u += u_step) {
+      for (int64_t u = u_begin; u < u_end && ok; u += u_step) {
         Unit t;
-        decode(u, t);
+        decode((int)u, t);
         const uint32_t idesc = (1u << 4) | ((uint32_t)p.bf16 << 7) | ((uint32_t)p.bf16 << 10) |
                                (MODE == kProduct ? 0u : 1u << 15) | (kWG ? 1u << 16 : 0u) |
                                ((uint32_t)(t.n >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);
@@ -526,9 +527,9 @@ __global__ void __launch_bounds__(threads(MODE), 1)
     // ------------------------- tails of segments -------------------------
     uint32_t it = 0, ph = 0;
     bool ok = true;
-    for (int u = u_begin; u < u_end && ok; u += u_step) {
+    for (int64_t u = u_begin; u < u_end && ok; u += u_step) {
       Unit t;
-      decode(u, t);
+      decode((int)u, t);
       const int steps = (t.len + kBK - 1) / kBK, v = t.len % kBK;
       if (v != 0) {
         const int st = (it + steps - 1) % S;
@@ -549,9 +550,9 @@ __global__ void __launch_bounds__(threads(MODE), 1)
     // ------------------------ saved rows: codes ------------------------
     if (lane == 0) {
       uint32_t it = 0;
-      for (int u = u_begin; u < u_end && !s_abort; u += u_step) {
+      for (int64_t u = u_begin; u < u_end && !s_abort; u += u_step) {
         Unit t;
-        decode(u, t);
+        decode((int)u, t);
         const int steps = (t.len + kBK - 1) / kBK, ma = t.m0 + (int)crank * 128;
         for (int s = 0; s < steps; ++s, ++it) {
           const int r = it % kRawSlots;
@@ -582,9 +583,9 @@ __global__ void __launch_bounds__(threads(MODE), 1)
     const bool words = p.ld_out % 2 == 0 && p.out_expert % 2 == 0 && reinterpret_cast<uintptr_t>(p.out) % 4 == 0;
     const bool f32 = kSum || p.out_dtype == FTMOE_OUT_FP32;
     const bool tma_out = p.tma_out && (!p.accumulate || p.out_dtype == FTMOE_OUT_FP32);
-    for (int u = u_begin; u < u_end; u += u_step) {
+    for (int64_t u = u_begin; u < u_end; u += u_step) {
       Unit t;
-      decode(u, t);
+      decode((int)u, t);
       const bool none = kWG && t.len == 0;  // an expert without rows: zeros, or nothing to add
       if (none && p.accumulate) continue;
       const int mc = t.m0 + (int)crank * 128, ml = 32 * quarter + lane, m = mc + ml;
@@ -733,9 +734,9 @@ __global__ void __launch_bounds__(threads(MODE), 1)
     const int kg = p.m_dim / kMxBlock;
     uint32_t it = 0, tph = 0;  // tph, bit st: uses of lfull[st], mod 2 (every team counts them all)
     bool ok = true;
-    for (int u = u_begin; u < u_end && ok; u += u_step) {
+    for (int64_t u = u_begin; u < u_end && ok; u += u_step) {
       Unit t;
-      decode(u, t);
+      decode((int)u, t);
       const int steps = (t.len + kBK - 1) / kBK;
       const int g = (t.m0 + (int)crank * 128) / kMxBlock + grp;
       // scale bytes, fetched one of the team's stages ahead of their codes
