@@ -1,6 +1,6 @@
 """A training step of the routed expert FFN on libftmoe's 16-bit products.
 
-    python examples/train_experts.py [--steps 20]
+    python examples/train_experts.py [--steps 20 --tokens 1024 --hidden 1024 --inter 512 --experts 16 --topk 4]
 
 expert_ffn(x, route_weights, w_gateup, w_down, expert_ids) is a torch function with gradients of
 x, the routing weights and both weight banks. Between the passes it keeps, per token, the input row
@@ -104,9 +104,10 @@ def main():
     import synth
     parser = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     parser.add_argument("--steps", type=int, default=20)
-    parser.add_argument("--tokens", type=int, default=1024)
+    for name, default in (("tokens", 1024), ("hidden", 1024), ("inter", 512), ("experts", 16), ("topk", 4)):
+        parser.add_argument("--" + name, type=int, default=default)
     args = parser.parse_args()
-    T, H, inter, E, topk, dev = args.tokens, 1024, 512, 16, 4, "cuda"
+    T, H, inter, E, topk, dev = args.tokens, args.hidden, args.inter, args.experts, args.topk, "cuda"
     ids = synth.routes_fast(T, topk, E, 1, dev)
     logits = torch.zeros(T, topk, device=dev, requires_grad=True)
 
