@@ -27,25 +27,7 @@ __device__ __forceinline__ int64_t valid_rows(int64_t rows, const int32_t* rows_
   return d < 0 ? 0 : (d < rows ? d : rows);
 }
 
-// Pairs of fp32 values in one instruction (Blackwell's packed fp32 pipe): these kernels run at the
-// issue rate, and this halves their products and sums.
-struct Pair {
-  unsigned long long v;
-  __device__ __forceinline__ Pair() {}
-  __device__ __forceinline__ Pair(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
-  __device__ __forceinline__ explicit Pair(float both) : Pair(both, both) {}
-  __device__ __forceinline__ void get(float& lo, float& hi) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
-};
-__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
-  Pair r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-  Pair r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
+using Pair = F32Pair;
 
 // The sigmoids 1 / (1 + exp(-x)) of two values x = g + r, r a residual far below g's rounding.
 // exp(-x) = 2^t (1 + ln2 (T - t)) with T = -x log2(e) and t its fp32 rounding: the difference T - t,

@@ -100,6 +100,26 @@ __device__ __forceinline__ void elem_store8(typename Elem::T* p, bool vec, int n
   }
 }
 
+// Pairs of fp32 values in one instruction (Blackwell's packed fp32 pipe): for kernels that run at
+// the issue rate it halves their products and sums.
+struct F32Pair {
+  unsigned long long v;
+  __device__ __forceinline__ F32Pair() {}
+  __device__ __forceinline__ F32Pair(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
+  __device__ __forceinline__ explicit F32Pair(float both) : F32Pair(both, both) {}
+  __device__ __forceinline__ void get(float& lo, float& hi) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+};
+__device__ __forceinline__ F32Pair operator*(F32Pair a, F32Pair b) {
+  F32Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F32Pair fma2(F32Pair a, F32Pair b, F32Pair c) {
+  F32Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
 // whether rows of `elem_bytes`-byte elements at base with stride ld may take 8-element vectors
 // (16-byte accesses)
 inline bool elem_vec_ok(const void* base, int64_t ld, int elem_bytes) {

@@ -27,7 +27,7 @@
 // step of a segment lands on a barrier of its own; a warp then zeroes the rows past the
 // segment, in A and in B (what is there may be NaN), up to the next multiple of 16, and hands
 // the stage to the MMA issuer, which runs only the 16-row steps that hold rows.
-// From saved rows (MXFP8), A arrives as codes; eight warps decode them into the operand tile,
+// From saved rows (MXFP8), A arrives as codes; sixteen warps decode them into the operand tile,
 // a 32-wide group with its power-of-two scale at a time, exactly.
 //
 // Long sums. The tensor core cuts low bits off as it adds a product to its fp32 accumulator: the
@@ -39,7 +39,7 @@
 // parts are added in memory by TMA.
 //
 // Roles: warp 0 TMA, warp 1 MMA issue and TMEM, warp 2 segment tails (weight grad) or codes
-// (saved rows), warps 4-11 epilogue, warps 12-19 decode (saved rows). Every mbarrier wait is bounded: on timeout the
+// (saved rows), warps 4-11 epilogue, warps 12-27 decode (saved rows). Every mbarrier wait is bounded: on timeout the
 // kernel raises FTMOE_ERR_WAIT_TIMEOUT, stops its roles, waits for its own loads and MMAs,
 // frees its TMEM and returns.
 #include <cuda.h>
@@ -62,7 +62,7 @@ constexpr int kRaw = 128 * kBK;           // saved rows: 8 KiB of codes
 constexpr int kRawSlots = 4;
 constexpr int kOutBuf = 8192;             // an output box: 32 columns of c (16 of fp32) by 128 of m
 constexpr int kOutBufs = 3;               // boxes in flight for each half of the epilogue
-constexpr int kEpiWarps = 8, kDecWarps = 8, kDecTeams = 4, kTeamWarps = kDecWarps / kDecTeams;
+constexpr int kEpiWarps = 8, kDecWarps = 16, kDecTeams = 4, kTeamWarps = kDecWarps / kDecTeams;
 constexpr int kMaxExperts = 4096;
 
 __host__ __device__ constexpr bool is_wgrad(int mode) { return mode >= kWeightGrad; }
@@ -273,10 +273,15 @@ __device__ __forceinline__ void store_columns(typename Elem::T* out, int64_t ld,
   }
 }
 
-// Registers with kSum: 384 threads launch with 168 each; the control warpgroup keeps 80, the two
-// epilogue warpgroups take 208.
-constexpr int kCtlRegs = 80, kSumRegs = 208;
-constexpr int kSumRegsNeeded = 128 * kCtlRegs + 256 * kSumRegs;
+// Register splits (setmaxnreg). With kSum 384 threads launch with 168 registers each; the control
+// warpgroup keeps 80, the two epilogue warpgroups take 208. From saved rows 896 threads launch
+// with 72: control keeps 56, the epilogue takes 96, the four decoding warpgroups keep 64.
+template <int MODE, bool kSum>
+struct Regs {
+  static constexpr bool kSplit = kSum || MODE == kWeightGradSaved;
+  static constexpr int kCtl = kSum ? 80 : 56, kEpi = kSum ? 208 : 96, kDec = 64;
+  static constexpr int kNeeded = 128 * kCtl + 256 * kEpi + (MODE == kWeightGradSaved ? 32 * kDecWarps * kDec : 0);
+};
 constexpr int kSumStages = 8, kAddStages = 32, kNoChunk = 0x3fffffff;
 
 template <int MODE, bool kSum>
@@ -397,7 +402,8 @@ __global__ void __launch_bounds__(threads(MODE), 1)
   };
 
   if (warp < 4) {
-  if constexpr (kSum) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtlRegs));
+  using R = Regs<MODE, kSum>;
+  if constexpr (R::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kCtl));
   if (warp == 0) {
     // ------------------------------- TMA producer -------------------------------
     if (lane == 0) {
@@ -571,7 +577,8 @@ __global__ void __launch_bounds__(threads(MODE), 1)
   }
   } else if (warp < 4 + kEpiWarps) {
     // --------------------------------- epilogue ---------------------------------
-    if constexpr (kSum) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
+    using R = Regs<MODE, kSum>;
+    if constexpr (R::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::kEpi));
     // Two groups of four warps take chunks of 32 columns in turn. A chunk goes through shared
     // memory and leaves as TMA boxes of 128 m by 32 c (16 of fp32), 256 or 512 contiguous bytes
     // a row. (Stored from registers, 64 bytes a row and warp, the weight gradient of 64 experts
@@ -723,7 +730,8 @@ __global__ void __launch_bounds__(threads(MODE), 1)
     if (leader) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   } else if constexpr (kSaved) {
     // ------------------------ saved rows: decode ------------------------
-    // Four teams of two warps take stages in turn, so that some decode while others wait for
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<MODE, kSum>::kDec));
+    // Four teams of four warps take stages in turn, so that some decode while others wait for
     // codes, for a free operand slot or for their stores to be visible. Thread (warp dw of the
     // team, lane): lines r0 + 16 v of the stage's 64, r0 = 8 dw + lane % 8, and the 32-wide group
     // lane / 8 of their 128 codes. Eight lanes with consecutive lines touch eight different
@@ -792,7 +800,9 @@ __global__ void __launch_bounds__(threads(MODE), 1)
                 const uint32_t two = (cw[k >> 1] >> (16 * (k & 1))) & 0xffffu;
                 const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
                 const float2 f = __half22float2(__half2(hr));
-                o[k] = pack2<Elem>(f.x * sc, f.y * sc);
+                float lo, hi;
+                (F32Pair(f.x, f.y) * F32Pair(sc)).get(lo, hi);
+                o[k] = pack2<Elem>(lo, hi);
               }
               const int col = (grp & 1) * 4 + 2 * h;
               st_shared_16(line + ((col ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
@@ -884,12 +894,12 @@ static cudaError_t launch(const CUtensorMap* maps, const Params& p, cudaStream_t
     if (e != cudaSuccess) return e;
     np = max_active_clusters(tc_matmul16_kernel<MODE, kSum>, dim3(threads(MODE)), most, 2, 2 * (sm_count() / 2));
     if (np > sm_count() / 2) np = sm_count() / 2;
-    if constexpr (kSum) {
+    if constexpr (Regs<MODE, kSum>::kSplit) {
       // the register split has to fit what the block is launched with
       cudaFuncAttributes fa;
       const cudaError_t ea = cudaFuncGetAttributes(&fa, tc_matmul16_kernel<MODE, kSum>);
       if (ea != cudaSuccess) return ea;
-      if (fa.numRegs * threads(MODE) < kSumRegsNeeded) np = 0;
+      if (fa.numRegs * threads(MODE) < Regs<MODE, kSum>::kNeeded) np = 0;
     }
     if (dev >= 0 && dev < 64) pairs[dev] = np;
   }
