@@ -4,14 +4,15 @@
 //   product       out[r, i]    = sum_j a[r, j] w[e, i, j]
 //   input grad    out[r, j]    = sum_i a[r, i] w[e, i, j]
 //   weight grad   dw[e, i, j] (+)= sum_r dy[r, i] x[r, j]
-// are one tile product D[m, c] = sum_l A[m, l] B[c, l] whose result is stored transposed,
-// out[c, m]: m runs along the contiguous axis of the output (i, j and j), c along its rows (the
-// expert's rows, or i). So the 32 lanes of an epilogue warp, which hold 32 consecutive m of one
-// column c, always write consecutive addresses, and the ragged axis is always the MMA's N, which
-// an instruction descriptor sets at run time in steps of 32:
-//   product       A = w (l contiguous, "K-major")   B = a rows (K-major)      l: j, c: rows
-//   input grad    A = w (m contiguous, "MN-major")  B = a rows (K-major)      l: i, c: rows
-//   weight grad   A = x (MN-major)                  B = dy (MN-major)         l: rows, c: i
+// are one tile product D[m, c] = sum_l A[m, l] B[c, l], m along the lanes of an accumulator and c
+// along its columns, whose width an instruction descriptor sets at run time in steps of 32:
+//   product       A = w (l contiguous, "K-major")   B = a rows (K-major)      l: j, m: i, c: rows
+//   input grad    A = w (m contiguous, "MN-major")  B = a rows (K-major)      l: i, m: j, c: rows
+//   weight grad   A = dy (MN-major)                 B = x (MN-major)          l: rows, m: i, c: j
+// The first two keep the ragged axis in c and store the result transposed, out[c, m]: the 32
+// lanes of an epilogue warp, 32 consecutive m of one column, write consecutive addresses. The
+// weight gradient's accumulator is a tile of dw as it lies in memory, or (fp32) its transpose,
+// with A and B exchanged.
 // One kernel therefore serves one row per expert and thousands: an expert's m_e rows make
 // ceil(m_e / 256) column tiles of equal width, rounded up to 32.
 //
@@ -27,7 +28,7 @@
 // step of a segment lands on a barrier of its own; a warp then zeroes the rows past the
 // segment, in A and in B (what is there may be NaN), up to the next multiple of 16, and hands
 // the stage to the MMA issuer, which runs only the 16-row steps that hold rows.
-// From saved rows (MXFP8), A arrives as codes; sixteen warps decode them into the operand tile,
+// From saved rows (MXFP8), B arrives as codes; twelve warps decode them into the operand tile,
 // a 32-wide group with its power-of-two scale at a time, exactly.
 //
 // Long sums. The tensor core cuts low bits off as it adds a product to its fp32 accumulator: the
@@ -35,11 +36,12 @@
 // over 4,096 terms, where fp32 sums rounded to nearest have 6e-7). A 16-bit output hides that, an
 // fp32 output does not. For fp32 outputs an accumulator takes 8 stages (512 terms) and the
 // epilogue adds the accumulators up in registers, 128 per thread, the control warps giving up
-// theirs; from saved rows, whose decoding warps need the registers, it takes 32 stages and the
-// parts are added in memory by TMA.
+// theirs. A weight gradient from saved rows (whose decoding warps need the registers), or of
+// segments that are short on average, takes 16 stages and adds the parts of the few segments that
+// are longer in memory, by TMA.
 //
 // Roles: warp 0 TMA, warp 1 MMA issue and TMEM, warp 2 segment tails (weight grad) or codes
-// (saved rows), warps 4-11 epilogue, warps 12-27 decode (saved rows). Every mbarrier wait is bounded: on timeout the
+// (saved rows), warps 4-11 epilogue, warps 12-23 decode (saved rows). Every mbarrier wait is bounded: on timeout the
 // kernel raises FTMOE_ERR_WAIT_TIMEOUT, stops its roles, waits for its own loads and MMAs,
 // frees its TMEM and returns.
 #include <cuda.h>
@@ -53,24 +55,37 @@ namespace ftmoe {
 
 namespace tc16 {
 
-enum Mode { kProduct = 0, kInputGrad = 1, kWeightGrad = 2, kWeightGradSaved = 3 };
+// kWeightGradT: the weight gradient with the operands' roles exchanged (A = x, B = dy), stored
+// transposed like the product: fp32 outputs, see the epilogue
+enum Mode { kProduct = 0, kInputGrad = 1, kWeightGrad = 2, kWeightGradSaved = 3, kWeightGradT = 4 };
 
 constexpr int kBK = 64;                   // elements of l per stage: one 128-byte swizzle atom
 constexpr int kM = 256, kN = 256;         // of the pair
 constexpr int kTile = 128 * kBK * 2;      // 16 KiB: this CTA's half of A, and of B at most
 constexpr int kRaw = 128 * kBK;           // saved rows: 8 KiB of codes
-constexpr int kRawSlots = 4;
+constexpr int kRawSlots = 3;
 constexpr int kOutBuf = 8192;             // an output box: 32 columns of c (16 of fp32) by 128 of m
 constexpr int kOutBufs = 3;               // boxes in flight for each half of the epilogue
-constexpr int kEpiWarps = 8, kDecWarps = 16, kDecTeams = 4, kTeamWarps = kDecWarps / kDecTeams;
-constexpr int kMaxExperts = 4096;
+constexpr int kEpiWarps = 8, kDecWarps = 12, kDecTeams = 3, kTeamWarps = kDecWarps / kDecTeams;
+// A team meets each code slot in every one of its phases: waiting by parity, it could take a
+// phase that another team has yet to see for its own.
+static_assert(kRawSlots % kDecTeams == 0, "a code slot belongs to one team");
+constexpr int kMaxExperts = 1024;  // segment bounds and unit counts live in shared memory
 
 __host__ __device__ constexpr bool is_wgrad(int mode) { return mode >= kWeightGrad; }
-// 32 KiB a stage (a fill takes about as long as three stages' MMAs; 4, 5 and 6 stages measured
-// the same), the output boxes of both halves of the epilogue, and the ring of codes.
+// whether an accumulator is a tile of the output as it lies in memory
+__host__ __device__ constexpr bool by_rows(int mode) { return mode == kWeightGrad || mode == kWeightGradSaved; }
+constexpr int kSquareRows = 4096;         // weight grad: see the order of units
+// 32 KiB a stage, the output boxes, and the ring of codes. Five stages: with four a weight
+// gradient of 24,576 rows, 4096 x 7168, takes 863 us instead of 715.
 __host__ __device__ constexpr int stages(int mode) { return mode == kWeightGradSaved ? 4 : 5; }
+// Weight grad: boxes of 64 rows of 128 bytes, two buffers for each pair of epilogue warps. A TMA
+// instruction costs the loads' engine about 100 clocks whatever it moves: with boxes of 16 rows 24,576
+// rows over 32 experts took 904 us.
+constexpr int kRowBuf = 64 * 128;
+__host__ __device__ constexpr int out_bytes(int mode) { return by_rows(mode) ? 4 * 2 * kRowBuf : 2 * kOutBufs * kOutBuf; }
 __host__ __device__ constexpr int smem_bytes(int mode) {
-  return stages(mode) * 2 * kTile + 2 * kOutBufs * kOutBuf + (mode == kWeightGradSaved ? kRawSlots * kRaw : 0);
+  return stages(mode) * 2 * kTile + out_bytes(mode) + (mode == kWeightGradSaved ? kRawSlots * kRaw : 0);
 }
 __host__ __device__ constexpr int threads(int mode) { return 32 * (4 + kEpiWarps + (mode == kWeightGradSaved ? kDecWarps : 0)); }
 
@@ -235,14 +250,14 @@ __device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, uint32_t src,
                : "memory");
 }
 
-// 32 columns d[0..31] of this lane's m into out[(c0 + j) * ld + m], j < cols, m < m_dim. 16-bit
-// types: neighbouring lanes trade every second column, so that each stores two adjacent m of
-// one column as one word (where `words` says that rows keep 4-byte alignment).
+// 32 columns d[0..31] of this lane's m into out[j * ld + m], j < cols, m < m_dim, or (`add`) added
+// to it in fp32 and rounded once. 16-bit types: neighbouring lanes trade every second column, so that each stores two adjacent m of one column
+// as one word (where `words` says that rows keep 4-byte alignment).
 template <typename Elem>
 __device__ __forceinline__ void store_columns(typename Elem::T* out, int64_t ld, const float (&d)[32], int cols, int m,
-                                              int m_dim, int lane, bool words, bool accumulate) {
+                                              int m_dim, int lane, bool words, bool add) {
   using T = typename Elem::T;
-  if (sizeof(T) == 2 && words && !accumulate) {
+  if (sizeof(T) == 2 && words && !add) {
     const bool odd = lane & 1;
     T* o = out + (m & ~1) + (odd ? ld : 0);
     const bool in = (m | 1) < m_dim;
@@ -262,40 +277,63 @@ __device__ __forceinline__ void store_columns(typename Elem::T* out, int64_t ld,
 #pragma unroll
     for (int j0 = 0; j0 < 32; j0 += 8) {
       float old[8] = {};
-      if (accumulate) {
+      if (add) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) old[j] = j0 + j < cols ? Elem::get(o[(j0 + j) * ld]) : 0.0f;
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (j0 + j < cols) o[(j0 + j) * ld] = Elem::put(accumulate ? old[j] + d[j0 + j] : d[j0 + j]);
+        if (j0 + j < cols) o[(j0 + j) * ld] = Elem::put(add ? old[j] + d[j0 + j] : d[j0 + j]);
     }
   }
 }
 
+// d[0 .. cols - 1] (32 at most) along a row, added to what is there (in fp32, rounded once) or in its place
+template <typename Elem>
+__device__ __forceinline__ void store_row(typename Elem::T* o, const float (&d)[32], int cols, bool add) {
+  const bool vec = (uintptr_t)o % 16 == 0;
+#pragma unroll
+  for (int j0 = 0; j0 < 32; j0 += 8) {
+    const int n = cols - j0;
+    if (n <= 0) break;
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = d[j0 + j];
+    if (add) {
+      float old[8];
+      raw_get8<Elem>(raw_load8<Elem>(o + j0, vec, n), old);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += old[j];
+    }
+    elem_store8<Elem>(o + j0, vec, n, v);
+  }
+}
+
 // Register splits (setmaxnreg). With kSum 384 threads launch with 168 registers each; the control
-// warpgroup keeps 80, the two epilogue warpgroups take 208. From saved rows 896 threads launch
-// with 72: control keeps 56, the epilogue takes 96, the four decoding warpgroups keep 64.
+// warpgroup keeps 80, the two epilogue warpgroups take 208. From saved rows 768 threads launch
+// with 80: control keeps 56, the epilogue takes 96, the three decoding warpgroups keep 72.
 template <int MODE, bool kSum>
 struct Regs {
   static constexpr bool kSplit = kSum || MODE == kWeightGradSaved;
-  static constexpr int kCtl = kSum ? 80 : 56, kEpi = kSum ? 208 : 96, kDec = 64;
+  static constexpr int kCtl = kSum ? 80 : 56, kEpi = kSum ? 208 : 96, kDec = 72;
   static constexpr int kNeeded = 128 * kCtl + 256 * kEpi + (MODE == kWeightGradSaved ? 32 * kDecWarps * kDec : 0);
 };
-constexpr int kSumStages = 8, kAddStages = 32, kNoChunk = 0x3fffffff;
+constexpr int kSumStages = 8, kAddStages = 16, kNoChunk = 0x3fffffff;
 
 template <int MODE, bool kSum>
 __global__ void __launch_bounds__(threads(MODE), 1)
     tc_matmul16_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b0,
                        const __grid_constant__ CUtensorMap map_b1, const __grid_constant__ CUtensorMap map_b2,
                        const __grid_constant__ CUtensorMap map_b3, const __grid_constant__ CUtensorMap map_o, Params p) {
-  constexpr bool kWG = is_wgrad(MODE), kSaved = MODE == kWeightGradSaved;
+  constexpr bool kWG = is_wgrad(MODE), kSaved = MODE == kWeightGradSaved, kRows = by_rows(MODE);
   constexpr int S = stages(MODE), kStage = 2 * kTile;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  uint8_t* outbuf = tiles + (size_t)S * kStage;        // [2 halves of the epilogue][kOutBufs] output boxes
-  uint8_t* raws = outbuf + 2 * kOutBufs * kOutBuf;     // saved rows: [kRawSlots] codes
-  int* cum = reinterpret_cast<int*>(raws);             // else: [E + 1] units before expert e (not weight grad)
+  uint8_t* outbuf = tiles + (size_t)S * kStage;  // [2 halves of the epilogue][kOutBufs], or [warp pairs][2], boxes
+  uint8_t* raws = outbuf + out_bytes(MODE);      // saved rows: [kRawSlots] codes
+  // product and input grad: [E + 1] segment offsets, cut to [0, rows]; [E + 1] units before expert e
+  int* seg = reinterpret_cast<int*>(raws);
+  int* cum = seg + p.E + 1;
   __shared__ __align__(8) uint64_t full[S], empty[S], lfull[S], tfull[2], tempty[2];
   __shared__ __align__(8) uint64_t rfull[kRawSlots], rempty[kRawSlots];  // saved rows: codes landed, codes taken
   __shared__ uint32_t s_tmem;
@@ -306,12 +344,13 @@ __global__ void __launch_bounds__(threads(MODE), 1)
   const int MB = (p.m_dim + kM - 1) / kM;
   const int CB = kWG ? (p.c_dim + kN - 1) / kN : 0;
 
+  auto cut = [&](int v) { return v < 0 ? 0 : v > p.rows ? (int)p.rows : v; };
+  if constexpr (!kWG)
+    for (int e = threadIdx.x; e <= p.E; e += blockDim.x) seg[e] = cut(__ldg(p.offsets + e));
+  // (weight grad: one expert has many units in a row, its offsets stay in L1)
   auto bounds = [&](int e, int& lo, int& hi) {
-    lo = __ldg(p.offsets + e);
-    hi = __ldg(p.offsets + e + 1);
-    lo = lo < 0 ? 0 : lo;
-    hi = hi > p.rows ? (int)p.rows : hi;
-    if (hi < lo) hi = lo;
+    lo = kWG ? cut(__ldg(p.offsets + e)) : seg[e];
+    hi = max(lo, kWG ? cut(__ldg(p.offsets + e + 1)) : seg[e + 1]);
   };
 
   if (threadIdx.x == 0) {
@@ -334,6 +373,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  __syncthreads();
   if constexpr (!kWG) {
     if (warp == 0) {
       // (64-bit, and cut off at the largest int: overlapping segments can count rows many times)
@@ -371,16 +411,27 @@ __global__ void __launch_bounds__(threads(MODE), 1)
 
   auto decode = [&](int u, Unit& t) {
     if constexpr (kWG) {
-      // units of one expert adjacent: they read the same rows
+      // Units of one expert adjacent: they read the same rows.
       t.e = u / (MB * CB);
-      const int local = u - t.e * MB * CB;
-      t.m0 = local / CB * kM;
-      t.c0 = local % CB * kN;
-      t.cols = min(kN, p.c_dim - t.c0);
       int lo, hi;
       bounds(t.e, lo, hi);
       t.l0 = lo;
       t.len = hi - lo;
+      int local = u - t.e * MB * CB;
+      if (t.len > kSquareRows) {
+        // bound by what it reads: eight blocks of m at a time, m innermost, so that the pairs at
+        // work cover a near square: 8 + 10 tiles of 7,168 columns, not 3 + 28
+        const int group = local / (8 * CB), width = min(8, MB - 8 * group);
+        local -= group * 8 * CB;
+        t.m0 = (8 * group + local % width) * kM;
+        t.c0 = local / width * kN;
+      } else {
+        // whole rows of dw at a time (32 experts of 768 rows: 849 us, in squares 875; one of
+        // 24,576 rows: 755 us, in squares 706)
+        t.m0 = local / CB * kM;
+        t.c0 = local % CB * kN;
+      }
+      t.cols = min(kN, p.c_dim - t.c0);
     } else {
       int a = 0, b = p.E - 1;
       while (a < b) {  // the last expert whose units begin at or before u
@@ -398,7 +449,8 @@ __global__ void __launch_bounds__(threads(MODE), 1)
       t.l0 = 0;
       t.len = p.l_dim;
     }
-    t.n = (t.cols + 31) & ~31;
+    // (saved rows: each CTA's half starts on a 32-wide scale group)
+    t.n = kSaved ? (t.cols + 63) & ~63 : (t.cols + 31) & ~31;
   };
 
   if (warp < 4) {
@@ -418,7 +470,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
         const int hb = half <= 16 ? 16 : half <= 32 ? 32 : half <= 64 ? 64 : 128;
         const CUtensorMap* mb = half <= 16 ? &map_b3 : half <= 32 ? &map_b2 : half <= 64 ? &map_b1 : &map_b0;
         const uint32_t bytes_b = kWG ? (half > 64 ? kTile : kTile / 2) : (uint32_t)hb * 128;
-        const uint32_t bytes = (kSaved ? 0 : kTile) + bytes_b;
+        const uint32_t bytes = kTile + (kSaved ? 0 : bytes_b);
         for (int s = 0; s < steps; ++s, ++it) {
           const int st = it % S;
           if (!mbar_wait(smem_u32(&empty[st]), ((it / S) & 1) ^ 1, &s_abort)) break;
@@ -437,12 +489,12 @@ __global__ void __launch_bounds__(threads(MODE), 1)
           }
           if constexpr (kWG) {
             const int l = t.l0 + s * kBK;
+            tma_pair_2d(ta, &map_a, bar, ma, l);
+            tma_pair_2d(ta + kTile / 2, &map_a, bar, ma + 64, l);
             if constexpr (!kSaved) {
-              tma_pair_2d(ta, &map_a, bar, ma, l);
-              tma_pair_2d(ta + kTile / 2, &map_a, bar, ma + 64, l);
+              tma_pair_2d(tb, &map_b0, bar, cb, l);
+              if (half > 64) tma_pair_2d(tb + kTile / 2, &map_b0, bar, cb + 64, l);
             }
-            tma_pair_2d(tb, &map_b0, bar, cb, l);
-            if (half > 64) tma_pair_2d(tb + kTile / 2, &map_b0, bar, cb + 64, l);
           } else {
             if constexpr (MODE == kProduct) {
               tma_pair_3d(ta, &map_a, bar, s * kBK, ma, t.e);
@@ -529,7 +581,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
         }
       }
     }
-  } else if (MODE == kWeightGrad && warp == 2) {
+  } else if (kWG && !kSaved && warp == 2) {
     // ------------------------- tails of segments -------------------------
     uint32_t it = 0, ph = 0;
     bool ok = true;
@@ -559,12 +611,12 @@ __global__ void __launch_bounds__(threads(MODE), 1)
       for (int64_t u = u_begin; u < u_end && !s_abort; u += u_step) {
         Unit t;
         decode((int)u, t);
-        const int steps = (t.len + kBK - 1) / kBK, ma = t.m0 + (int)crank * 128;
+        const int steps = (t.len + kBK - 1) / kBK, cb = t.c0 + (int)crank * (t.n >> 1);
         for (int s = 0; s < steps; ++s, ++it) {
           const int r = it % kRawSlots;
           if (!mbar_wait(smem_u32(&rempty[r]), ((it / kRawSlots) & 1) ^ 1, &s_abort)) break;
           mbar_expect_tx(smem_u32(&rfull[r]), kRaw);
-          tma_pair_2d(smem_u32(raws + r * kRaw), &map_a, smem_u32(&rfull[r]), ma, t.l0 + s * kBK);
+          tma_pair_2d(smem_u32(raws + r * kRaw), &map_b0, smem_u32(&rfull[r]), cb, t.l0 + s * kBK);
         }
       }
       for (int r = 0; r < kRawSlots && (uint32_t)r < it; ++r) {  // in flight after an abort
@@ -579,11 +631,17 @@ __global__ void __launch_bounds__(threads(MODE), 1)
     // --------------------------------- epilogue ---------------------------------
     using R = Regs<MODE, kSum>;
     if constexpr (R::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::kEpi));
-    // Two groups of four warps take chunks of 32 columns in turn. A chunk goes through shared
-    // memory and leaves as TMA boxes of 128 m by 32 c (16 of fp32), 256 or 512 contiguous bytes
-    // a row. (Stored from registers, 64 bytes a row and warp, the weight gradient of 64 experts
-    // of 128 rows, 2048 x 4096, took 477 us for 1.07 GB.) A chunk that ends inside the tile of
-    // an expert's rows, an unaligned output and a 16-bit accumulation are stored from registers.
+    // Two groups of four warps take runs of 32 columns in turn. A run goes through shared memory
+    // and leaves by TMA. Transposed (product, input grad, fp32 weight grad): boxes of 128 m by 32 c
+    // (16 of fp32), 256 or 512 contiguous bytes a row, one for the four warps of a group; a run
+    // that ends inside the tile of an expert's rows is stored from registers. By rows (weight
+    // grad): boxes of 64 rows of 128 bytes, one for a pair of warps. By rows a lane writes 16
+    // bytes to shared memory at a time, transposed 2 or 4; transposed, memory is written in longer
+    // rows. Measured on the weight gradient of 64 experts, 2048 x 4096, transposed and by rows, us:
+    // bf16, 20 rows each 297, 250; 128 rows 308, 252; 700 rows 460, 473; fp32, 20 rows 355, 371;
+    // 128 rows 403, 423; 700 rows 600, 639. So 16-bit gradients go by rows, fp32 ones transposed.
+    // (From registers, 64 bytes a row and warp, bf16 at 128 rows took 477.) An unaligned output and
+    // a 16-bit accumulation are stored from registers.
     const int ew = warp - 4, quarter = warp & 3, half = ew >> 2;
     const bool leader = quarter == 0 && lane == 0;
     uint32_t acc = 0, box = 0;  // accumulators, output boxes so far
@@ -597,8 +655,8 @@ __global__ void __launch_bounds__(threads(MODE), 1)
       if (none && p.accumulate) continue;
       const int mc = t.m0 + (int)crank * 128, ml = 32 * quarter + lane, m = mc + ml;
       const int64_t first = (int64_t)t.e * p.out_expert + (int64_t)t.c0 * p.ld_out;
-      // 32 columns from c on, added to what memory holds or in place of it
-      auto emit = [&](int c, const float (&d)[32], bool add) {
+      // 32 columns from c on, transposed: written, or (`add`) added to what memory holds
+      auto emit_transposed = [&](int c, const float (&d)[32], bool add) {
         const int cols = t.cols - c;
         if (tma_out && (kWG || cols >= 32)) {  // (a weight gradient's edge is clipped by its tensor map)
           const int per = f32 ? 16 : 32;
@@ -652,6 +710,72 @@ __global__ void __launch_bounds__(threads(MODE), 1)
             store_columns<ElemF16>(static_cast<uint16_t*>(p.out) + o, p.ld_out, d, cols, m, p.m_dim, lane, words, add);
         }
       };
+      // Weight grad: 32 columns from c on of this warp's 32 rows (lane: row), added to what memory
+      // holds or in place of it. A pair of warps fills a box of 64 rows of 128 bytes; 16-bit calls
+      // come in twos, an even one fills the rows' first halves, an odd one the second and sends.
+      auto emit_rows = [&](int c, const float (&d)[32], bool add) {
+        if (tma_out) {  // (edges are clipped by the tensor map)
+          const int pair = 2 * half + (quarter >> 1);
+          const bool sender = (quarter & 1) == 0 && lane == 0;
+          uint8_t* ob = outbuf + (2 * pair + (int)(box & 1)) * kRowBuf;
+          const bool first_half = !f32 && (c & 32) == 0, sends = !first_half || c + 32 >= t.cols;
+          if (f32 || first_half) {
+            // the store that used this buffer two boxes ago has read it
+            if (sender) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            named_bar(3 + pair, 64);
+          }
+          const uint32_t row = smem_u32(ob) + (32 * (quarter & 1) + lane) * 128;
+          if (f32) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              st_shared_16(row + ((j ^ (lane & 7)) << 4), __float_as_uint(d[4 * j]), __float_as_uint(d[4 * j + 1]),
+                           __float_as_uint(d[4 * j + 2]), __float_as_uint(d[4 * j + 3]));
+          } else {
+            const int j0 = first_half ? 0 : 4;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                w[i] = p.out_dtype == FTMOE_OUT_BF16 ? pack2<ElemBf16>(d[8 * j + 2 * i], d[8 * j + 2 * i + 1])
+                                                     : pack2<ElemF16>(d[8 * j + 2 * i], d[8 * j + 2 * i + 1]);
+              st_shared_16(row + (((j0 + j) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+            }
+          }
+          if (sends) {
+            fence_async_shared();
+            named_bar(3 + pair, 64);
+            if (sender) {
+              const int x = t.c0 + (f32 ? c : c & ~32), y = mc + 64 * (quarter >> 1);
+              if (y < p.m_dim) {
+                if (add)
+                  tma_add_3d(&map_o, smem_u32(ob), x, y, t.e);
+                else
+                  tma_store_3d(&map_o, smem_u32(ob), x, y, t.e);
+              }
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+            ++box;
+          }
+        } else if (m < p.m_dim) {
+          const int64_t o = (int64_t)t.e * p.out_expert + (int64_t)m * p.ld_out + t.c0 + c;
+          const int cols = t.cols - c;
+          if (f32)
+            store_row<ElemF32>(static_cast<float*>(p.out) + o, d, cols, add);
+          else if (p.out_dtype == FTMOE_OUT_BF16)
+            store_row<ElemBf16>(static_cast<uint16_t*>(p.out) + o, d, cols, add);
+          else
+            store_row<ElemF16>(static_cast<uint16_t*>(p.out) + o, d, cols, add);
+        }
+      };
+      auto emit = [&](int c, const float (&d)[32], bool add) {
+        if constexpr (kRows)
+          emit_rows(c, d, add);
+        else
+          emit_transposed(c, d, add);
+      };
+      // the first column of this half's i-th run of 32 (by rows: runs in pairs)
+      auto column = [&](int i) { return kRows ? 64 * half + 128 * (i >> 1) + 32 * (i & 1) : 32 * half + 64 * i; };
       auto wait_acc = [&]() {
         const int got = mbar_wait(smem_u32(&tfull[acc & 1]), (acc >> 1) & 1, &s_abort) ? 1 : 0;
         // the group's warps share barriers in emit: they leave together
@@ -678,7 +802,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
           if (!ok) break;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int c = 32 * half + 64 * i;
+            const int c = column(i);
             if (c < t.cols) {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
@@ -695,7 +819,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
         if (!ok) break;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (32 * half + 64 * i < t.cols) emit(32 * half + 64 * i, sum[i], p.accumulate != 0);
+          if (column(i) < t.cols) emit(column(i), sum[i], p.accumulate != 0);
       } else {
         bool ok = true;
         for (int q = 0; q < parts; ++q) {
@@ -704,9 +828,11 @@ __global__ void __launch_bounds__(threads(MODE), 1)
             if (!ok) break;
           }
           // a part is added to what the parts before it have left in memory
-          if (q > 0 && leader) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+          if (q > 0 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
           bool held = !none;
-          for (int c = 32 * half; c < t.cols; c += 64) {
+          for (int i = 0; i < 4; ++i) {
+            const int c = column(i);
+            if (c >= t.cols) break;
             float d[32];
             if (none) {
 #pragma unroll
@@ -714,7 +840,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
             } else {
               tmem_ld<32>(lanes + (acc & 1) * kN + c, d);
               tmem_ld_wait();
-              if (c + 64 >= t.cols) {
+              if (i == 3 || column(i + 1) >= t.cols) {
                 release_acc();
                 held = false;
               }
@@ -727,11 +853,11 @@ __global__ void __launch_bounds__(threads(MODE), 1)
         if (!ok) break;
       }
     }
-    if (leader) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   } else if constexpr (kSaved) {
     // ------------------------ saved rows: decode ------------------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<MODE, kSum>::kDec));
-    // Four teams of four warps take stages in turn, so that some decode while others wait for
+    // Three teams of four warps take stages in turn, so that some decode while others wait for
     // codes, for a free operand slot or for their stores to be visible. Thread (warp dw of the
     // team, lane): lines r0 + 16 v of the stage's 64, r0 = 8 dw + lane % 8, and the 32-wide group
     // lane / 8 of their 128 codes. Eight lanes with consecutive lines touch eight different
@@ -739,14 +865,14 @@ __global__ void __launch_bounds__(threads(MODE), 1)
     const int dw = (warp - 4 - kEpiWarps) % kTeamWarps, team = (warp - 4 - kEpiWarps) / kTeamWarps;
     const int r0 = 8 * dw + (lane & 7), grp = lane >> 3;
     constexpr int kLines = 64 / (8 * kTeamWarps);
-    const int kg = p.m_dim / kMxBlock;
+    const int kg = p.c_dim / kMxBlock;
     uint32_t it = 0, tph = 0;  // tph, bit st: uses of lfull[st], mod 2 (every team counts them all)
     bool ok = true;
     for (int64_t u = u_begin; u < u_end && ok; u += u_step) {
       Unit t;
       decode((int)u, t);
       const int steps = (t.len + kBK - 1) / kBK;
-      const int g = (t.m0 + (int)crank * 128) / kMxBlock + grp;
+      const int g = (t.c0 + (int)crank * (t.n >> 1)) / kMxBlock + grp;
       // scale bytes, fetched one of the team's stages ahead of their codes
       uint32_t next = 0;
       auto fetch = [&](int s) {
@@ -758,7 +884,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
           next |= b << (8 * v);
         }
       };
-      int s = (int)(((uint32_t)team - it) % kDecTeams);
+      int s = (int)((team + kDecTeams - it % kDecTeams) % kDecTeams);
       fetch(s);
       const bool ragged = t.len % kBK != 0;
       for (; s < steps; s += kDecTeams) {
@@ -774,7 +900,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
         if (tail) ok = ok && mbar_wait(smem_u32(&lfull[st]), tph >> st & 1, &s_abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint32_t ta = smem_u32(tiles + (size_t)st * kStage), raw = smem_u32(raws + raw_slot * kRaw);
+        const uint32_t ta = smem_u32(tiles + (size_t)st * kStage), tb = ta + kTile, raw = smem_u32(raws + raw_slot * kRaw);
         // (the element type is chosen outside the loops)
         auto lines = [&](auto elem) {
           using Elem = decltype(elem);
@@ -784,7 +910,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
             const bool live = r < left;
             const float sc = e8m0_to_f((uint8_t)(scales >> (8 * v)));
             // columns 32 grp + 16 h .. + 15: two 16-byte columns of the line in box grp / 2
-            const uint32_t line = ta + (grp >> 1) * (kTile / 2) + r * 128;
+            const uint32_t line = tb + (grp >> 1) * (kTile / 2) + r * 128;
             uint4 c[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -820,7 +946,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
             const int r = r0 + 8 * kTeamWarps * v;
             if (r < left) continue;
             // dy's line past the segment's end: this thread's quarter of both 64-column boxes
-            const uint32_t line = ta + kTile + r * 128;
+            const uint32_t line = ta + r * 128;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int chunk = grp * 4 + k;
@@ -866,21 +992,21 @@ static bool encode16(CUtensorMap* map, const void* base, int rank, const uint64_
   return encode(map, base, CU_TENSOR_MAP_DATA_TYPE_UINT16, rank, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Output boxes; false (and an unused map) where rows do not start on 16-byte boundaries.
-static bool encode_out(CUtensorMap* map, void* base, int32_t dtype, uint64_t m, uint64_t rows, uint64_t E, int64_t ld,
-                       int64_t expert) {
+// Output boxes of `cols` elements by `rows` rows; false (and an unused map) where rows of memory do
+// not start on 16-byte boundaries.
+static bool encode_out(CUtensorMap* map, void* base, int32_t dtype, uint64_t width, uint64_t height, uint64_t E, int64_t ld,
+                       int64_t expert, uint32_t cols, uint32_t rows, CUtensorMapSwizzle swizzle) {
   const bool f32 = dtype == FTMOE_OUT_FP32;
   const int64_t b = f32 ? 4 : 2;
   if ((uintptr_t)base % 16 != 0 || ld * b % 16 != 0 || (E > 1 && expert * b % 16 != 0)) return false;
-  const uint64_t dims[3] = {m, rows, E}, st[2] = {(uint64_t)(ld * b), (uint64_t)(E > 1 ? expert * b : ld * b)};
-  const uint32_t box[3] = {128, f32 ? 16u : 32u, 1};
-  return encode(map, base, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, dims, st, box,
-                CU_TENSOR_MAP_SWIZZLE_NONE);
+  const uint64_t dims[3] = {width, height, E}, st[2] = {(uint64_t)(ld * b), (uint64_t)(E > 1 ? expert * b : ld * b)};
+  const uint32_t box[3] = {cols, rows, 1};
+  return encode(map, base, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, dims, st, box, swizzle);
 }
 
 template <int MODE, bool kSum>
 static cudaError_t launch(const CUtensorMap* maps, const Params& p, cudaStream_t st, int* unsupported) {
-  const size_t smem = 1024 + (size_t)smem_bytes(MODE) + (is_wgrad(MODE) ? 0 : ((size_t)p.E + 1) * 4);
+  const size_t smem = 1024 + (size_t)smem_bytes(MODE) + (is_wgrad(MODE) ? 0 : ((size_t)p.E + 1) * 8);
   int dev = 0;
   cudaGetDevice(&dev);
   // per device: CTA pairs that can be resident at once, with the largest shared memory this
@@ -888,7 +1014,7 @@ static cudaError_t launch(const CUtensorMap* maps, const Params& p, cudaStream_t
   static int pairs[64] = {};
   int np = dev >= 0 && dev < 64 ? pairs[dev] : 0;
   if (np == 0) {
-    const size_t most = 1024 + (size_t)smem_bytes(MODE) + (is_wgrad(MODE) ? 0 : (kMaxExperts + 1) * 4);
+    const size_t most = 1024 + (size_t)smem_bytes(MODE) + (is_wgrad(MODE) ? 0 : (size_t)(kMaxExperts + 1) * 8);
     const cudaError_t e =
         cudaFuncSetAttribute(tc_matmul16_kernel<MODE, kSum>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (e != cudaSuccess) return e;
@@ -949,7 +1075,8 @@ cudaError_t launch_tc_matmul16(const Matmul16Args& a, cudaStream_t st, int* unsu
     p.m_dim = (int)m;
     p.l_dim = (int)l;
     p.out_dtype = a.out_dtype;
-    p.tma_out = encode_out(&maps[5], a.out, a.out_dtype, (uint64_t)m, R, 1, a.ld_out, 0);
+    p.tma_out = encode_out(&maps[5], a.out, a.out_dtype, (uint64_t)m, R, 1, a.ld_out, 0, 128,
+                           a.out_dtype == FTMOE_OUT_FP32 ? 16 : 32, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (!p.tma_out) maps[5] = maps[0];
     *unsupported = 0;
     p.chunk = kNoChunk;
@@ -959,45 +1086,47 @@ cudaError_t launch_tc_matmul16(const Matmul16Args& a, cudaStream_t st, int* unsu
     }
     return a.input_grad ? launch<kInputGrad, false>(maps, p, st, unsupported) : launch<kProduct, false>(maps, p, st, unsupported);
   }
-  if (!tma16(a.a, a.ld_a) || E * cdiv(w.k, kM) * cdiv(w.n, kN) > 0x7fffffff) return cudaSuccess;
+  if (!tma16(a.a, a.ld_a) || E * cdiv(w.n, kM) * cdiv(w.k, kN) > 0x7fffffff) return cudaSuccess;
+  const bool f32 = w.dtype == FTMOE_OUT_FP32, transposed = f32 && !a.x_scales;
+  CUtensorMap &mdy = maps[transposed ? 1 : 0], &mx = maps[transposed ? 0 : 1];
   const uint64_t dd[2] = {(uint64_t)w.n, R}, ds[1] = {2 * (uint64_t)a.ld_a};
   const uint32_t box[2] = {64, 64};
-  if (!encode16(&maps[1], a.a, 2, dd, ds, box)) return cudaSuccess;
-  maps[2] = maps[3] = maps[4] = maps[1];
+  if (!encode16(&mdy, a.a, 2, dd, ds, box)) return cudaSuccess;
   const uint64_t xd[2] = {(uint64_t)w.k, R};
   if (a.x_scales) {
     if ((uintptr_t)a.x % 16 != 0 || a.ld_x % 16 != 0) return cudaSuccess;
     const uint64_t xs[1] = {(uint64_t)a.ld_x};
     const uint32_t xb[2] = {128, 64};
-    if (!encode_u8_tmap(&maps[0], a.x, 2, xd, xs, xb)) return cudaSuccess;
+    if (!encode_u8_tmap(&mx, a.x, 2, xd, xs, xb)) return cudaSuccess;
   } else {
     if (!tma16(a.x, a.ld_x)) return cudaSuccess;
     const uint64_t xs[1] = {2 * (uint64_t)a.ld_x};
-    if (!encode16(&maps[0], a.x, 2, xd, xs, box)) return cudaSuccess;
+    if (!encode16(&mx, a.x, 2, xd, xs, box)) return cudaSuccess;
   }
+  maps[2] = maps[3] = maps[4] = maps[1];
   p.x_scales = a.x_scales;
   p.out = w.w;
   p.ld_out = w.ld;
   p.out_expert = w.expert_stride;
-  p.m_dim = (int)w.k;
-  p.c_dim = (int)w.n;
+  p.m_dim = (int)(transposed ? w.k : w.n);
+  p.c_dim = (int)(transposed ? w.n : w.k);
   p.out_dtype = w.dtype;
   p.accumulate = a.accumulate;
-  p.tma_out = encode_out(&maps[5], w.w, w.dtype, (uint64_t)w.k, (uint64_t)w.n, (uint64_t)E, w.ld, w.expert_stride);
+  p.tma_out = encode_out(&maps[5], w.w, w.dtype, (uint64_t)w.k, (uint64_t)w.n, (uint64_t)E, w.ld, w.expert_stride,
+                         transposed ? 128 : f32 ? 32 : 64, transposed ? 16 : 64,
+                         transposed ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B);
   if (!p.tma_out) maps[5] = maps[0];
   *unsupported = 0;
-  // (the longest segment is known on the device only: at most all rows)
-  const bool f32 = w.dtype == FTMOE_OUT_FP32;
-  p.chunk = kNoChunk;
-  if (a.x_scales) {
-    if (f32) p.chunk = kAddStages;
-    return launch<kWeightGradSaved, false>(maps, p, st, unsupported);
-  }
-  if (f32 && a.rows > kSumStages * kBK) {
+  p.chunk = f32 ? kAddStages : kNoChunk;
+  if (a.x_scales) return launch<kWeightGradSaved, false>(maps, p, st, unsupported);
+  if (!f32) return launch<kWeightGrad, false>(maps, p, st, unsupported);
+  // Segments that are long on average are summed in registers; otherwise the few that are long
+  // are added in memory and the rest need neither.
+  if (a.rows > E * kSumStages * kBK) {
     p.chunk = kSumStages;
-    return launch<kWeightGrad, true>(maps, p, st, unsupported);
+    return launch<kWeightGradT, true>(maps, p, st, unsupported);
   }
-  return launch<kWeightGrad, false>(maps, p, st, unsupported);
+  return launch<kWeightGradT, false>(maps, p, st, unsupported);
 }
 
 FTMOE_DEFINE_ERR_READER(read_err_tc_matmul16)

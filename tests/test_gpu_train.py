@@ -288,9 +288,9 @@ def test_weight_gradient_strides(pad, shift):
 @pytest.mark.parametrize("kind", ["product", "input_grad", "weight_grad", "saved"])
 @pytest.mark.parametrize("accumulate", [False, True])
 def test_long_sums_keep_fp32(kind, accumulate):
-    """fp32 outputs of long contractions. An accumulator takes 512 terms in 32 additions (2,048 in
-    128 from saved rows), each losing at most 2^-23 of the partial sum, and the partial sums are
-    of the result's size (independent terms): the error's norm is below 32 (128) 2^-23 of it."""
+    """fp32 outputs of long contractions. An accumulator takes 512 terms in 32 additions (up to
+    2,048 in 128 from saved rows), each losing at most 2^-23 of the partial sum, and the partial
+    sums are of the result's size (independent terms): the error's norm is below 32 (128) 2^-23 of it."""
     if accumulate and kind in ("product", "input_grad"):
         pytest.skip("only weight gradients accumulate")
     counts, long, m = [1, 9000, 300], 16384, 136
