@@ -11,8 +11,8 @@
 //   weight grad   A = dy (MN-major)                 B = x (MN-major)          l: rows, m: i, c: j
 // The first two keep the ragged axis in c and store the result transposed, out[c, m]: the 32
 // lanes of an epilogue warp, 32 consecutive m of one column, write consecutive addresses. The
-// weight gradient's accumulator is a tile of dw as it lies in memory, or (fp32) its transpose,
-// with A and B exchanged.
+// weight gradient's accumulator is a tile of dw as it lies in memory, or (fp32, long segments) its
+// transpose, with A and B exchanged.
 // One kernel therefore serves one row per expert and thousands: an expert's m_e rows make
 // ceil(m_e / 256) column tiles of equal width, rounded up to 32.
 //
@@ -56,7 +56,7 @@ namespace ftmoe {
 namespace tc16 {
 
 // kWeightGradT: the weight gradient with the operands' roles exchanged (A = x, B = dy), stored
-// transposed like the product: fp32 outputs, see the epilogue
+// transposed like the product: fp32 outputs and long segments, see the epilogue
 enum Mode { kProduct = 0, kInputGrad = 1, kWeightGrad = 2, kWeightGradSaved = 3, kWeightGradT = 4 };
 
 constexpr int kBK = 64;                   // elements of l per stage: one 128-byte swizzle atom
@@ -639,7 +639,8 @@ __global__ void __launch_bounds__(threads(MODE), 1)
     // bytes to shared memory at a time, transposed 2 or 4; transposed, memory is written in longer
     // rows. Measured on the weight gradient of 64 experts, 2048 x 4096, transposed and by rows, us:
     // bf16, 20 rows each 297, 250; 128 rows 308, 252; 700 rows 460, 473; fp32, 20 rows 355, 371;
-    // 128 rows 403, 423; 700 rows 600, 639. So 16-bit gradients go by rows, fp32 ones transposed.
+    // 128 rows 403, 423; 700 rows 600, 639. So 16-bit gradients of segments of up to 512 rows on
+    // average go by rows, others and fp32 ones transposed.
     // (From registers, 64 bytes a row and warp, bf16 at 128 rows took 477.) An unaligned output and
     // a 16-bit accumulation are stored from registers.
     const int ew = warp - 4, quarter = warp & 3, half = ew >> 2;
@@ -1087,7 +1088,9 @@ cudaError_t launch_tc_matmul16(const Matmul16Args& a, cudaStream_t st, int* unsu
     return a.input_grad ? launch<kInputGrad, false>(maps, p, st, unsupported) : launch<kProduct, false>(maps, p, st, unsupported);
   }
   if (!tma16(a.a, a.ld_a) || E * cdiv(w.n, kM) * cdiv(w.k, kN) > 0x7fffffff) return cudaSuccess;
-  const bool f32 = w.dtype == FTMOE_OUT_FP32, transposed = f32 && !a.x_scales;
+  // see the epilogue: by rows for 16-bit outputs of segments that are short on average
+  const bool f32 = w.dtype == FTMOE_OUT_FP32, long_segments = a.rows > E * kSumStages * kBK;
+  const bool transposed = !a.x_scales && (f32 || long_segments);
   CUtensorMap &mdy = maps[transposed ? 1 : 0], &mx = maps[transposed ? 0 : 1];
   const uint64_t dd[2] = {(uint64_t)w.n, R}, ds[1] = {2 * (uint64_t)a.ld_a};
   const uint32_t box[2] = {64, 64};
@@ -1113,16 +1116,16 @@ cudaError_t launch_tc_matmul16(const Matmul16Args& a, cudaStream_t st, int* unsu
   p.out_dtype = w.dtype;
   p.accumulate = a.accumulate;
   p.tma_out = encode_out(&maps[5], w.w, w.dtype, (uint64_t)w.k, (uint64_t)w.n, (uint64_t)E, w.ld, w.expert_stride,
-                         transposed ? 128 : f32 ? 32 : 64, transposed ? 16 : 64,
+                         transposed ? 128 : f32 ? 32 : 64, !transposed ? 64 : f32 ? 16 : 32,
                          transposed ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B);
   if (!p.tma_out) maps[5] = maps[0];
   *unsupported = 0;
   p.chunk = f32 ? kAddStages : kNoChunk;
   if (a.x_scales) return launch<kWeightGradSaved, false>(maps, p, st, unsupported);
-  if (!f32) return launch<kWeightGrad, false>(maps, p, st, unsupported);
-  // Segments that are long on average are summed in registers; otherwise the few that are long
-  // are added in memory and the rest need neither.
-  if (a.rows > E * kSumStages * kBK) {
+  if (!transposed) return launch<kWeightGrad, false>(maps, p, st, unsupported);
+  // fp32: segments that are long on average are summed in registers; otherwise the few that are
+  // long are added in memory and the rest need neither.
+  if (f32 && long_segments) {
     p.chunk = kSumStages;
     return launch<kWeightGradT, true>(maps, p, st, unsupported);
   }

@@ -82,6 +82,7 @@ SHAPES = [
     ([5, 9], 33, 47),      # widths that no 16-byte copy takes
     ([17, 1, 64], 1, 7),
     ([64] * 9, 8, 1024),
+    ([1, 1200], 264, 136),  # segments long on average
 ]
 
 
