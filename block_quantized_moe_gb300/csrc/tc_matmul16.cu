@@ -994,12 +994,13 @@ static bool encode16(CUtensorMap* map, const void* base, int rank, const uint64_
 }
 
 // Output boxes of `cols` elements by `rows` rows; false (and an unused map) where rows of memory do
-// not start on 16-byte boundaries.
+// not start on 16-byte boundaries, or do not end on one: a TMA store cut off inside 16 bytes writes
+// all of them (measured: seven bf16 past rows of 33).
 static bool encode_out(CUtensorMap* map, void* base, int32_t dtype, uint64_t width, uint64_t height, uint64_t E, int64_t ld,
                        int64_t expert, uint32_t cols, uint32_t rows, CUtensorMapSwizzle swizzle) {
   const bool f32 = dtype == FTMOE_OUT_FP32;
   const int64_t b = f32 ? 4 : 2;
-  if ((uintptr_t)base % 16 != 0 || ld * b % 16 != 0 || (E > 1 && expert * b % 16 != 0)) return false;
+  if ((uintptr_t)base % 16 != 0 || ld * b % 16 != 0 || (E > 1 && expert * b % 16 != 0) || width * b % 16 != 0) return false;
   const uint64_t dims[3] = {width, height, E}, st[2] = {(uint64_t)(ld * b), (uint64_t)(E > 1 ? expert * b : ld * b)};
   const uint32_t box[3] = {cols, rows, 1};
   return encode(map, base, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, dims, st, box, swizzle);

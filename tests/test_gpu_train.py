@@ -136,6 +136,41 @@ def test_product_strides_and_rows_past_the_end(pad, shift, input_grad):
     assert int((~torch.isnan(base)).sum()) == R * outw
 
 
+@pytest.mark.parametrize("counts,n,k", [([3, 0, 70], 33, 47), ([130, 300], 257, 131), ([40], 1, 1), ([600, 500], 391, 259)])
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+def test_odd_widths_in_aligned_rows(counts, n, k, out):
+    """Widths that no vector divides, in rows whose starts are 16-byte aligned: the copies end
+    inside a vector, and what pads the rows (NaN) is neither used nor written."""
+    R, E = sum(counts), len(counts)
+    off = offsets_of(counts)
+
+    def padded(shape, dtype, std=None, seed=0):
+        base, t = strided(shape, -shape[-1] % 8 + 8, 0, dtype)
+        if std is not None:
+            t.copy_(normal(shape, std, dtype, seed))
+        return base, t
+    _, a = padded((R, k), torch.bfloat16, 1.0, 71)
+    _, c = padded((R, n), torch.bfloat16, 0.5, 72)
+    _, w = padded((E, n, k), torch.bfloat16, 0.1, 73)
+    by, y = padded((R, n), DT[out])
+    ft.ftmoe_grouped_matmul(a, off, w, y)
+    ref, mag = product_ref(a, w, counts, False)
+    check(y, ref, mag, k, "product")
+    bd, da = padded((R, k), DT[out])
+    ft.ftmoe_grouped_matmul(c, off, w, da, input_grad=True)
+    ref, mag = product_ref(c, w, counts, True)
+    check(da, ref, mag, n, "input gradient")
+    bw, dw = padded((E, n, k), DT[out])
+    ft.ftmoe_grouped_matmul_wgrad(c, a, off, dw)
+    ref, mag = wgrad_ref(c, a, counts)
+    check(dw, ref, mag, max(counts), "weight gradient")
+    ft.ftmoe_grouped_matmul_wgrad(c, a, off, dw, accumulate=True)
+    check(dw, 2 * ref, 2 * mag + ref.abs(), max(counts) + 2 + (2 ** 15 if out == "bf16" else 0), "accumulated")
+    for base, t in ((by, y), (bd, da), (bw, dw)):
+        assert int((~torch.isnan(base)).sum()) == t.numel()
+    assert ft.ftmoe_read_error_flags() == 0
+
+
 @pytest.mark.parametrize("input_grad", [False, True])
 def test_product_keeps_infinities_and_nan_in_their_rows(input_grad):
     """A NaN or infinite row of one expert changes no other row, and gives NaN or infinities itself."""
