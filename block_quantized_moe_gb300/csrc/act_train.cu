@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(256, 4) silu_backward_kernel(
 
 // Four CTAs per SM (64 registers a thread), each walking its share of the rows.
 static int grid_for(int64_t rows, int tpr) {
-  const int64_t blocks = cdiv(rows, 256 / tpr), cap = (int64_t)sm_count() * 4;
+  const int64_t blocks = cdiv(rows, 256 / tpr), cap = (int64_t)sm_count_once() * 4;
   return (int)(blocks < cap ? blocks : cap);
 }
 

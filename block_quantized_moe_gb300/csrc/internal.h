@@ -90,6 +90,14 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiledFn encode_fn();  // cuTensorMapEncodeTiled from the driver, or NULL
 int sm_count();
+// sm_count of the current device, asked for once per device (calls of a few microseconds)
+inline int sm_count_once() {
+  static int known[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sm_count();
+  if (known[dev] == 0) known[dev] = sm_count();
+  return known[dev];
+}
 // 128B-swizzled uint8 tensor map of rank 2 or 3 (dims innermost first, byte strides of the
 // outer dims); false if the driver entry point is missing or the encoding is rejected
 bool encode_u8_tmap(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,

@@ -147,7 +147,7 @@ cudaError_t launch_stream_matmul16(const Matmul16Args& a, cudaStream_t st) {
   p.out = a.out;
   p.ld_out = a.ld_out;
   p.out_dtype = a.out_dtype;
-  const int64_t units = (a.rows < p.E ? a.rows : p.E) * cdiv(w.n, kWarps), cap = (int64_t)sm_count() * 4;
+  const int64_t units = (a.rows < p.E ? a.rows : p.E) * cdiv(w.n, kWarps), cap = (int64_t)sm_count_once() * 4;
   const int grid = (int)(units < cap ? units : cap);
   return launch_kernel(a.dtype == FTMOE_OUT_BF16 ? stream_matmul16_kernel<ElemBf16> : stream_matmul16_kernel<ElemF16>,
                        dim3(grid), dim3(32 * kWarps), 0, st, false, p);

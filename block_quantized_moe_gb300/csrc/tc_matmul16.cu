@@ -344,6 +344,14 @@ __global__ void __launch_bounds__(threads(MODE), 1)
   const int MB = (p.m_dim + kM - 1) / kM;
   const int CB = kWG ? (p.c_dim + kN - 1) / kN : 0;
 
+  if (threadIdx.x < 6) {  // the descriptors are fetched while the rest is set up
+    const CUtensorMap* maps[6] = {&map_a, &map_b0, &map_b1, &map_b2, &map_b3, &map_o};
+    const CUtensorMap* m = maps[0];
+#pragma unroll
+    for (int i = 1; i < 6; ++i)
+      if (threadIdx.x == i) m = maps[i];
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+  }
   auto cut = [&](int v) { return v < 0 ? 0 : v > p.rows ? (int)p.rows : v; };
   if constexpr (!kWG)
     for (int e = threadIdx.x; e <= p.E; e += blockDim.x) seg[e] = cut(__ldg(p.offsets + e));
