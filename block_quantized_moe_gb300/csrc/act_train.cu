@@ -142,6 +142,8 @@ __global__ void __launch_bounds__(256, 4) silu_save_kernel(
     const int32_t* __restrict__ rows_dev, typename Out::T* __restrict__ h, int64_t ld_h, uint8_t* __restrict__ q,
     void* __restrict__ scales, bool vec_gu, bool vec_h, bool vec_q) {
   const int nb = (int)(kMx ? inter / kMxBlock : (inter + kGroup - 1) / kGroup);
+  pdl_wait();
+  pdl_trigger();
   Walk<kTpr> at(valid_rows(rows, rows_dev), inter);
   auto load = [&](Raw8<In>& g, Raw8<In>& u) {
     const typename In::T* gr = gu + at.row * ld_gu + at.c0;
@@ -215,6 +217,8 @@ __global__ void __launch_bounds__(256, 4) silu_backward_kernel(
   __shared__ float part[2][8];
   const int sub = threadIdx.x / kTpr, tid = threadIdx.x % kTpr, lane = threadIdx.x & 31;
   const int nb = (int)(kMx ? inter / kMxBlock : (inter + kGroup - 1) / kGroup);
+  pdl_wait();
+  pdl_trigger();
   Walk<kTpr> at(valid_rows(rows, rows_dev), inter);
   struct Operands {
     uint2 g, u;
@@ -326,7 +330,8 @@ cudaError_t launch_silu_save(const SiluSaveArgs& a, cudaStream_t st) {
         const bool vh = elem_vec_ok(a.h, a.ld_h, sizeof(typename Out::T));
         const bool vq = (uintptr_t)a.q % 8 == 0 && a.inter % 8 == 0;
         auto k = a.mx ? silu_save_kernel<In, Out, true, kTpr> : silu_save_kernel<In, Out, false, kTpr>;
-        return launch_kernel(k, dim3(grid_for(a.rows, kTpr)), dim3(256), 0, st, false,
+        const OverlapLaunch overlap;
+        return launch_kernel(k, dim3(grid_for(a.rows, kTpr)), dim3(256), 0, st, true,
                              static_cast<const typename In::T*>(a.gu), a.rows, a.inter, a.ld_gu, a.rows_dev,
                              static_cast<typename Out::T*>(a.h), a.ld_h, a.q, a.scales, vg, vh, vq);
       });
@@ -346,7 +351,8 @@ cudaError_t launch_silu_backward(const SiluBackwardArgs& a, cudaStream_t st) {
     return with_threads_per_row(a.inter, [&](auto t) {
       constexpr int kTpr = decltype(t)::value;
       auto k = a.mx ? silu_backward_kernel<E, true, kTpr> : silu_backward_kernel<E, false, kTpr>;
-      return launch_kernel(k, dim3(grid_for(a.rows, kTpr)), dim3(256), 0, st, false, a.q, a.scales, a.rows, a.inter,
+      const OverlapLaunch overlap;
+      return launch_kernel(k, dim3(grid_for(a.rows, kTpr)), dim3(256), 0, st, true, a.q, a.scales, a.rows, a.inter,
                            a.rows_dev, static_cast<const T*>(a.dh), a.ld_dh, a.row_weights, static_cast<T*>(a.dgu),
                            a.ld_dgu, static_cast<T*>(a.hw), a.ld_hw, a.dweights, vq, vd, vgu, vhw);
     });

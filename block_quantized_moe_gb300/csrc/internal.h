@@ -25,6 +25,15 @@ inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // before it triggers.
 bool& pdl_enabled();
 
+// Lets the launches in its scope overlap the previous kernel's end (see pdl_enabled). The training
+// kernels do so on every call: they read and write nothing before their own wait, so that only
+// their launch and setup move under the predecessor, whatever it is.
+struct OverlapLaunch {
+  const bool before;
+  OverlapLaunch() : before(pdl_enabled()) { pdl_enabled() = true; }
+  ~OverlapLaunch() { pdl_enabled() = before; }
+};
+
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
                                  bool allow_overlap, Args... args) {

@@ -53,6 +53,8 @@ __global__ void __launch_bounds__(32 * kWarps) stream_matmul16_kernel(Params p) 
   __shared__ int s_e[32 * kWarps], s_lo[32 * kWarps], s_m[32 * kWarps], s_count[kWarps + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int blocks = (p.n + kWarps - 1) / kWarps;
+  pdl_wait();
+  pdl_trigger();
   // 256 experts at a time: those that have rows, in order
   for (int base = 0; base < p.E; base += 32 * kWarps) {
     const int e = base + threadIdx.x;
@@ -149,8 +151,9 @@ cudaError_t launch_stream_matmul16(const Matmul16Args& a, cudaStream_t st) {
   p.out_dtype = a.out_dtype;
   const int64_t units = (a.rows < p.E ? a.rows : p.E) * cdiv(w.n, kWarps), cap = (int64_t)sm_count_once() * 4;
   const int grid = (int)(units < cap ? units : cap);
+  const OverlapLaunch overlap;
   return launch_kernel(a.dtype == FTMOE_OUT_BF16 ? stream_matmul16_kernel<ElemBf16> : stream_matmul16_kernel<ElemF16>,
-                       dim3(grid), dim3(32 * kWarps), 0, st, false, p);
+                       dim3(grid), dim3(32 * kWarps), 0, st, true, p);
 }
 
 }  // namespace ftmoe

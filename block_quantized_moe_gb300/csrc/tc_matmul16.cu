@@ -352,15 +352,6 @@ __global__ void __launch_bounds__(threads(MODE), 1)
       if (threadIdx.x == i) m = maps[i];
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
   }
-  auto cut = [&](int v) { return v < 0 ? 0 : v > p.rows ? (int)p.rows : v; };
-  if constexpr (!kWG)
-    for (int e = threadIdx.x; e <= p.E; e += blockDim.x) seg[e] = cut(__ldg(p.offsets + e));
-  // (weight grad: one expert has many units in a row, its offsets stay in L1)
-  auto bounds = [&](int e, int& lo, int& hi) {
-    lo = kWG ? cut(__ldg(p.offsets + e)) : seg[e];
-    hi = max(lo, kWG ? cut(__ldg(p.offsets + e + 1)) : seg[e + 1]);
-  };
-
   if (threadIdx.x == 0) {
     s_abort = 0;
     for (int i = 0; i < S; ++i) {
@@ -381,6 +372,22 @@ __global__ void __launch_bounds__(threads(MODE), 1)
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  // everything so far overlaps the end of the previous kernel, whose results are complete from here on
+  pdl_wait();
+  pdl_trigger();
+  auto cut = [&](int v) { return v < 0 ? 0 : v > p.rows ? (int)p.rows : v; };
+  if constexpr (!kWG)
+    for (int e = threadIdx.x; e <= p.E; e += blockDim.x) seg[e] = cut(__ldg(p.offsets + e));
+  // (weight grad: one expert has many units in a row, its offsets stay in L1)
+  auto bounds = [&](int e, int& lo, int& hi) {
+    lo = kWG ? cut(__ldg(p.offsets + e)) : seg[e];
+    hi = max(lo, kWG ? cut(__ldg(p.offsets + e + 1)) : seg[e + 1]);
+  };
+
   __syncthreads();
   if constexpr (!kWG) {
     if (warp == 0) {
@@ -405,10 +412,6 @@ __global__ void __launch_bounds__(threads(MODE), 1)
       }
       if (lane == 0) cum[p.E] = (int)min(run, (long long)0x7fffffff);
     }
-  }
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
   fence_before();
   cluster_sync();  // both CTAs' barriers are initialised before either reports to the other
@@ -862,7 +865,8 @@ __global__ void __launch_bounds__(threads(MODE), 1)
         if (!ok) break;
       }
     }
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    // (their shared memory has been read; the writes complete with the kernel)
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   } else if constexpr (kSaved) {
     // ------------------------ saved rows: decode ------------------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<MODE, kSum>::kDec));
@@ -1043,7 +1047,8 @@ static cudaError_t launch(const CUtensorMap* maps, const Params& p, cudaStream_t
     *unsupported = 1;
     return cudaSuccess;
   }
-  return launch_kernel_cluster(tc_matmul16_kernel<MODE, kSum>, dim3(2 * np), dim3(threads(MODE)), smem, st, false, 2, maps[0],
+  const OverlapLaunch overlap;
+  return launch_kernel_cluster(tc_matmul16_kernel<MODE, kSum>, dim3(2 * np), dim3(threads(MODE)), smem, st, true, 2, maps[0],
                                maps[1], maps[2], maps[3], maps[4], maps[5], p);
 }
 
