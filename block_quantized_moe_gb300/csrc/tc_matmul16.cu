@@ -28,7 +28,7 @@
 // step of a segment lands on a barrier of its own; a warp then zeroes the rows past the
 // segment, in A and in B (what is there may be NaN), up to the next multiple of 16, and hands
 // the stage to the MMA issuer, which runs only the 16-row steps that hold rows.
-// From saved rows (MXFP8), B arrives as codes; twelve warps decode them into the operand tile,
+// From saved rows (MXFP8), B arrives as codes; teams of warps decode them into the operand tile,
 // a 32-wide group with its power-of-two scale at a time, exactly.
 //
 // Long sums. The tensor core cuts low bits off as it adds a product to its fp32 accumulator: the
@@ -41,7 +41,7 @@
 // are longer in memory, by TMA.
 //
 // Roles: warp 0 TMA, warp 1 MMA issue and TMEM, warp 2 segment tails (weight grad) or codes
-// (saved rows), warps 4-11 epilogue, warps 12-23 decode (saved rows). Every mbarrier wait is bounded: on timeout the
+// (saved rows), warps 4-11 epilogue, warps 12 on decode (saved rows). Every mbarrier wait is bounded: on timeout the
 // kernel raises FTMOE_ERR_WAIT_TIMEOUT, stops its roles, waits for its own loads and MMAs,
 // frees its TMEM and returns.
 #include <cuda.h>
@@ -57,37 +57,42 @@ namespace tc16 {
 
 // kWeightGradT: the weight gradient with the operands' roles exchanged (A = x, B = dy), stored
 // transposed like the product: fp32 outputs and long segments, see the epilogue
-enum Mode { kProduct = 0, kInputGrad = 1, kWeightGrad = 2, kWeightGradSaved = 3, kWeightGradT = 4 };
+// kWeightGradSavedLong: kWeightGradSaved for segments that are long on average
+enum Mode { kProduct = 0, kInputGrad = 1, kWeightGrad = 2, kWeightGradSaved = 3, kWeightGradT = 4, kWeightGradSavedLong = 5 };
 
 constexpr int kBK = 64;                   // elements of l per stage: one 128-byte swizzle atom
 constexpr int kM = 256, kN = 256;         // of the pair
 constexpr int kTile = 128 * kBK * 2;      // 16 KiB: this CTA's half of A, and of B at most
 constexpr int kRaw = 128 * kBK;           // saved rows: 8 KiB of codes
-constexpr int kRawSlots = 3;
 constexpr int kOutBuf = 8192;             // an output box: 32 columns of c (16 of fp32) by 128 of m
 constexpr int kOutBufs = 3;               // boxes in flight for each half of the epilogue
-constexpr int kEpiWarps = 8, kDecWarps = 12, kDecTeams = 3, kTeamWarps = kDecWarps / kDecTeams;
-// A team meets each code slot in every one of its phases: waiting by parity, it could take a
-// phase that another team has yet to see for its own.
-static_assert(kRawSlots % kDecTeams == 0, "a code slot belongs to one team");
+constexpr int kEpiWarps = 8, kTeamWarps = 4;
 constexpr int kMaxExperts = 1024;  // segment bounds and unit counts live in shared memory
 
 __host__ __device__ constexpr bool is_wgrad(int mode) { return mode >= kWeightGrad; }
 // whether an accumulator is a tile of the output as it lies in memory
-__host__ __device__ constexpr bool by_rows(int mode) { return mode == kWeightGrad || mode == kWeightGradSaved; }
+__host__ __device__ constexpr bool by_rows(int mode) { return is_wgrad(mode) && mode != kWeightGradT; }
+__host__ __device__ constexpr bool is_saved(int mode) { return mode == kWeightGradSaved || mode == kWeightGradSavedLong; }
 constexpr int kSquareRows = 4096;         // weight grad: see the order of units
 // 32 KiB a stage, the output boxes, and the ring of codes. Five stages: with four a weight
 // gradient of 24,576 rows, 4096 x 7168, takes 863 us instead of 715.
 __host__ __device__ constexpr int stages(int mode) { return mode == kWeightGradSaved ? 4 : 5; }
-// Weight grad: boxes of 64 rows of 128 bytes, two buffers for each pair of epilogue warps. A TMA
+// Saved rows: teams of decoding warps and code slots, as many of one as of the other: a team meets
+// its slot in every one of its phases. (Waiting by parity, it could take a phase that another team
+// has yet to see for its own.) Long segments: a fifth stage and a fourth team for one of the two
+// box buffers of each pair of epilogue warps. Measured (64 experts, 2048 x 4096, fp32, us), short
+// and long: 128 rows each 366, 394; 300 rows 448, 449; 500 rows 566, 520; 1,500 rows 1416, 1223.
+__host__ __device__ constexpr int teams(int mode) { return !is_saved(mode) ? 0 : mode == kWeightGradSaved ? 3 : 4; }
+__host__ __device__ constexpr int row_bufs(int mode) { return mode == kWeightGradSavedLong ? 1 : 2; }
+// Weight grad: boxes of 64 rows of 128 bytes for each pair of epilogue warps. A TMA
 // instruction costs the loads' engine about 100 clocks whatever it moves: with boxes of 16 rows 24,576
 // rows over 32 experts took 904 us.
 constexpr int kRowBuf = 64 * 128;
-__host__ __device__ constexpr int out_bytes(int mode) { return by_rows(mode) ? 4 * 2 * kRowBuf : 2 * kOutBufs * kOutBuf; }
+__host__ __device__ constexpr int out_bytes(int mode) { return by_rows(mode) ? 4 * row_bufs(mode) * kRowBuf : 2 * kOutBufs * kOutBuf; }
 __host__ __device__ constexpr int smem_bytes(int mode) {
-  return stages(mode) * 2 * kTile + out_bytes(mode) + (mode == kWeightGradSaved ? kRawSlots * kRaw : 0);
+  return stages(mode) * 2 * kTile + out_bytes(mode) + teams(mode) * kRaw;
 }
-__host__ __device__ constexpr int threads(int mode) { return 32 * (4 + kEpiWarps + (mode == kWeightGradSaved ? kDecWarps : 0)); }
+__host__ __device__ constexpr int threads(int mode) { return 32 * (4 + kEpiWarps + kTeamWarps * teams(mode)); }
 
 struct Params {
   const int32_t* offsets;
@@ -310,13 +315,14 @@ __device__ __forceinline__ void store_row(typename Elem::T* o, const float (&d)[
 }
 
 // Register splits (setmaxnreg). With kSum 384 threads launch with 168 registers each; the control
-// warpgroup keeps 80, the two epilogue warpgroups take 208. From saved rows 768 threads launch
-// with 80: control keeps 56, the epilogue takes 96, the three decoding warpgroups keep 72.
+// warpgroup keeps 80, the two epilogue warpgroups take 208. From saved rows 768 (long
+// segments: 896) threads launch with 80 (72): control keeps 56, the epilogue takes 96, the decoding
+// warpgroups, a team each, keep 72 (64).
 template <int MODE, bool kSum>
 struct Regs {
-  static constexpr bool kSplit = kSum || MODE == kWeightGradSaved;
-  static constexpr int kCtl = kSum ? 80 : 56, kEpi = kSum ? 208 : 96, kDec = 72;
-  static constexpr int kNeeded = 128 * kCtl + 256 * kEpi + (MODE == kWeightGradSaved ? 32 * kDecWarps * kDec : 0);
+  static constexpr bool kSplit = kSum || is_saved(MODE);
+  static constexpr int kCtl = kSum ? 80 : 56, kEpi = kSum ? 208 : 96, kDec = MODE == kWeightGradSavedLong ? 64 : 72;
+  static constexpr int kNeeded = 128 * kCtl + 256 * kEpi + 128 * teams(MODE) * kDec;
 };
 constexpr int kSumStages = 8, kAddStages = 16, kNoChunk = 0x3fffffff;
 
@@ -325,7 +331,8 @@ __global__ void __launch_bounds__(threads(MODE), 1)
     tc_matmul16_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b0,
                        const __grid_constant__ CUtensorMap map_b1, const __grid_constant__ CUtensorMap map_b2,
                        const __grid_constant__ CUtensorMap map_b3, const __grid_constant__ CUtensorMap map_o, Params p) {
-  constexpr bool kWG = is_wgrad(MODE), kSaved = MODE == kWeightGradSaved, kRows = by_rows(MODE);
+  constexpr bool kWG = is_wgrad(MODE), kSaved = is_saved(MODE), kRows = by_rows(MODE);
+  constexpr int kTeams = teams(MODE), kRawSlots = kTeams > 0 ? kTeams : 1, kRowBufs = row_bufs(MODE);
   constexpr int S = stages(MODE), kStage = 2 * kTile;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -729,11 +736,11 @@ __global__ void __launch_bounds__(threads(MODE), 1)
         if (tma_out) {  // (edges are clipped by the tensor map)
           const int pair = 2 * half + (quarter >> 1);
           const bool sender = (quarter & 1) == 0 && lane == 0;
-          uint8_t* ob = outbuf + (2 * pair + (int)(box & 1)) * kRowBuf;
+          uint8_t* ob = outbuf + (kRowBufs * pair + (int)(box % kRowBufs)) * kRowBuf;
           const bool first_half = !f32 && (c & 32) == 0, sends = !first_half || c + 32 >= t.cols;
           if (f32 || first_half) {
-            // the store that used this buffer two boxes ago has read it
-            if (sender) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            // the store that last used this buffer has read it
+            if (sender) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kRowBufs - 1) : "memory");
             named_bar(3 + pair, 64);
           }
           const uint32_t row = smem_u32(ob) + (32 * (quarter & 1) + lane) * 128;
@@ -870,7 +877,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
   } else if constexpr (kSaved) {
     // ------------------------ saved rows: decode ------------------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<MODE, kSum>::kDec));
-    // Three teams of four warps take stages in turn, so that some decode while others wait for
+    // Teams of four warps take stages in turn, so that some decode while others wait for
     // codes, for a free operand slot or for their stores to be visible. Thread (warp dw of the
     // team, lane): lines r0 + 16 v of the stage's 64, r0 = 8 dw + lane % 8, and the 32-wide group
     // lane / 8 of their 128 codes. Eight lanes with consecutive lines touch eight different
@@ -897,13 +904,13 @@ __global__ void __launch_bounds__(threads(MODE), 1)
           next |= b << (8 * v);
         }
       };
-      int s = (int)((team + kDecTeams - it % kDecTeams) % kDecTeams);
+      int s = (int)((team + kTeams - it % kTeams) % kTeams);
       fetch(s);
       const bool ragged = t.len % kBK != 0;
-      for (; s < steps; s += kDecTeams) {
+      for (; s < steps; s += kTeams) {
         const uint32_t i = it + s, scales = next;
         const int st = i % S, raw_slot = i % kRawSlots;
-        fetch(s + kDecTeams);
+        fetch(s + kTeams);
         const bool tail = ragged && s == steps - 1;
         const int left = t.len - s * kBK;
         ok = mbar_wait(smem_u32(&rfull[raw_slot]), (i / kRawSlots) & 1, &s_abort);
@@ -1135,7 +1142,9 @@ cudaError_t launch_tc_matmul16(const Matmul16Args& a, cudaStream_t st, int* unsu
   if (!p.tma_out) maps[5] = maps[0];
   *unsupported = 0;
   p.chunk = f32 ? kAddStages : kNoChunk;
-  if (a.x_scales) return launch<kWeightGradSaved, false>(maps, p, st, unsupported);
+  if (a.x_scales)
+    return a.rows > E * 256 ? launch<kWeightGradSavedLong, false>(maps, p, st, unsupported)
+                            : launch<kWeightGradSaved, false>(maps, p, st, unsupported);
   if (!transposed) return launch<kWeightGrad, false>(maps, p, st, unsupported);
   // fp32: segments that are long on average are summed in registers; otherwise the few that are
   // long are added in memory and the rest need neither.

@@ -446,9 +446,9 @@ typedef struct ftmoe_matrix_bank {
  * for the rows r of every expert e. a and w are bf16 or fp16, both w->dtype; out is
  * out_dtype (that type or any other), rounded to nearest even once from an fp32 sum. Row
  * strides ld_a, ld_out in elements. Rows at or beyond offsets[E] are neither read nor
- * written. Any sizes and strides are taken; where every base and row stride of a and w is a
- * multiple of 16 bytes the tensor cores or, for few rows, the streaming kernel run, else a
- * slower general kernel. w is only read. rows == 0 launches nothing. */
+ * written. Any sizes and strides are taken; where every base, row stride and expert stride of
+ * a and w is a multiple of 16 bytes (and there are at most 1,024 experts) the tensor cores or,
+ * for few rows, the streaming kernel run, else a slower general kernel. w is only read. rows == 0 launches nothing. */
 ftmoe_status ftmoe_grouped_matmul(const void* a, int64_t rows, int64_t ld_a, const int32_t* offsets,
                                   const ftmoe_matrix_bank* w, int32_t input_grad, void* out, int64_t ld_out,
                                   int32_t out_dtype, void* stream);

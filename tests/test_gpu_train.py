@@ -264,7 +264,8 @@ def test_weight_gradient(counts, n, k, dtype, out):
 
 
 @pytest.mark.parametrize("counts,n,k", [([1], 16, 32), ([0, 3, 0, 17], 136, 96), ([63, 64, 65, 1], 264, 320),
-                                        ([300, 0, 129], 128, 544), ([0, 0], 64, 64), ([15, 16, 17], 33, 64)])
+                                        ([300, 0, 129], 128, 544), ([0, 0], 64, 64), ([15, 16, 17], 33, 64),
+                                        ([400, 77, 1000], 264, 672)])
 @pytest.mark.parametrize("dtype,out", [("bf16", "fp32"), ("fp16", "fp16"), ("bf16", "bf16")])
 def test_weight_gradient_from_saved_rows(counts, n, k, dtype, out):
     R, E = sum(counts), len(counts)
