@@ -113,8 +113,8 @@ struct Params {
 // uniform registers, and with predicates instead of branches nothing stands between the MMAs.
 // (The loop is what bounds the kernel where it is longer than the MMAs it issues. Measured on
 // GB300 without any loads, clocks a stage: run by lane 0 alone, which moves every descriptor
-// over, 830; whole warp, a branch in front of each MMA, 900; predicates, 590; this form is what
-// is in use.) acc: whether the first MMA adds to the accumulator; left: rows of l that count, the
+// over, 830; whole warp, a branch in front of each MMA, 900; predicates, 590; one block, 460; no
+// vote on the waits, 410.) acc: whether the first MMA adds to the accumulator; left: rows of l that count, the
 // MMAs past them are off (kTail).
 template <bool kTail>
 __device__ __forceinline__ void mma_stage(uint32_t d, const uint64_t (&a)[4], const uint64_t (&b)[4], uint32_t idesc,
@@ -543,7 +543,9 @@ __global__ void __launch_bounds__(threads(MODE), 1)
     }
   } else if (warp == 1) {
     // -------------------------------- MMA issuer --------------------------------
-    // (the whole warp runs the loop, one elected lane issues)
+    // The whole warp runs the loop, one elected lane issues. Nothing in it needs the warp together
+    // (a vote on each wait cost 50 clocks a stage): after a wait that ran out the lanes leave one by
+    // one, as each sees the abort flag.
     if (crank == 0) {
       const uint32_t lead = elect_one();
       uint32_t acc = 0, st = 0, ph = 0;  // accumulators so far; the ring's slot and its phase
@@ -563,13 +565,12 @@ __global__ void __launch_bounds__(threads(MODE), 1)
         uint32_t d = 0;
         while (left > 0) {
           if (part == 0) {  // a free accumulator
-            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&tempty[acc & 1]), ((acc >> 1) & 1) ^ 1, &s_abort));
+            ok = mbar_wait(smem_u32(&tempty[acc & 1]), ((acc >> 1) & 1) ^ 1, &s_abort);
             if (!ok) break;
             d = tmem_base + (acc & 1) * kN;
           }
           const uint32_t bar = full0 + 8 * st;
           ok = kWG ? wait_cluster(bar, ph, &s_abort) : mbar_wait(bar, ph, &s_abort);
-          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           fence_after();
           uint64_t da[4], db[4];
