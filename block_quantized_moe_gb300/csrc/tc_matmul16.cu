@@ -104,7 +104,7 @@ struct Params {
   int l_dim;                 // extent of l (product, input grad)
   int c_dim;                 // weight grad: extent of c
   int E, out_dtype, bf16, accumulate;
-  int tma_out;               // whether map_o describes the output
+  int tma_out;               // whether maps.o describes the output
   int chunk;                 // stages that one accumulator adds up (see "Long sums")
 };
 
@@ -314,6 +314,12 @@ __device__ __forceinline__ void store_row(typename Elem::T* o, const float (&d)[
   }
 }
 
+// Tensor maps: A, the output, and B (K-major: boxes of 16, 32, .. 128 rows, half of a column tile's
+// width each, since what a wider box brings along costs as much as what is used; else one map).
+struct Maps {
+  CUtensorMap a, o, b[8];
+};
+
 // Register splits (setmaxnreg). With kSum 384 threads launch with 168 registers each; the control
 // warpgroup keeps 80, the two epilogue warpgroups take 208. From saved rows 768 (long
 // segments: 896) threads launch with 80 (72): control keeps 56, the epilogue takes 96, the decoding
@@ -328,9 +334,7 @@ constexpr int kSumStages = 8, kAddStages = 16, kNoChunk = 0x3fffffff;
 
 template <int MODE, bool kSum>
 __global__ void __launch_bounds__(threads(MODE), 1)
-    tc_matmul16_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b0,
-                       const __grid_constant__ CUtensorMap map_b1, const __grid_constant__ CUtensorMap map_b2,
-                       const __grid_constant__ CUtensorMap map_b3, const __grid_constant__ CUtensorMap map_o, Params p) {
+    tc_matmul16_kernel(const __grid_constant__ Maps maps, Params p) {
   constexpr bool kWG = is_wgrad(MODE), kSaved = is_saved(MODE), kRows = by_rows(MODE);
   constexpr int kTeams = teams(MODE), kRawSlots = kTeams > 0 ? kTeams : 1, kRowBufs = row_bufs(MODE);
   constexpr int S = stages(MODE), kStage = 2 * kTile;
@@ -351,14 +355,8 @@ __global__ void __launch_bounds__(threads(MODE), 1)
   const int MB = (p.m_dim + kM - 1) / kM;
   const int CB = kWG ? (p.c_dim + kN - 1) / kN : 0;
 
-  if (threadIdx.x < 6) {  // the descriptors are fetched while the rest is set up
-    const CUtensorMap* maps[6] = {&map_a, &map_b0, &map_b1, &map_b2, &map_b3, &map_o};
-    const CUtensorMap* m = maps[0];
-#pragma unroll
-    for (int i = 1; i < 6; ++i)
-      if (threadIdx.x == i) m = maps[i];
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
-  }
+  if (threadIdx.x < (kWG ? 3 : 10))  // the descriptors are fetched while the rest is set up
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps) + threadIdx.x * sizeof(CUtensorMap)) : "memory");
   if (threadIdx.x == 0) {
     s_abort = 0;
     for (int i = 0; i < S; ++i) {
@@ -484,10 +482,8 @@ __global__ void __launch_bounds__(threads(MODE), 1)
         const int half = t.n >> 1;  // of c in each CTA
         const int steps = (t.len + kBK - 1) / kBK;
         const int cb = t.c0 + (int)crank * half, ma = t.m0 + (int)crank * 128;
-        // K-major B: the smallest box that holds the half tile
-        const int hb = half <= 16 ? 16 : half <= 32 ? 32 : half <= 64 ? 64 : 128;
-        const CUtensorMap* mb = half <= 16 ? &map_b3 : half <= 32 ? &map_b2 : half <= 64 ? &map_b1 : &map_b0;
-        const uint32_t bytes_b = kWG ? (half > 64 ? kTile : kTile / 2) : (uint32_t)hb * 128;
+        const CUtensorMap* mb = &maps.b[kWG ? 0 : half / 16 - 1];
+        const uint32_t bytes_b = kWG ? (half > 64 ? kTile : kTile / 2) : (uint32_t)half * 128;
         const uint32_t bytes = kTile + (kSaved ? 0 : bytes_b);
         for (int s = 0; s < steps; ++s, ++it) {
           const int st = it % S;
@@ -507,18 +503,18 @@ __global__ void __launch_bounds__(threads(MODE), 1)
           }
           if constexpr (kWG) {
             const int l = t.l0 + s * kBK;
-            tma_pair_2d(ta, &map_a, bar, ma, l);
-            tma_pair_2d(ta + kTile / 2, &map_a, bar, ma + 64, l);
+            tma_pair_2d(ta, &maps.a, bar, ma, l);
+            tma_pair_2d(ta + kTile / 2, &maps.a, bar, ma + 64, l);
             if constexpr (!kSaved) {
-              tma_pair_2d(tb, &map_b0, bar, cb, l);
-              if (half > 64) tma_pair_2d(tb + kTile / 2, &map_b0, bar, cb + 64, l);
+              tma_pair_2d(tb, mb, bar, cb, l);
+              if (half > 64) tma_pair_2d(tb + kTile / 2, mb, bar, cb + 64, l);
             }
           } else {
             if constexpr (MODE == kProduct) {
-              tma_pair_3d(ta, &map_a, bar, s * kBK, ma, t.e);
+              tma_pair_3d(ta, &maps.a, bar, s * kBK, ma, t.e);
             } else {
-              tma_pair_3d(ta, &map_a, bar, ma, s * kBK, t.e);
-              tma_pair_3d(ta + kTile / 2, &map_a, bar, ma + 64, s * kBK, t.e);
+              tma_pair_3d(ta, &maps.a, bar, ma, s * kBK, t.e);
+              tma_pair_3d(ta + kTile / 2, &maps.a, bar, ma + 64, s * kBK, t.e);
             }
             tma_pair_2d(tb, mb, bar, s * kBK, cb);
           }
@@ -635,7 +631,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
           const int r = it % kRawSlots;
           if (!mbar_wait(smem_u32(&rempty[r]), ((it / kRawSlots) & 1) ^ 1, &s_abort)) break;
           mbar_expect_tx(smem_u32(&rfull[r]), kRaw);
-          tma_pair_2d(smem_u32(raws + r * kRaw), &map_b0, smem_u32(&rfull[r]), cb, t.l0 + s * kBK);
+          tma_pair_2d(smem_u32(raws + r * kRaw), &maps.b[0], smem_u32(&rfull[r]), cb, t.l0 + s * kBK);
         }
       }
       for (int r = 0; r < kRawSlots && (uint32_t)r < it; ++r) {  // in flight after an abort
@@ -712,9 +708,9 @@ __global__ void __launch_bounds__(threads(MODE), 1)
               const int y = t.c0 + c + 16 * h;
               if (mc < p.m_dim && (!kWG || y < p.c_dim)) {
                 if (add)
-                  tma_add_3d(&map_o, smem_u32(ob), mc, y, kWG ? t.e : 0);
+                  tma_add_3d(&maps.o, smem_u32(ob), mc, y, kWG ? t.e : 0);
                 else
-                  tma_store_3d(&map_o, smem_u32(ob), mc, y, kWG ? t.e : 0);
+                  tma_store_3d(&maps.o, smem_u32(ob), mc, y, kWG ? t.e : 0);
               }
               asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             }
@@ -769,9 +765,9 @@ __global__ void __launch_bounds__(threads(MODE), 1)
               const int x = t.c0 + (f32 ? c : c & ~32), y = mc + 64 * (quarter >> 1);
               if (y < p.m_dim) {
                 if (add)
-                  tma_add_3d(&map_o, smem_u32(ob), x, y, t.e);
+                  tma_add_3d(&maps.o, smem_u32(ob), x, y, t.e);
                 else
-                  tma_store_3d(&map_o, smem_u32(ob), x, y, t.e);
+                  tma_store_3d(&maps.o, smem_u32(ob), x, y, t.e);
               }
               asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             }
@@ -1027,7 +1023,7 @@ static bool encode_out(CUtensorMap* map, void* base, int32_t dtype, uint64_t wid
 }
 
 template <int MODE, bool kSum>
-static cudaError_t launch(const CUtensorMap* maps, const Params& p, cudaStream_t st, int* unsupported) {
+static cudaError_t launch(const Maps& maps, const Params& p, cudaStream_t st, int* unsupported) {
   const size_t smem = 1024 + (size_t)smem_bytes(MODE) + (is_wgrad(MODE) ? 0 : ((size_t)p.E + 1) * 8);
   int dev = 0;
   cudaGetDevice(&dev);
@@ -1056,8 +1052,7 @@ static cudaError_t launch(const CUtensorMap* maps, const Params& p, cudaStream_t
     return cudaSuccess;
   }
   const OverlapLaunch overlap;
-  return launch_kernel_cluster(tc_matmul16_kernel<MODE, kSum>, dim3(2 * np), dim3(threads(MODE)), smem, st, true, 2, maps[0],
-                               maps[1], maps[2], maps[3], maps[4], maps[5], p);
+  return launch_kernel_cluster(tc_matmul16_kernel<MODE, kSum>, dim3(2 * np), dim3(threads(MODE)), smem, st, true, 2, maps, p);
 }
 
 }  // namespace tc16
@@ -1071,7 +1066,7 @@ cudaError_t launch_tc_matmul16(const Matmul16Args& a, cudaStream_t st, int* unsu
   const ftmoe_matrix_bank& w = a.w;
   const int64_t E = w.num_experts;
   if (E > kMaxExperts || a.rows < 1) return cudaSuccess;
-  CUtensorMap maps[6];
+  Maps maps;
   Params p = {};
   p.offsets = a.offsets;
   p.rows = a.rows;
@@ -1087,20 +1082,21 @@ cudaError_t launch_tc_matmul16(const Matmul16Args& a, cudaStream_t st, int* unsu
     const uint64_t es = E > 1 ? (uint64_t)w.expert_stride : (uint64_t)w.n * w.ld;
     const uint64_t wd[3] = {(uint64_t)w.k, (uint64_t)w.n, (uint64_t)E}, ws[2] = {2 * (uint64_t)w.ld, 2 * es};
     const uint32_t wb[3] = {64, a.input_grad ? 64u : 128u, 1};
-    if (!encode16(&maps[0], w.w, 3, wd, ws, wb)) return cudaSuccess;
+    if (!encode16(&maps.a, w.w, 3, wd, ws, wb)) return cudaSuccess;
     const uint64_t ad[2] = {(uint64_t)l, R}, as[1] = {2 * (uint64_t)a.ld_a};
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t ab[2] = {64, 128u >> i};
-      if (!encode16(&maps[1 + i], a.a, 2, ad, as, ab)) return cudaSuccess;
+    const int widest = (int)(R < 256 ? cdiv(a.rows, 32) : 8);  // no column tile is wider than all rows
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t ab[2] = {64, 16u * (i + 1)};
+      if (i < widest ? !encode16(&maps.b[i], a.a, 2, ad, as, ab) : (maps.b[i] = maps.b[0], false)) return cudaSuccess;
     }
     p.out = a.out;
     p.ld_out = a.ld_out;
     p.m_dim = (int)m;
     p.l_dim = (int)l;
     p.out_dtype = a.out_dtype;
-    p.tma_out = encode_out(&maps[5], a.out, a.out_dtype, (uint64_t)m, R, 1, a.ld_out, 0, 128,
+    p.tma_out = encode_out(&maps.o, a.out, a.out_dtype, (uint64_t)m, R, 1, a.ld_out, 0, 128,
                            a.out_dtype == FTMOE_OUT_FP32 ? 16 : 32, CU_TENSOR_MAP_SWIZZLE_NONE);
-    if (!p.tma_out) maps[5] = maps[0];
+    if (!p.tma_out) maps.o = maps.a;
     *unsupported = 0;
     p.chunk = kNoChunk;
     if (a.out_dtype == FTMOE_OUT_FP32 && l > kSumStages * kBK) {
@@ -1113,7 +1109,7 @@ cudaError_t launch_tc_matmul16(const Matmul16Args& a, cudaStream_t st, int* unsu
   // see the epilogue: by rows for 16-bit outputs of segments that are short on average
   const bool f32 = w.dtype == FTMOE_OUT_FP32, long_segments = a.rows > E * kSumStages * kBK;
   const bool transposed = !a.x_scales && (f32 || long_segments);
-  CUtensorMap &mdy = maps[transposed ? 1 : 0], &mx = maps[transposed ? 0 : 1];
+  CUtensorMap &mdy = transposed ? maps.b[0] : maps.a, &mx = transposed ? maps.a : maps.b[0];
   const uint64_t dd[2] = {(uint64_t)w.n, R}, ds[1] = {2 * (uint64_t)a.ld_a};
   const uint32_t box[2] = {64, 64};
   if (!encode16(&mdy, a.a, 2, dd, ds, box)) return cudaSuccess;
@@ -1128,7 +1124,7 @@ cudaError_t launch_tc_matmul16(const Matmul16Args& a, cudaStream_t st, int* unsu
     const uint64_t xs[1] = {2 * (uint64_t)a.ld_x};
     if (!encode16(&mx, a.x, 2, xd, xs, box)) return cudaSuccess;
   }
-  maps[2] = maps[3] = maps[4] = maps[1];
+  for (int i = 1; i < 8; ++i) maps.b[i] = maps.b[0];
   p.x_scales = a.x_scales;
   p.out = w.w;
   p.ld_out = w.ld;
@@ -1137,10 +1133,10 @@ cudaError_t launch_tc_matmul16(const Matmul16Args& a, cudaStream_t st, int* unsu
   p.c_dim = (int)(transposed ? w.n : w.k);
   p.out_dtype = w.dtype;
   p.accumulate = a.accumulate;
-  p.tma_out = encode_out(&maps[5], w.w, w.dtype, (uint64_t)w.k, (uint64_t)w.n, (uint64_t)E, w.ld, w.expert_stride,
+  p.tma_out = encode_out(&maps.o, w.w, w.dtype, (uint64_t)w.k, (uint64_t)w.n, (uint64_t)E, w.ld, w.expert_stride,
                          transposed ? 128 : f32 ? 32 : 64, !transposed ? 64 : f32 ? 16 : 32,
                          transposed ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B);
-  if (!p.tma_out) maps[5] = maps[0];
+  if (!p.tma_out) maps.o = maps.a;
   *unsupported = 0;
   p.chunk = f32 ? kAddStages : kNoChunk;
   if (a.x_scales)
