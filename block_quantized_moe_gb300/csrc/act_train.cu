@@ -7,10 +7,13 @@
 // Backward, with the kept g and u, the gradient dh of the unweighted h and the routing weight w:
 //   d h / d u = g s,   d h / d g = u s (1 + g (1 - s))
 //   dgu = w dh (d h / d g | d h / d u),   hw = w h,   dweight = sum_i dh_i h_i
-// Both passes are elementwise but for the group maxima and dweight: they are bound by memory.
-// The forward moves 8 bytes per intermediate column (4 read, 2 + 2 written) and 1/16 to 1/32 of
-// scales; the backward 10 (2 codes and 2 of dh read, 4 + 2 written). Keeping gate/up in bf16
-// would move 4 more bytes per column and hold twice the memory between the passes.
+// Both passes are elementwise but for the group maxima and dweight. The forward moves 8 bytes per
+// intermediate column (4 read, 2 + 2 written) and 1/16 to 1/32 of scales, the backward 10 (2 codes
+// and 2 of dh read, 4 + 2 written): memory bounds them, closely followed by the issue rate (about
+// 310 and 340 instructions per warp and 8 columns a lane). Keeping gate/up in bf16 would move 4
+// more bytes per column and hold twice the memory between the passes. Measured on GB300, both
+// passes of 24,576 rows of 2,048 columns, bf16, FP8: 154 us, 5.9 TB/s, 88% of the measured copy
+// rate (280 us before packed fp32 pairs, the sigmoid below and the loads ahead).
 #include <type_traits>
 
 #include "common.cuh"

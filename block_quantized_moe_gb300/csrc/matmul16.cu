@@ -7,7 +7,8 @@
 // each written as D[i, j] = sum_l A[i, l] B[l, j] with element strides. A block takes 64 x 64
 // outputs, a thread 4 x 4 of them in fp32 registers, the contraction in steps of 16 through
 // shared memory. It runs where the tensor cores cannot: TMA wants 16-byte bases and row
-// strides. fp32 FMAs bound it (about 1/30 of the tensor-core rate).
+// strides. fp32 FMAs and the strided loads bound it: 145 us for the weight gradient of 333 rows
+// over 8 experts, 1536 x 2048 (14 TFLOP/s; the tensor cores take 24 us).
 #include "common.cuh"
 #include "elem16.cuh"
 #include "internal.h"

@@ -7,7 +7,8 @@
 // L1) before the next piece; fp32 sums, one butterfly per output. Eight warps of a CTA take eight
 // consecutive i. All SMs stream, whatever the number of experts: the tensor-core kernel's units
 // of 256 weight rows leave most of the SMs idle here (two rows over two experts, 1536 x 2048: 12
-// units).
+// units). Measured there: 5.0 us, of which about 3 are launch and the offsets' round trip; one row,
+// 4096 x 7168: 19 us (3 TB/s).
 #include "common.cuh"
 #include "elem16.cuh"
 #include "internal.h"
