@@ -37,7 +37,8 @@ using Pair = F32Pair;
 // from the residual of the product, log2(e)'s low part and r, keeps the exponential to a few units
 // in the last place however large |g| is (the rounding of t alone would cost |g| of them). The
 // factor is applied as a factor, so that an infinite 2^t stays infinite. 1 + e is scaled by 2^-24
-// before the reciprocal, which would flush to zero from 2^126 on, and its result again.
+// before the reciprocal, which would flush to zero from 2^126 on, and its result again. (Where
+// exp(-x) passes fp32's range, x < -88.7, the sigmoid is 0; its value there is below 1e-38.)
 constexpr float kLog2e = 1.44269502f, kLog2eLow = 1.92596303e-8f, kLn2 = 0.693147182f, kDown = 0x1p-24f;
 template <bool kResidual>
 __device__ __forceinline__ Pair sigmoid(Pair g, Pair r) {
@@ -165,8 +166,9 @@ __global__ void __launch_bounds__(256, 4) silu_save_kernel(
     load(g_next, u_next);
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
-      const Pair g2(g[i], g[i + 1]);
-      (g2 * sigmoid<false>(g2, g2) * Pair(u[i], u[i + 1])).get(a[i], a[i + 1]);
+      // (the sigmoid is 1 long before 128, and the product with an infinite g has no residual)
+      const Pair x(fminf(g[i], 128.0f), fminf(g[i + 1], 128.0f));
+      (Pair(g[i], g[i + 1]) * sigmoid<false>(x, x) * Pair(u[i], u[i + 1])).get(a[i], a[i + 1]);
     }
     float sg, su;
     uint8_t bg, bu;

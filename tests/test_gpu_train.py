@@ -473,6 +473,30 @@ def test_silu_saved_codes_bit_for_bit(fmt):
 
 
 @pytest.mark.parametrize("fmt", [ft.FMT_FP8, ft.FMT_MXFP8])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_silu_saved_infinities_nan_and_large_values(fmt, dtype):
+    """h where g or u is infinite, NaN, or of any finite size: infinite, NaN and zero where the
+    formula is; rows without such values are not touched by their neighbours'."""
+    odd = [float("inf"), float("-inf"), float("nan"), 3e38, -3e38, 1e30, -1e30, 1000.0, -1000.0, 0.0, -0.0, 1.0, -80.0]
+    pairs = [(g, u) for g in odd for u in (1.0, -2.0, 0.0, float("inf"), float("nan"))]
+    inter = 32 * -(-len(pairs) // 32)
+    row = torch.zeros(2 * inter, device=DEV)
+    row[: len(pairs)] = torch.tensor([p[0] for p in pairs])
+    row[inter: inter + len(pairs)] = torch.tensor([p[1] for p in pairs])
+    gu = normal((3, 2 * inter), 1.0, torch.float32, 39)
+    gu[1] = row
+    gu = gu.to(DT[dtype])
+    h, _, _, _ = save(gu, fmt, DT[dtype])
+    g, u = gu[:, :inter].double(), gu[:, inter:].double()
+    ref = (g / (1 + torch.exp(-g)) * u).to(DT[dtype]).double()
+    assert torch.equal(torch.isnan(h), torch.isnan(ref))
+    keep = ~torch.isnan(ref)
+    assert torch.equal(h.double()[keep & torch.isinf(ref)], ref[keep & torch.isinf(ref)])
+    fin = keep & torch.isfinite(ref)
+    check(h[fin], (g / (1 + torch.exp(-g)) * u)[fin], ref.abs()[fin], 8, "h")
+
+
+@pytest.mark.parametrize("fmt", [ft.FMT_FP8, ft.FMT_MXFP8])
 def test_silu_gradient_agrees_with_differences(fmt):
     """dgu against central differences of sum(dh * w * h) in 64 bits at the kept values."""
     rows, inter = 5, 96
