@@ -33,12 +33,17 @@
 //
 // Long sums. The tensor core cuts low bits off as it adds a product to its fp32 accumulator: the
 // error is a bias that grows with the number of additions (measured: 4.4e-6 of the result's norm
-// over 4,096 terms, where fp32 sums rounded to nearest have 6e-7). A 16-bit output hides that, an
-// fp32 output does not. For fp32 outputs an accumulator takes 8 stages (512 terms) and the
-// epilogue adds the accumulators up in registers, 128 per thread, the control warps giving up
-// theirs. A weight gradient from saved rows (whose decoding warps need the registers), or of
-// segments that are short on average, takes 16 stages and adds the parts of the few segments that
-// are longer in memory, by TMA.
+// over 4,096 terms, where fp32 sums rounded to nearest have 6e-7). So an accumulator takes 8 stages
+// (512 terms) for fp32 outputs and 32 (2,048 terms: 2.2e-6, an eightieth of fp16's rounding) for
+// 16-bit ones, and the epilogue adds the accumulators up in registers, 128 per thread, the control
+// warps giving up theirs. 16-bit products cost nothing by it (32 stages, 8 stages and one
+// accumulator throughout: 24,576 rows over 32 experts, 4096 x 7168: 911, 925, 910 us). 16-bit weight
+// gradients do, as their output boxes then leave in bursts (500 rows for each of 64 experts, 2048 x
+// 4096: 409 us against 391; the 32 experts above 993 against 976), so they have it in calls of more
+// than 32,768 rows, below which one accumulator's bias stays under 3.6e-5, a fourteenth of fp16's unit
+// roundoff. A weight gradient from saved rows (whose decoding warps need the registers), or an fp32
+// one of segments that are short on average, takes 16 stages and adds the parts of the few
+// segments that are longer in memory, by TMA.
 //
 // Measured on GB300: product of 24,576 rows over 256 experts, 4096 x 7168, 2,328 us (6.7 TB/s, the
 // measured copy rate); over 32 experts of 768 rows 791 us (1,825 TFLOP/s in a burst; 1,550 in a
@@ -338,7 +343,8 @@ struct Regs {
   static constexpr int kCtl = kSum ? 80 : 56, kEpi = kSum ? 208 : 96, kDec = MODE == kWeightGradSavedLong ? 64 : 72;
   static constexpr int kNeeded = 128 * kCtl + 256 * kEpi + 128 * teams(MODE) * kDec;
 };
-constexpr int kSumStages = 8, kAddStages = 16, kNoChunk = 0x3fffffff;
+constexpr int kSumStages = 8, kSumStages16 = 32, kAddStages = 16, kNoChunk = 0x3fffffff;
+constexpr int64_t kPlainRows = 32768;
 
 template <int MODE, bool kSum>
 __global__ void __launch_bounds__(threads(MODE), 1)
@@ -670,7 +676,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
     const bool leader = quarter == 0 && lane == 0;
     uint32_t acc = 0, box = 0;  // accumulators, output boxes so far
     const bool words = p.ld_out % 2 == 0 && p.out_expert % 2 == 0 && reinterpret_cast<uintptr_t>(p.out) % 4 == 0;
-    const bool f32 = kSum || p.out_dtype == FTMOE_OUT_FP32;
+    const bool f32 = p.out_dtype == FTMOE_OUT_FP32;
     const bool tma_out = p.tma_out && (!p.accumulate || p.out_dtype == FTMOE_OUT_FP32);
     for (int64_t u = u_begin; u < u_end; u += u_step) {
       Unit t;
@@ -1106,11 +1112,9 @@ cudaError_t launch_tc_matmul16(const Matmul16Args& a, cudaStream_t st, int* unsu
                            a.out_dtype == FTMOE_OUT_FP32 ? 16 : 32, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (!p.tma_out) maps.o = maps.a;
     *unsupported = 0;
-    p.chunk = kNoChunk;
-    if (a.out_dtype == FTMOE_OUT_FP32 && l > kSumStages * kBK) {
-      p.chunk = kSumStages;
+    p.chunk = a.out_dtype == FTMOE_OUT_FP32 ? kSumStages : kSumStages16;
+    if (l > p.chunk * kBK)
       return a.input_grad ? launch<kInputGrad, true>(maps, p, st, unsupported) : launch<kProduct, true>(maps, p, st, unsupported);
-    }
     return a.input_grad ? launch<kInputGrad, false>(maps, p, st, unsupported) : launch<kProduct, false>(maps, p, st, unsupported);
   }
   if (!tma16(a.a, a.ld_a) || E * cdiv(w.n, kM) * cdiv(w.k, kN) > 0x7fffffff) return cudaSuccess;
@@ -1150,14 +1154,13 @@ cudaError_t launch_tc_matmul16(const Matmul16Args& a, cudaStream_t st, int* unsu
   if (a.x_scales)
     return a.rows > E * 256 ? launch<kWeightGradSavedLong, false>(maps, p, st, unsupported)
                             : launch<kWeightGradSaved, false>(maps, p, st, unsupported);
-  if (!transposed) return launch<kWeightGrad, false>(maps, p, st, unsupported);
-  // fp32: segments that are long on average are summed in registers; otherwise the few that are
-  // long are added in memory and the rest need neither.
-  if (f32 && long_segments) {
-    p.chunk = kSumStages;
-    return launch<kWeightGradT, true>(maps, p, st, unsupported);
+  // fp32 and short on average: the few segments that are long are added in memory, the rest need
+  // neither that nor registers for a sum. 16 bits: see "Long sums".
+  if (f32 ? long_segments : a.rows > kPlainRows) {
+    p.chunk = f32 ? kSumStages : kSumStages16;
+    return transposed ? launch<kWeightGradT, true>(maps, p, st, unsupported) : launch<kWeightGrad, true>(maps, p, st, unsupported);
   }
-  return launch<kWeightGradT, false>(maps, p, st, unsupported);
+  return transposed ? launch<kWeightGradT, false>(maps, p, st, unsupported) : launch<kWeightGrad, false>(maps, p, st, unsupported);
 }
 
 FTMOE_DEFINE_ERR_READER(read_err_tc_matmul16)

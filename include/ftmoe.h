@@ -444,8 +444,9 @@ typedef struct ftmoe_matrix_bank {
  *   input_grad = 0: out[r, i] = sum_j a[r, j] * w[e, i, j]   a [rows][k], out [rows][n]
  *   input_grad = 1: out[r, j] = sum_i a[r, i] * w[e, i, j]   a [rows][n], out [rows][k]
  * for the rows r of every expert e. a and w are bf16 or fp16, both w->dtype; out is
- * out_dtype (that type or any other), rounded to nearest even once from an fp32 sum. Row
- * strides ld_a, ld_out in elements. Rows at or beyond offsets[E] are neither read nor
+ * out_dtype (that type or any other), rounded to nearest even once from an fp32 sum. (The tensor
+ * core's fp32 accumulator cuts low bits off as it adds; after 512 terms for fp32 outputs, 2,048 for
+ * 16-bit ones, sums leave it and are added rounding to nearest.) Row strides ld_a, ld_out in elements. Rows at or beyond offsets[E] are neither read nor
  * written. Any sizes and strides are taken; where every base, row stride and expert stride of
  * a and w is a multiple of 16 bytes (and there are at most 1,024 experts) the tensor cores or,
  * for few rows, the streaming kernel run, else a slower general kernel. w is only read. rows == 0 launches nothing. */
@@ -457,7 +458,8 @@ ftmoe_status ftmoe_grouped_matmul(const void* a, int64_t rows, int64_t ld_a, con
  *   dw[e, i, j] = (accumulate ? dw[e, i, j] : 0) + sum over the rows r of expert e of dy[r, i] * x[r, j]
  * dy [rows][n] and x [rows][k] are bf16 or fp16, both `dtype`; dw->dtype is any
  * ftmoe_out_dtype. The sum is fp32 and rounded once; an old value is added in fp32 before the
- * rounding. An expert without rows gets zeros (accumulate: keeps its values). rows == 0 is
+ * rounding. (As above; 16-bit gradients of up to 32,768 rows stay in the accumulator throughout,
+ * a relative bias of about 1e-9 a row.) An expert without rows gets zeros (accumulate: keeps its values). rows == 0 is
  * no error: every expert is then one without rows. dw must not overlap dy or x. */
 ftmoe_status ftmoe_grouped_matmul_wgrad(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, int64_t rows,
                                         int32_t dtype, const int32_t* offsets, const ftmoe_matrix_bank* dw,

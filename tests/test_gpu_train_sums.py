@@ -1,0 +1,54 @@
+"""Long sums of the products grouped by expert with 16-bit outputs, against 64-bit products.
+
+The tensor core cuts off what lies below its accumulator's last bit as it adds: over operands of one
+sign that is a bias, growing with the number of additions. Tolerances, from the arithmetic: an
+accumulator takes 2,048 terms in 128 additions, each losing at most 2^-23 of the partial sum (a weight
+gradient of up to 32,768 rows: all of them); the accumulators are added in fp32, each sum within 2^-24;
+the output rounds once.
+"""
+import pytest
+import torch
+
+import block_quantized_moe_gb300 as ft
+from test_gpu_train import DEV, DT, U, gen, offsets_of, product_ref, wgrad_ref
+
+pytestmark = pytest.mark.gpu
+LONG = 200_000
+
+
+def positive(shape, mid, dtype, seed):
+    return (torch.rand(shape, generator=gen(seed), device=DEV) + 0.5).mul_(mid).to(dtype)
+
+
+def check_sum(got, ref, terms, per, what):
+    """got within the tolerance of a sum of `terms` positive products, `per` to an accumulator"""
+    tol = (per // 16 * 2.0 ** -23 + (terms // per + 1) * 2.0 ** -24 + U[got.dtype]) * ref.abs()
+    err = (got.double() - ref).abs()
+    assert (err <= tol).all(), f"{what}: {int((err > tol).sum())} of {err.numel()} outside, worst {float((err / tol.clamp(min=1e-300)).max()):.3g}"
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("input_grad", [False, True])
+def test_product_of_long_rows(dtype, input_grad):
+    counts, m = [40, 0, 3], 72
+    n, k = (LONG, m) if input_grad else (m, LONG)
+    a, w = positive((43, LONG), 1.0, DT[dtype], 1), positive((3, n, k), 0.1, DT[dtype], 2)
+    got = torch.empty(43, m, dtype=DT[dtype], device=DEV)
+    ft.ftmoe_grouped_matmul(a, offsets_of(counts), w, got, input_grad=input_grad)
+    check_sum(got, product_ref(a, w, counts, input_grad)[0], LONG, 2048, "product")
+    assert ft.ftmoe_read_error_flags() == 0
+
+
+# many experts without rows: segments that are short on average, one that is not
+@pytest.mark.parametrize("experts", [2, 500])
+@pytest.mark.parametrize("rows,per", [(LONG, 2048), (32698, 32768)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_weight_gradient_of_many_rows(dtype, rows, per, experts):
+    counts = [rows] + [0] * (experts - 2) + [70]
+    R, n, k = sum(counts), 136, 160
+    dy, x = positive((R, n), 0.1, DT[dtype], 3), positive((R, k), 1.0, DT[dtype], 4)
+    dw = torch.empty(experts, n, k, dtype=DT[dtype], device=DEV)
+    ft.ftmoe_grouped_matmul_wgrad(dy, x, offsets_of(counts), dw)
+    ref, _ = wgrad_ref(dy, x, counts)
+    check_sum(dw, ref, rows, per, "weight gradient")
+    assert ft.ftmoe_read_error_flags() == 0
