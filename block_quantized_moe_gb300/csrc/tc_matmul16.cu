@@ -34,16 +34,16 @@
 // Long sums. The tensor core cuts low bits off as it adds a product to its fp32 accumulator: the
 // error is a bias that grows with the number of additions (measured: 4.4e-6 of the result's norm
 // over 4,096 terms, where fp32 sums rounded to nearest have 6e-7). So an accumulator takes 8 stages
-// (512 terms) for fp32 outputs and 32 (2,048 terms: 2.2e-6, an eightieth of fp16's rounding) for
-// 16-bit ones, and the epilogue adds the accumulators up in registers, 128 per thread, the control
-// warps giving up theirs. 16-bit products cost nothing by it (32 stages, 8 stages and one
-// accumulator throughout: 24,576 rows over 32 experts, 4096 x 7168: 911, 925, 910 us). 16-bit weight
-// gradients do, as their output boxes then leave in bursts (500 rows for each of 64 experts, 2048 x
-// 4096: 409 us against 391; the 32 experts above 993 against 976), so they have it in calls of more
-// than 32,768 rows, below which one accumulator's bias stays under 3.6e-5, a fourteenth of fp16's unit
-// roundoff. A weight gradient from saved rows (whose decoding warps need the registers), or an fp32
-// one of segments that are short on average, takes 16 stages and adds the parts of the few
-// segments that are longer in memory, by TMA.
+// (512 terms) for fp32 outputs and 32 (2,048 terms) for 16-bit ones, and the epilogue adds the
+// accumulators up in registers, 128 per thread, the control warps giving up theirs. 16-bit products
+// cost nothing by it (32 stages, 8 stages and one accumulator throughout: 24,576 rows over 32 experts,
+// 4096 x 7168: 911, 925, 910 us). 16-bit weight gradients do, as their output boxes then leave in
+// bursts (500 rows for each of 64 experts, 2048 x 4096: 409 us against 391; the 32 experts above 993
+// against 976), so they have it in calls of more than 4,096 rows (fp16) or 32,768 (bf16). Up to there
+// one accumulator's bias is a nineteenth of the type's unit roundoff at most: over operands of one
+// sign, where it is largest, 2.5e-5 and 2.1e-4 (6.4e-9 a row). A weight gradient from saved rows
+// (whose decoding warps need the registers), or an fp32 one of segments that are short on average,
+// takes 16 stages and adds the parts of the few segments that are longer in memory, by TMA.
 //
 // Measured on GB300: product of 24,576 rows over 256 experts, 4096 x 7168, 2,328 us (6.7 TB/s, the
 // measured copy rate); over 32 experts of 768 rows 791 us (1,825 TFLOP/s in a burst; 1,550 in a
@@ -344,7 +344,8 @@ struct Regs {
   static constexpr int kNeeded = 128 * kCtl + 256 * kEpi + 128 * teams(MODE) * kDec;
 };
 constexpr int kSumStages = 8, kSumStages16 = 32, kAddStages = 16, kNoChunk = 0x3fffffff;
-constexpr int64_t kPlainRows = 32768;
+// rows of a call up to which a 16-bit weight gradient stays in one accumulator
+constexpr int64_t plain_rows(int32_t out_dtype) { return out_dtype == FTMOE_OUT_FP16 ? 4096 : 32768; }
 
 template <int MODE, bool kSum>
 __global__ void __launch_bounds__(threads(MODE), 1)
@@ -1156,7 +1157,7 @@ cudaError_t launch_tc_matmul16(const Matmul16Args& a, cudaStream_t st, int* unsu
                             : launch<kWeightGradSaved, false>(maps, p, st, unsupported);
   // fp32 and short on average: the few segments that are long are added in memory, the rest need
   // neither that nor registers for a sum. 16 bits: see "Long sums".
-  if (f32 ? long_segments : a.rows > kPlainRows) {
+  if (f32 ? long_segments : a.rows > plain_rows(w.dtype)) {
     p.chunk = f32 ? kSumStages : kSumStages16;
     return transposed ? launch<kWeightGradT, true>(maps, p, st, unsupported) : launch<kWeightGrad, true>(maps, p, st, unsupported);
   }

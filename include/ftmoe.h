@@ -458,8 +458,8 @@ ftmoe_status ftmoe_grouped_matmul(const void* a, int64_t rows, int64_t ld_a, con
  *   dw[e, i, j] = (accumulate ? dw[e, i, j] : 0) + sum over the rows r of expert e of dy[r, i] * x[r, j]
  * dy [rows][n] and x [rows][k] are bf16 or fp16, both `dtype`; dw->dtype is any
  * ftmoe_out_dtype. The sum is fp32 and rounded once; an old value is added in fp32 before the
- * rounding. (As above; 16-bit gradients of up to 32,768 rows stay in the accumulator throughout,
- * a relative bias of about 1e-9 a row.) An expert without rows gets zeros (accumulate: keeps its values). rows == 0 is
+ * rounding. (As above; fp16 gradients of up to 4,096 rows and bf16 ones of up to 32,768 stay in the
+ * accumulator throughout: over operands of one sign a bias of 6.4e-9 a row.) An expert without rows gets zeros (accumulate: keeps its values). rows == 0 is
  * no error: every expert is then one without rows. dw must not overlap dy or x. */
 ftmoe_status ftmoe_grouped_matmul_wgrad(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, int64_t rows,
                                         int32_t dtype, const int32_t* offsets, const ftmoe_matrix_bank* dw,

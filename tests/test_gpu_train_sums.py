@@ -2,9 +2,9 @@
 
 The tensor core cuts off what lies below its accumulator's last bit as it adds: over operands of one
 sign that is a bias, growing with the number of additions. Tolerances, from the arithmetic: an
-accumulator takes 2,048 terms in 128 additions, each losing at most 2^-23 of the partial sum (a weight
-gradient of up to 32,768 rows: all of them); the accumulators are added in fp32, each sum within 2^-24;
-the output rounds once.
+accumulator takes 2,048 terms in 128 additions (a weight gradient of up to 4,096 rows in fp16, 32,768
+in bf16: all of them), which lose 2^-23 of the result each; the accumulators are added in fp32, each
+sum within 2^-24; the output rounds once.
 """
 import pytest
 import torch
@@ -41,8 +41,8 @@ def test_product_of_long_rows(dtype, input_grad):
 
 # many experts without rows: segments that are short on average, one that is not
 @pytest.mark.parametrize("experts", [2, 500])
-@pytest.mark.parametrize("rows,per", [(LONG, 2048), (32698, 32768)])
-@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dtype,rows,per", [("bf16", LONG, 2048), ("fp16", LONG, 2048), ("bf16", 32698, 32768),
+                                            ("fp16", 4026, 4096), ("fp16", 32698, 2048)])
 def test_weight_gradient_of_many_rows(dtype, rows, per, experts):
     counts = [rows] + [0] * (experts - 2) + [70]
     R, n, k = sum(counts), 136, 160
