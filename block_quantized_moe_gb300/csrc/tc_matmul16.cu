@@ -41,9 +41,12 @@
 // bursts (500 rows for each of 64 experts, 2048 x 4096: 409 us against 391; the 32 experts above 993
 // against 976), so they have it in calls of more than 4,096 rows (fp16) or 32,768 (bf16). Up to there
 // one accumulator's bias is a nineteenth of the type's unit roundoff at most: over operands of one
-// sign, where it is largest, 2.5e-5 and 2.1e-4 (6.4e-9 a row). A weight gradient from saved rows
-// (whose decoding warps need the registers), or an fp32 one of segments that are short on average,
-// takes 16 stages and adds the parts of the few segments that are longer in memory, by TMA.
+// sign, where it is largest, 2.5e-5 and 2.1e-4 (6.4e-9 a row). An fp32 weight gradient of segments
+// that are short on average, or from saved rows (whose decoding warps need the registers), takes 16
+// stages and adds the parts of the few segments that are longer in memory, by TMA. A 16-bit one from
+// saved rows, in calls of more rows than that, takes 64 stages (2.5e-5) and adds the parts of a longer
+// segment up in TMEM: one accumulator holds the sum, so that the MMAs wait while a part is added to
+// it.
 //
 // Measured on GB300: product of 24,576 rows over 256 experts, 4096 x 7168, 2,328 us (6.7 TB/s, the
 // measured copy rate); over 32 experts of 768 rows 791 us (1,825 TFLOP/s in a burst; 1,550 in a
@@ -340,10 +343,34 @@ struct Maps {
 template <int MODE, bool kSum>
 struct Regs {
   static constexpr bool kSplit = kSum || is_saved(MODE);
-  static constexpr int kCtl = kSum ? 80 : 56, kEpi = kSum ? 208 : 96, kDec = MODE == kWeightGradSavedLong ? 64 : 72;
+  static constexpr int kCtl = is_saved(MODE) ? 56 : 80, kEpi = is_saved(MODE) ? 96 : 208, kDec = MODE == kWeightGradSavedLong ? 64 : 72;
   static constexpr int kNeeded = 128 * kCtl + 256 * kEpi + 128 * teams(MODE) * kDec;
 };
-constexpr int kSumStages = 8, kSumStages16 = 32, kAddStages = 16, kNoChunk = 0x3fffffff;
+constexpr int kSumStages = 8, kSumStages16 = 32, kAddStages = 16, kHoldStages = 64, kNoChunk = 0x3fffffff;
+// The accumulator in turn: its index, the phase of its barriers, and, after the last one, the phase
+// of its last use. They alternate; with kHold a unit may go on with the one that it has.
+template <bool kHold>
+struct Turn {
+  uint32_t n = 0;
+  __device__ __forceinline__ uint32_t at() const { return n & 1; }
+  __device__ __forceinline__ uint32_t phase() const { return (n >> 1) & 1; }
+  __device__ __forceinline__ void next(bool) { ++n; }
+  __device__ __forceinline__ bool used(uint32_t b) const { return b < n; }
+  __device__ __forceinline__ uint32_t last(uint32_t b) const { return ((n - 1 - ((n - 1 - b) & 1)) >> 1) & 1; }
+};
+template <>
+struct Turn<true> {
+  uint32_t b = 0, odd = 0, any = 0;  // bit i: uses of accumulator i mod 2, whether it was used
+  __device__ __forceinline__ uint32_t at() const { return b; }
+  __device__ __forceinline__ uint32_t phase() const { return odd >> b & 1; }
+  __device__ __forceinline__ void next(bool stay) {
+    odd ^= 1u << b;
+    any |= 1u << b;
+    if (!stay) b ^= 1;
+  }
+  __device__ __forceinline__ bool used(uint32_t i) const { return any >> i & 1; }
+  __device__ __forceinline__ uint32_t last(uint32_t i) const { return (odd >> i & 1) ^ 1; }
+};
 // rows of a call up to which a 16-bit weight gradient stays in one accumulator
 constexpr int64_t plain_rows(int32_t out_dtype) { return out_dtype == FTMOE_OUT_FP16 ? 4096 : 32768; }
 
@@ -351,6 +378,7 @@ template <int MODE, bool kSum>
 __global__ void __launch_bounds__(threads(MODE), 1)
     tc_matmul16_kernel(const __grid_constant__ Maps maps, Params p) {
   constexpr bool kWG = is_wgrad(MODE), kSaved = is_saved(MODE), kRows = by_rows(MODE);
+  constexpr bool kHold = kSum && kSaved, kInRegs = kSum && !kSaved;  // where long sums are added up
   constexpr int kTeams = teams(MODE), kRawSlots = kTeams > 0 ? kTeams : 1, kRowBufs = row_bufs(MODE);
   constexpr int S = stages(MODE), kStage = 2 * kTile;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -483,6 +511,10 @@ __global__ void __launch_bounds__(threads(MODE), 1)
     // (saved rows: each CTA's half starts on a 32-wide scale group)
     t.n = kSaved ? (t.cols + 63) & ~63 : (t.cols + 31) & ~31;
   };
+  // A unit whose parts all go through one accumulator while the other holds their sum. The MMAs leave
+  // the other alone until the last part, and with it the sum, has been read: the unit after begins
+  // with the first one again.
+  auto hold = [&](const Unit& t) { return kHold && (t.len + kBK - 1) / kBK > p.chunk; };
 
   if (warp < 4) {
   using R = Regs<MODE, kSum>;
@@ -559,7 +591,8 @@ __global__ void __launch_bounds__(threads(MODE), 1)
     // one, as each sees the abort flag.
     if (crank == 0) {
       const uint32_t lead = elect_one();
-      uint32_t acc = 0, st = 0, ph = 0;  // accumulators so far; the ring's slot and its phase
+      Turn<kHold> acc;
+      uint32_t st = 0, ph = 0;  // the ring's slot and its phase
       // low words of the operands' descriptors for slot 0; a slot and 16 of l further on
       const uint64_t a0 = MODE == kProduct ? smem_desc_sw128(smem_u32(tiles)) : smem_desc_mn_sw128(smem_u32(tiles));
       const uint64_t b0 = kWG ? smem_desc_mn_sw128(smem_u32(tiles) + kTile) : smem_desc_sw128(smem_u32(tiles) + kTile);
@@ -573,12 +606,13 @@ __global__ void __launch_bounds__(threads(MODE), 1)
                                (MODE == kProduct ? 0u : 1u << 15) | (kWG ? 1u << 16 : 0u) |
                                ((uint32_t)(t.n >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);
         int left = t.len, part = 0;
+        const bool stay = hold(t);
         uint32_t d = 0;
         while (left > 0) {
           if (part == 0) {  // a free accumulator
-            ok = mbar_wait(smem_u32(&tempty[acc & 1]), ((acc >> 1) & 1) ^ 1, &s_abort);
+            ok = mbar_wait(smem_u32(&tempty[acc.at()]), acc.phase() ^ 1, &s_abort);
             if (!ok) break;
-            d = tmem_base + (acc & 1) * kN;
+            d = tmem_base + acc.at() * kN;
           }
           const uint32_t bar = full0 + 8 * st;
           ok = kWG ? wait_cluster(bar, ph, &s_abort) : mbar_wait(bar, ph, &s_abort);
@@ -597,17 +631,16 @@ __global__ void __launch_bounds__(threads(MODE), 1)
             ph ^= 1;
           }
           if (++part == p.chunk || left <= 0) {
-            commit_pair_lead(smem_u32(&tfull[acc & 1]), lead);
-            ++acc;
+            commit_pair_lead(smem_u32(&tfull[acc.at()]), lead);
+            acc.next(stay);
             part = 0;
           }
         }
       }
       // MMAs still running write TMEM: wait (bounded) for the last commit of each accumulator
-      for (uint32_t b = 0; b < 2 && b < acc; ++b) {
-        const uint32_t last = acc - 1 - ((acc - 1 - b) & 1);
+      for (uint32_t b = 0; b < 2 && acc.used(b); ++b) {
         const unsigned long long t0 = globaltimer();
-        while (!mbar_try_wait(smem_u32(&tfull[b]), (last >> 1) & 1) && globaltimer() - t0 < kTimeoutNs) {
+        while (!mbar_try_wait(smem_u32(&tfull[b]), acc.last(b)) && globaltimer() - t0 < kTimeoutNs) {
         }
       }
     }
@@ -675,7 +708,8 @@ __global__ void __launch_bounds__(threads(MODE), 1)
     // a 16-bit accumulation are stored from registers.
     const int ew = warp - 4, quarter = warp & 3, half = ew >> 2;
     const bool leader = quarter == 0 && lane == 0;
-    uint32_t acc = 0, box = 0;  // accumulators, output boxes so far
+    Turn<kHold> acc;
+    uint32_t box = 0;  // output boxes so far
     const bool words = p.ld_out % 2 == 0 && p.out_expert % 2 == 0 && reinterpret_cast<uintptr_t>(p.out) % 4 == 0;
     const bool f32 = p.out_dtype == FTMOE_OUT_FP32;
     const bool tma_out = p.tma_out && (!p.accumulate || p.out_dtype == FTMOE_OUT_FP32);
@@ -808,7 +842,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
       // the first column of this half's i-th run of 32 (by rows: runs in pairs)
       auto column = [&](int i) { return kRows ? 64 * half + 128 * (i >> 1) + 32 * (i & 1) : 32 * half + 64 * i; };
       auto wait_acc = [&]() {
-        const int got = mbar_wait(smem_u32(&tfull[acc & 1]), (acc >> 1) & 1, &s_abort) ? 1 : 0;
+        const int got = mbar_wait(smem_u32(&tfull[acc.at()]), acc.phase(), &s_abort) ? 1 : 0;
         // the group's warps share barriers in emit: they leave together
         const bool left = named_bar_or(1 + half, 128, got == 0);
         fence_after();
@@ -817,18 +851,18 @@ __global__ void __launch_bounds__(threads(MODE), 1)
       auto release_acc = [&]() {  // this warp's last read of the accumulator: it goes back to the MMAs
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc & 1]), 0));
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc.at()]), 0));
       };
       const uint32_t lanes = tmem_base + ((uint32_t)(32 * quarter) << 16);
       const int parts = none ? 1 : ((t.len + kBK - 1) / kBK + p.chunk - 1) / p.chunk;
-      if constexpr (kSum) {
+      if constexpr (kInRegs) {
         float sum[4][32];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int j = 0; j < 32; ++j) sum[i][j] = 0.0f;
         bool ok = true;
-        for (int q = 0; q < parts && !none; ++q, ++acc) {
+        for (int q = 0; q < parts && !none; ++q, acc.next(false)) {
           ok = wait_acc();
           if (!ok) break;
 #pragma unroll
@@ -838,7 +872,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 float d[16];
-                tmem_ld<16>(lanes + (acc & 1) * kN + c + 16 * h, d);
+                tmem_ld<16>(lanes + acc.at() * kN + c + 16 * h, d);
                 tmem_ld_wait();
 #pragma unroll
                 for (int j = 0; j < 16; ++j) sum[i][16 * h + j] += d[j];
@@ -852,6 +886,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
         for (int i = 0; i < 4; ++i)
           if (column(i) < t.cols) emit(column(i), sum[i], p.accumulate != 0);
       } else {
+        const bool stay = hold(t);
         bool ok = true;
         for (int q = 0; q < parts; ++q) {
           if (!none) {
@@ -859,7 +894,7 @@ __global__ void __launch_bounds__(threads(MODE), 1)
             if (!ok) break;
           }
           // a part is added to what the parts before it have left in memory
-          if (q > 0 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+          if (!kHold && q > 0 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
           bool held = !none;
           for (int i = 0; i < 4; ++i) {
             const int c = column(i);
@@ -869,17 +904,39 @@ __global__ void __launch_bounds__(threads(MODE), 1)
 #pragma unroll
               for (int j = 0; j < 32; ++j) d[j] = 0.0f;
             } else {
-              tmem_ld<32>(lanes + (acc & 1) * kN + c, d);
+              tmem_ld<32>(lanes + acc.at() * kN + c, d);
               tmem_ld_wait();
+              if constexpr (kHold) {
+                const uint32_t sum = lanes + (acc.at() ^ 1) * kN + c;
+                if (q > 0) {
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    float v[16];
+                    tmem_ld<16>(sum + 16 * h, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) d[16 * h + j] += v[j];
+                  }
+                }
+                if (q < parts - 1) {
+                  uint32_t w[32];
+#pragma unroll
+                  for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(d[j]);
+                  tmem_st16(sum, w);
+                  tmem_st16(sum + 16, w + 16);
+                  tmem_st_wait();
+                }
+              }
               if (i == 3 || column(i + 1) >= t.cols) {
                 release_acc();
                 held = false;
               }
+              if (kHold && q < parts - 1) continue;
             }
-            emit(c, d, p.accumulate != 0 || q > 0);
+            emit(c, d, p.accumulate != 0 || (!kHold && q > 0));
           }
           if (held) release_acc();  // no column of this unit was this warp's
-          if (!none) ++acc;
+          if (!none) acc.next(stay);
         }
         if (!ok) break;
       }
@@ -1152,9 +1209,16 @@ cudaError_t launch_tc_matmul16(const Matmul16Args& a, cudaStream_t st, int* unsu
   if (!p.tma_out) maps.o = maps.a;
   *unsupported = 0;
   p.chunk = f32 ? kAddStages : kNoChunk;
-  if (a.x_scales)
-    return a.rows > E * 256 ? launch<kWeightGradSavedLong, false>(maps, p, st, unsupported)
-                            : launch<kWeightGradSaved, false>(maps, p, st, unsupported);
+  if (a.x_scales) {
+    const bool many = a.rows > E * 256;  // rows per expert
+    if (!f32 && a.rows > plain_rows(w.dtype)) {
+      p.chunk = kHoldStages;
+      return many ? launch<kWeightGradSavedLong, true>(maps, p, st, unsupported)
+                  : launch<kWeightGradSaved, true>(maps, p, st, unsupported);
+    }
+    return many ? launch<kWeightGradSavedLong, false>(maps, p, st, unsupported)
+                : launch<kWeightGradSaved, false>(maps, p, st, unsupported);
+  }
   // fp32 and short on average: the few segments that are long are added in memory, the rest need
   // neither that nor registers for a sum. 16 bits: see "Long sums".
   if (f32 ? long_segments : a.rows > plain_rows(w.dtype)) {

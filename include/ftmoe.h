@@ -468,7 +468,8 @@ ftmoe_status ftmoe_grouped_matmul_wgrad(const void* dy, int64_t ld_dy, const voi
 /* The same gradient with x kept in 8 bits: x->format is FTMOE_FMT_MXFP8 (rows of k codes and
  * k/32 scale bytes, as ftmoe_quantize_act and ftmoe_gather_rows_scales write them). Codes are
  * decoded in front of the multiply; a code times a power of two is exact in bf16 (and in fp16
- * down to 2^-24), so dw is the gradient for the saved values with no further rounding. FP8
+ * down to 2^-24), so dw is the gradient for the saved values with no further rounding. Sums leave
+ * the accumulator after 1,024 terms (fp32), or 4,096 in calls of more rows than above (16 bits). FP8
  * rows (an fp32 scale per group) would have to be rounded to 16 bits first and are refused,
  * like NVFP4, as FTMOE_UNSUPPORTED. x->rows is the row count of dy too. */
 ftmoe_status ftmoe_grouped_matmul_wgrad_saved(const void* dy, int64_t ld_dy, int32_t dtype, const ftmoe_act* x,

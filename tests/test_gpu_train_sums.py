@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import block_quantized_moe_gb300 as ft
-from test_gpu_train import DEV, DT, U, gen, offsets_of, product_ref, wgrad_ref
+from test_gpu_train import DEV, DT, U, check, gen, normal, offsets_of, product_ref, saved, wgrad_ref
 
 pytestmark = pytest.mark.gpu
 LONG = 200_000
@@ -51,4 +51,42 @@ def test_weight_gradient_of_many_rows(dtype, rows, per, experts):
     ft.ftmoe_grouped_matmul_wgrad(dy, x, offsets_of(counts), dw)
     ref, _ = wgrad_ref(dy, x, counts)
     check_sum(dw, ref, rows, per, "weight gradient")
+    assert ft.ftmoe_read_error_flags() == 0
+
+
+@pytest.mark.parametrize("experts", [2, 1000])
+@pytest.mark.parametrize("dtype,rows,per", [("bf16", LONG, 4096), ("fp16", LONG, 4096), ("bf16", 32698, 32768), ("fp16", 4026, 4096),
+                                            ("fp16", 32698, 4096)])
+def test_weight_gradient_of_many_saved_rows(dtype, rows, per, experts):
+    """Where a segment takes several accumulators, they take 4,096 terms each."""
+    counts = [rows] + [0] * (experts - 2) + [70]
+    R, n, k = sum(counts), 136, 160
+    dy, x = positive((R, n), 0.1, DT[dtype], 5), positive((R, k), 1.0, torch.bfloat16, 6)
+    q, s, v = saved(x)
+    dw = torch.empty(experts, n, k, dtype=DT[dtype], device=DEV)
+    ft.ftmoe_grouped_matmul_wgrad_saved(dy, q, s, offsets_of(counts), dw)
+    ref, _ = wgrad_ref(dy, v, counts)
+    check_sum(dw, ref, rows, per, "weight gradient of saved rows")
+    assert ft.ftmoe_read_error_flags() == 0
+
+
+@pytest.mark.parametrize("empty,n,k", [(0, 1100, 2080), (120, 520, 1056), (120, 33, 64)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_saved_rows_long_and_short_segments_in_turn(empty, n, k, accumulate):
+    """Segments of one accumulator and of several, one after another on the same CTA pairs."""
+    counts = [4096, 4097, 100, 0, 9000, 64, 17000, 3] + [0] * empty
+    R = sum(counts)
+    dy, x = normal((R, n), 0.5, torch.bfloat16, 7), normal((R, k), 1.0, torch.bfloat16, 8)
+    q, s, v = saved(x)
+    old = normal((len(counts), n, k), 1.0, torch.bfloat16, 9)
+    got = []
+    for _ in range(3):
+        dw = old.clone()
+        ft.ftmoe_grouped_matmul_wgrad_saved(dy, q, s, offsets_of(counts), dw, accumulate=accumulate)
+        got.append(dw)
+    ref, mag = wgrad_ref(dy, v, counts)
+    if accumulate:
+        ref, mag = ref + old.double(), mag + old.double().abs()
+    check(got[0], ref, mag, max(counts), "weight gradient of saved rows")
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
     assert ft.ftmoe_read_error_flags() == 0
