@@ -61,11 +61,10 @@ __global__ void __launch_bounds__(32 * kWarps) stream_matmul16_kernel(Params p) 
     const int e = base + threadIdx.x;
     int lo = 0, m = 0;
     if (e < p.E) {
-      int hi = __ldg(p.offsets + e + 1);
-      lo = __ldg(p.offsets + e);
-      lo = lo < 0 ? 0 : lo;
-      hi = hi > p.rows ? (int)p.rows : hi;
-      m = hi - lo;
+      // (both cut to [0, rows], so that no difference of them leaves 32 bits)
+      const int most = (int)p.rows;
+      lo = max(0, min(__ldg(p.offsets + e), most));
+      m = max(0, min(__ldg(p.offsets + e + 1), most)) - lo;
     }
     const uint32_t have = __ballot_sync(0xffffffffu, m > 0);
     __syncthreads();  // the previous pass has read the list
