@@ -334,7 +334,11 @@ def ftmoe_expert_slots(expert_ids, slot_expert, slot_usage, expert_slot, step, m
 
 # The training entry points check what the C entry cannot see (devices, shapes, dtypes, contiguous
 # rows) in as few tensor queries as that takes: at decode sizes the binding costs more than the
-# kernel, and each query of a tensor costs about as much as a Python call.
+# kernel, and each query of a tensor costs about as much as a Python call. The kernels launch on
+# the current device, so all tensors of a call have to be there; where the process sees one device,
+# being on a CUDA device says that (asking every tensor for its index made a call 0.3 to 0.4 us longer).
+
+_one_device = None  # whether the process sees one device only; None until a call has asked
 
 def _dtype_code(t, name):
     code = _OUT_DTYPES.get(t.dtype)
@@ -343,10 +347,25 @@ def _dtype_code(t, name):
     return code
 
 
-def _refuse(t, name, shape, dtype):
-    """Says what is wrong with a tensor that failed a check."""
-    if not t.is_cuda:
+def _device_of(t, name):
+    """Index of the device that a call runs on: the tensor's, which has to be the current one."""
+    global _one_device
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} is not on a CUDA device")
+    if _one_device is None:
+        _one_device = torch.cuda.device_count() == 1
+    if dev != _current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{_current_device()}")
+    return dev
+
+
+def _refuse(t, name, shape, dtype, dev):
+    """Says what is wrong with a tensor that failed a check."""
+    if t.get_device() < 0:
+        raise ValueError(f"{name} is not on a CUDA device")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, other tensors of the call on cuda:{dev}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if dtype is not None and t.dtype != dtype:
@@ -354,71 +373,88 @@ def _refuse(t, name, shape, dtype):
     raise ValueError(f"the rows of {name} are not contiguous")
 
 
-def _rows_of(t, name, rows, cols, dtype=None):
+def _rows_of(t, name, rows, cols, dev, dtype=None):
     """Row stride of a [rows, cols] tensor with contiguous rows (any stride where there is one row)."""
-    if not t.is_cuda or t.shape != (rows, cols) or (dtype is not None and t.dtype != dtype):
-        _refuse(t, name, (rows, cols), dtype)
+    if not t.is_cuda or (not _one_device and t.get_device() != dev) or t.shape != (rows, cols) or (dtype is not None and t.dtype != dtype):
+        _refuse(t, name, (rows, cols), dtype, dev)
     ld, one = t.stride()
     if one != 1 and cols > 1 and rows:
-        _refuse(t, name, (rows, cols), dtype)
+        _refuse(t, name, (rows, cols), dtype, dev)
     return ld if rows > 1 else max(cols, ld)
 
 
-def _dense_of(t, name, shape, dtype):
+def _dense_of(t, name, shape, dtype, dev):
     """Address of a contiguous tensor of this shape."""
-    if not t.is_cuda or t.shape != shape or t.dtype != dtype or not t.is_contiguous():
-        _refuse(t, name, shape, dtype)
+    if not t.is_cuda or (not _one_device and t.get_device() != dev) or t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        _refuse(t, name, shape, dtype, dev)
     return t.data_ptr()
 
 
-def _raw_stream(stream, t):
-    """The stream handle as an int: the given one, or the current one of the tensor's device."""
+def _count_of(t, name, dev):
+    """Address of a row count, the first element of an int32 tensor (None for None)."""
+    if t is None:
+        return None
+    if not t.is_cuda or (not _one_device and t.get_device() != dev) or t.dtype != torch.int32 or t.numel() < 1:
+        _refuse(t, name, tuple(t.shape) if t.numel() else (1,), torch.int32, dev)
+    return t.data_ptr()
+
+
+def _raw_stream(stream, dev):
+    """The stream handle as an int: the given one, or the current one of the device."""
     if stream is None:
-        return _current_raw_stream(t.get_device())
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+        return _current_raw_stream(dev)
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device_index != dev:
+            raise ValueError(f"the stream is on cuda:{stream.device_index}, the call's tensors on cuda:{dev}")
+        return stream.cuda_stream
+    return int(stream)
 
 
 try:
-    _current_raw_stream = torch._C._cuda_getCurrentRawStream
+    _current_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 except AttributeError:  # a torch without CUDA
     def _current_raw_stream(device):
         return torch.cuda.current_stream(device).cuda_stream
+
+    def _current_device():
+        return torch.cuda.current_device()
 
 
 _pack_bank = struct.Struct("@iiqqqqP").pack  # the fields of MatrixBank, about three times as fast to fill
 
 
-def _bank_of(w):
-    """(bytes of a MatrixBank, E, n, k) of a [E, n, k] tensor."""
+def _bank_of(w, name, dev):
+    """(bytes of a MatrixBank, E, n, k) of a [E, n, k] tensor on CUDA device dev."""
     E, n, k = w.shape
     es, ld, one = w.stride()
     if not w.is_cuda or (one != 1 and k > 1):
-        _refuse(w, "w", (E, n, k), None)
+        _refuse(w, name, (E, n, k), None, dev)
     if n <= 1:
         ld = max(k, ld)
     if E <= 1:
         es = max((n - 1) * ld + k, es)
-    return _pack_bank(_dtype_code(w, "w"), E, n, k, ld, es, w.data_ptr()), E, n, k
+    return _pack_bank(_dtype_code(w, name), E, n, k, ld, es, w.data_ptr()), E, n, k
 
 
 def make_matrix_bank(w):
     """MatrixBank view of a [E, n, k] tensor of bf16, fp16 or fp32 matrices (any expert and row
     strides, contiguous rows)."""
-    return MatrixBank.from_buffer_copy(_bank_of(w)[0])
+    return MatrixBank.from_buffer_copy(_bank_of(w, "w", w.get_device())[0])
 
 
 def ftmoe_grouped_matmul(a, offsets, w, out, input_grad=False, stream=None):
     """out rows = a rows times the transposed matrix of their expert (input_grad: times the
     matrix itself). a [rows, k] (input_grad: [rows, n]), w [E, n, k], both bf16 or fp16; out
     [rows, n] (input_grad: [rows, k]) bf16, fp16 or fp32; offsets int32 [E + 1]."""
-    bank, E, wide_out, wide_in = _bank_of(w)
+    dev = 0 if _one_device else _device_of(w, "w")
+    bank, E, wide_out, wide_in = _bank_of(w, "w", dev)
     rows = a.shape[0]
     if input_grad:
         wide_in, wide_out = wide_out, wide_in
-    off = _dense_of(offsets, "offsets", (E + 1,), torch.int32)
-    ld_a, ld_out = _rows_of(a, "a", rows, wide_in, w.dtype), _rows_of(out, "out", rows, wide_out)
+    off = _dense_of(offsets, "offsets", (E + 1,), torch.int32, dev)
+    ld_a, ld_out = _rows_of(a, "a", rows, wide_in, dev, w.dtype), _rows_of(out, "out", rows, wide_out, dev)
     st = lib().ftmoe_grouped_matmul(a.data_ptr(), rows, ld_a, off, bank, 1 if input_grad else 0, out.data_ptr(), ld_out,
-                                    _dtype_code(out, "out"), _raw_stream(stream, a))
+                                    _dtype_code(out, "out"), _raw_stream(stream, dev))
     if st:
         raise FtmoeError("ftmoe_grouped_matmul", st)
 
@@ -426,38 +462,40 @@ def ftmoe_grouped_matmul(a, offsets, w, out, input_grad=False, stream=None):
 def ftmoe_grouped_matmul_wgrad(dy, x, offsets, dw, accumulate=False, stream=None):
     """dw[e] = dy_e^T x_e over the rows of expert e (accumulate: added to dw). dy [rows, n] and
     x [rows, k] bf16 or fp16, dw [E, n, k] bf16, fp16 or fp32."""
-    bank, E, n, k = _bank_of(dw)
+    dev = 0 if _one_device else _device_of(dw, "dw")
+    bank, E, n, k = _bank_of(dw, "dw", dev)
     rows, dt = dy.shape[0], dy.dtype
-    off = _dense_of(offsets, "offsets", (E + 1,), torch.int32)
-    ld_dy, ld_x = _rows_of(dy, "dy", rows, n), _rows_of(x, "x", rows, k, dt)
+    off = _dense_of(offsets, "offsets", (E + 1,), torch.int32, dev)
+    ld_dy, ld_x = _rows_of(dy, "dy", rows, n, dev), _rows_of(x, "x", rows, k, dev, dt)
     st = lib().ftmoe_grouped_matmul_wgrad(dy.data_ptr(), ld_dy, x.data_ptr(), ld_x, rows, _dtype_code(dy, "dy"), off,
-                                          bank, 1 if accumulate else 0, _raw_stream(stream, dw))
+                                          bank, 1 if accumulate else 0, _raw_stream(stream, dev))
     if st:
         raise FtmoeError("ftmoe_grouped_matmul_wgrad", st)
 
 
 def ftmoe_grouped_matmul_wgrad_saved(dy, q, scales, offsets, dw, fmt=FMT_MXFP8, accumulate=False, stream=None):
     """The same with x as MXFP8 rows: q uint8 [rows, k], scales uint8 [rows, k / 32]."""
-    bank, E, n, k = _bank_of(dw)
+    dev = 0 if _one_device else _device_of(dw, "dw")
+    bank, E, n, k = _bank_of(dw, "dw", dev)
     rows = dy.shape[0]
-    off = _dense_of(offsets, "offsets", (E + 1,), torch.int32)
-    ld_dy = _rows_of(dy, "dy", rows, n)
-    qp = _dense_of(q, "q", (rows, k), torch.uint8)
-    sp = _dense_of(scales, "scales", (rows, k // 32), torch.uint8) if fmt == FMT_MXFP8 else scales.data_ptr()
+    off = _dense_of(offsets, "offsets", (E + 1,), torch.int32, dev)
+    ld_dy = _rows_of(dy, "dy", rows, n, dev)
+    qp = _dense_of(q, "q", (rows, k), torch.uint8, dev)
+    sp = _dense_of(scales, "scales", (rows, k // 32), torch.uint8, dev) if fmt == FMT_MXFP8 else scales.data_ptr()
     act = Act(fmt, 0, rows, k, qp, sp, None)
     st = lib().ftmoe_grouped_matmul_wgrad_saved(dy.data_ptr(), ld_dy, _dtype_code(dy, "dy"), act, off, bank,
-                                                1 if accumulate else 0, _raw_stream(stream, dw))
+                                                1 if accumulate else 0, _raw_stream(stream, dev))
     if st:
         raise FtmoeError("ftmoe_grouped_matmul_wgrad_saved", st)
 
 
-def _saved_of(q, scales, rows, inter, fmt):
+def _saved_of(q, scales, rows, inter, fmt, dev):
     """Addresses of q uint8 [rows, 2 * inter] and scales [rows, 2 * groups] of kept gate/up rows."""
-    qp = _dense_of(q, "q", (rows, 2 * inter), torch.uint8)
+    qp = _dense_of(q, "q", (rows, 2 * inter), torch.uint8, dev)
     if fmt == FMT_FP8:
-        return qp, _dense_of(scales, "scales", (rows, 2 * cdiv(inter, 128)), torch.float32)
+        return qp, _dense_of(scales, "scales", (rows, 2 * cdiv(inter, 128)), torch.float32, dev)
     if fmt == FMT_MXFP8:
-        return qp, _dense_of(scales, "scales", (rows, 2 * (inter // 32)), torch.uint8)
+        return qp, _dense_of(scales, "scales", (rows, 2 * (inter // 32)), torch.uint8, dev)
     return qp, scales.data_ptr()
 
 
@@ -465,11 +503,12 @@ def ftmoe_silu_mul_save(gu, h, q, scales, fmt=FMT_MXFP8, rows_dev=None, stream=N
     """h = silu(gate) * up from gu [rows, 2 * inter], and both halves kept in 8 bits: q uint8
     [rows, 2 * inter], scales [rows, 2 * groups] (FP8: fp32 per 128, MXFP8: uint8 per 32)."""
     rows, inter = h.shape
-    ld_gu, ld_h = _rows_of(gu, "gu", rows, 2 * inter), _rows_of(h, "h", rows, inter)
-    qp, sp = _saved_of(q, scales, rows, inter, fmt)
+    dev = 0 if _one_device else _device_of(gu, "gu")
+    ld_gu, ld_h = _rows_of(gu, "gu", rows, 2 * inter, dev), _rows_of(h, "h", rows, inter, dev)
+    qp, sp = _saved_of(q, scales, rows, inter, fmt, dev)
     st = lib().ftmoe_silu_mul_save(gu.data_ptr(), _dtype_code(gu, "gu"), rows, inter, ld_gu,
-                                   None if rows_dev is None else rows_dev.data_ptr(), h.data_ptr(), ld_h,
-                                   _dtype_code(h, "h"), fmt, qp, sp, _raw_stream(stream, h))
+                                   _count_of(rows_dev, "rows_dev", dev), h.data_ptr(), ld_h,
+                                   _dtype_code(h, "h"), fmt, qp, sp, _raw_stream(stream, dev))
     if st:
         raise FtmoeError("ftmoe_silu_mul_save", st)
 
@@ -479,15 +518,15 @@ def ftmoe_silu_mul_backward(q, scales, dh, dgu, hw=None, row_weights=None, dweig
     """Gradients from the kept gate/up rows: dgu [rows, 2 * inter], hw = weight * h [rows, inter]
     and dweights fp32 [rows], for the gradient dh [rows, inter] of the unweighted h."""
     rows, inter = dh.shape
-    dt = dh.dtype
-    ld_dh, ld_dgu = _rows_of(dh, "dh", rows, inter), _rows_of(dgu, "dgu", rows, 2 * inter, dt)
-    hp, ld_hw = (None, 0) if hw is None else (hw.data_ptr(), _rows_of(hw, "hw", rows, inter, dt))
-    wp = None if row_weights is None else _dense_of(row_weights, "row_weights", (rows,), torch.float32)
-    dp = None if dweights is None else _dense_of(dweights, "dweights", (rows,), torch.float32)
-    qp, sp = _saved_of(q, scales, rows, inter, fmt)
-    st = lib().ftmoe_silu_mul_backward(qp, sp, fmt, rows, inter, None if rows_dev is None else rows_dev.data_ptr(),
+    dev, dt = 0 if _one_device else _device_of(dh, "dh"), dh.dtype
+    ld_dh, ld_dgu = _rows_of(dh, "dh", rows, inter, dev), _rows_of(dgu, "dgu", rows, 2 * inter, dev, dt)
+    hp, ld_hw = (None, 0) if hw is None else (hw.data_ptr(), _rows_of(hw, "hw", rows, inter, dev, dt))
+    wp = None if row_weights is None else _dense_of(row_weights, "row_weights", (rows,), torch.float32, dev)
+    dp = None if dweights is None else _dense_of(dweights, "dweights", (rows,), torch.float32, dev)
+    qp, sp = _saved_of(q, scales, rows, inter, fmt, dev)
+    st = lib().ftmoe_silu_mul_backward(qp, sp, fmt, rows, inter, _count_of(rows_dev, "rows_dev", dev),
                                        dh.data_ptr(), ld_dh, _dtype_code(dh, "dh"), wp, dgu.data_ptr(), ld_dgu, hp,
-                                       ld_hw, dp, _raw_stream(stream, dh))
+                                       ld_hw, dp, _raw_stream(stream, dev))
     if st:
         raise FtmoeError("ftmoe_silu_mul_backward", st)
 
