@@ -27,6 +27,7 @@ ftmoe_status check_matrix_bank(const ftmoe_matrix_bank* w, bool half_only) {
 
 // element addresses have to be multiples of the element
 bool aligned(const void* p, int32_t dtype) { return (uintptr_t)p % (dtype == FTMOE_OUT_FP32 ? 4 : 2) == 0; }
+bool aligned4(const void* p) { return (uintptr_t)p % 4 == 0; }
 
 }  // namespace
 
@@ -42,7 +43,8 @@ ftmoe_status ftmoe_grouped_matmul(const void* a, int64_t rows, int64_t ld_a, con
   if (ld_a < in || ld_out < outw || ld_a >= kMaxDim || ld_out >= kMaxDim) return FTMOE_INVALID_ARG;
   if (rows == 0) return FTMOE_OK;
   if (!a || !offsets || !out) return FTMOE_INVALID_ARG;
-  if (!aligned(a, w->dtype) || !aligned(w->w, w->dtype) || !aligned(out, out_dtype)) return FTMOE_INVALID_ARG;
+  if (!aligned(a, w->dtype) || !aligned(w->w, w->dtype) || !aligned(out, out_dtype) || !aligned4(offsets))
+    return FTMOE_INVALID_ARG;
   Matmul16Args g = {};
   g.a = a;
   g.ld_a = ld_a;
@@ -65,7 +67,9 @@ static ftmoe_status wgrad(const void* dy, int64_t ld_dy, const void* x, int64_t 
   if (st != FTMOE_OK) return st;
   if (ld_dy < dw->n || ld_x < dw->k || ld_dy >= kMaxDim || ld_x >= kMaxDim || !offsets) return FTMOE_INVALID_ARG;
   if (rows > 0 && (!dy || !x)) return FTMOE_INVALID_ARG;
-  if (!aligned(dy, dtype) || (!x_scales && !aligned(x, dtype)) || !aligned(dw->w, dw->dtype)) return FTMOE_INVALID_ARG;
+  if (!aligned(dy, dtype) || (!x_scales && !aligned(x, dtype)) || !aligned(dw->w, dw->dtype) ||
+      !aligned4(offsets))
+    return FTMOE_INVALID_ARG;
   Matmul16Args g = {};
   g.a = dy;
   g.ld_a = ld_dy;
@@ -110,7 +114,7 @@ ftmoe_status ftmoe_silu_mul_save(const void* gu, int32_t gu_dtype, int64_t rows,
   if (format == FTMOE_FMT_MXFP8 && inter % kMxBlock != 0) return FTMOE_INVALID_ARG;
   if (rows == 0) return FTMOE_OK;
   if (!gu || !h || !q || !scales) return FTMOE_INVALID_ARG;
-  if (!aligned(gu, gu_dtype) || !aligned(h, h_dtype) || (format == FTMOE_FMT_FP8 && (uintptr_t)scales % 4 != 0))
+  if (!aligned(gu, gu_dtype) || !aligned(h, h_dtype) || (format == FTMOE_FMT_FP8 && !aligned4(scales)) || !aligned4(rows_dev))
     return FTMOE_INVALID_ARG;
   SiluSaveArgs s = {gu, gu_dtype, rows, inter, ld_gu, rows_dev, h, ld_h, h_dtype, format == FTMOE_FMT_MXFP8, q, scales};
   return from_cuda(launch_silu_save(s, as_stream(stream)));
@@ -129,8 +133,7 @@ ftmoe_status ftmoe_silu_mul_backward(const uint8_t* q, const void* scales, int32
   if (rows == 0) return FTMOE_OK;
   if (!q || !scales || !dh || !dgu) return FTMOE_INVALID_ARG;
   if (!aligned(dh, dtype) || !aligned(dgu, dtype) || !aligned(hw, dtype) ||
-      (format == FTMOE_FMT_FP8 && (uintptr_t)scales % 4 != 0) || (uintptr_t)row_weights % 4 != 0 ||
-      (uintptr_t)dweights % 4 != 0)
+      (format == FTMOE_FMT_FP8 && !aligned4(scales)) || !aligned4(row_weights) || !aligned4(dweights) || !aligned4(rows_dev))
     return FTMOE_INVALID_ARG;
   SiluBackwardArgs s = {q,   scales, format == FTMOE_FMT_MXFP8, rows, inter, rows_dev, dh, ld_dh, dtype, row_weights,
                         dgu, ld_dgu, hw, ld_hw, dweights};

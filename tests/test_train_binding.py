@@ -171,3 +171,23 @@ def test_banks_of_matrices(calls):
               dev(E, N, K, dtype=torch.int64)):
         with pytest.raises(ValueError):
             ft.make_matrix_bank(t)
+
+
+def test_counts_and_bounds_off_their_alignment_are_refused():
+    """The C entries answer an offsets or rows_dev address off 4 bytes with an error, on the host."""
+    import ctypes
+
+    from block_quantized_moe_gb300 import build_lib
+    build_lib.build()
+    P, bad = ctypes.c_void_p, ft.FTMOE_INVALID_ARG
+    bank = ctypes.byref(ft.MatrixBank(0, E, N, K, K, N * K, P(256)))
+    act = ctypes.byref(ft.Act(ft.FMT_MXFP8, 0, R, K, P(256), P(256), None))
+    lib = ft.lib()
+    for off in (257, 258, 259):
+        assert lib.ftmoe_grouped_matmul(P(256), R, K, P(off), bank, 0, P(256), N, 0, None) == bad
+        assert lib.ftmoe_grouped_matmul_wgrad(P(256), N, P(256), K, R, 0, P(off), bank, 0, None) == bad
+        assert lib.ftmoe_grouped_matmul_wgrad_saved(P(256), N, 0, act, P(off), bank, 0, None) == bad
+        assert lib.ftmoe_silu_mul_save(P(256), 0, R, K, 2 * K, P(off), P(256), K, 0, ft.FMT_MXFP8, P(256), P(256),
+                                       None) == bad
+        assert lib.ftmoe_silu_mul_backward(P(256), P(256), ft.FMT_MXFP8, R, K, P(off), P(256), K, 0, None, P(256), 2 * K,
+                                           None, 0, None, None) == bad
