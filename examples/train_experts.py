@@ -30,6 +30,8 @@ class _ExpertFFN(torch.autograd.Function):
     def forward(ctx, x, route_weights, w_gateup, w_down, expert_ids):
         """x [T, H] and the banks w_gateup [E, 2I, H], w_down [E, H, I] in bf16; route_weights
         fp32 [T, topk]; expert_ids int32 [T, topk], < 0 for an inactive route. Returns [T, H]."""
+        # (rows and routes are handed on by address: dense)
+        x, route_weights, expert_ids = x.contiguous(), route_weights.contiguous(), expert_ids.contiguous()
         T, H = x.shape
         E, inter = w_down.shape[0], w_down.shape[2]
         topk, dev = expert_ids.shape[1], x.device
@@ -97,6 +99,22 @@ class _ExpertFFN(torch.autograd.Function):
 
 
 def expert_ffn(x, route_weights, w_gateup, w_down, expert_ids):
+    """The routed FFN's output [T, H] for x bf16 [T, H], route_weights fp32 [T, topk], the banks w_gateup
+    bf16 [E, 2 I, H] and w_down bf16 [E, H, I], and expert_ids int32 [T, topk] (< 0: an inactive
+    route); H and I multiples of 32. x, the weights and the ids may have any strides."""
+    if w_down.dim() != 3 or x.dim() != 2 or expert_ids.dim() != 2:
+        raise ValueError("expert_ffn takes x [T, H], banks of three axes and expert_ids [T, topk]")
+    (T, H), (E, _, inter) = x.shape, w_down.shape
+    for name, t, shape, dtype in (("x", x, (T, H), torch.bfloat16), ("w_gateup", w_gateup, (E, 2 * inter, H), torch.bfloat16),
+                                  ("w_down", w_down, (E, H, inter), torch.bfloat16),
+                                  ("expert_ids", expert_ids, (T, expert_ids.shape[1]), torch.int32),
+                                  ("route_weights", route_weights, (T, expert_ids.shape[1]), torch.float32)):
+        if tuple(t.shape) != shape or t.dtype != dtype:
+            raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}, expected {dtype} {shape}")
+        if t.device != w_down.device or not t.is_cuda:
+            raise ValueError(f"{name} is on {t.device}: all operands have to be on one CUDA device")
+    if H % 32 or inter % 32:
+        raise ValueError(f"hidden size {H} and intermediate size {inter} have to be multiples of 32 (MXFP8 groups)")
     return _ExpertFFN.apply(x, route_weights, w_gateup, w_down, expert_ids)
 
 

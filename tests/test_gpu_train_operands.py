@@ -1,0 +1,46 @@
+"""Operands of the training example's expert_ffn as a model hands them over."""
+import pytest
+import torch
+
+import block_quantized_moe_gb300 as ft
+import synth
+from examples.train_experts import expert_ffn
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+T, H, INTER, E, TOPK = 37, 128, 96, 5, 3
+
+
+def operands(seed=1, active=None):
+    ids = synth.routes(T, TOPK, E, seed, active_per_token=active, device=DEV)
+    banks = [torch.stack([synth.expert_weight_fp32(n, k, seed, e, tag, DEV, std=0.1) for e in range(E)]).to(torch.bfloat16)
+             for n, k, tag in ((2 * INTER, H, "g"), (H, INTER, "d"))]
+    return [synth.activations_bf16(T, H, seed + 1, DEV), synth.routing_weights(T, TOPK, seed + 2, DEV), *banks], ids
+
+
+def step(args, ids, dout, needs=(True,) * 4):
+    args = [t.detach().requires_grad_(n) for t, n in zip(args, needs)]
+    out = expert_ffn(*args, ids)
+    out.backward(dout)
+    return out.detach(), [t.grad for t in args]
+
+
+def wider(t):
+    """The same values as columns of a tensor whose other columns hold something else."""
+    w = torch.full((*t.shape[:-1], t.shape[-1] + 5), 7, dtype=t.dtype, device=DEV)
+    w[..., 2:-3] = t
+    return w[..., 2:-3]
+
+
+@pytest.mark.parametrize("change", [wider, lambda t: t.T.contiguous().T, lambda t: wider(t.repeat_interleave(2, 0))[::2]])
+def test_strides(change):
+    """Column slices, transposed storage and every other row: the same bits as from dense operands."""
+    args, ids = operands()
+    dout = synth.activations_bf16(T, H, 9, DEV)
+    want, grads = step(args, ids, dout)
+    x, weights = change(args[0]), change(args[1])
+    got, other = step([x, weights, *args[2:]], change(ids), change(dout))
+    assert torch.equal(got, want)
+    for a, b in zip(other, grads):
+        assert torch.equal(a, b)
+    assert ft.ftmoe_read_error_flags() == 0
