@@ -20,6 +20,7 @@ import os
 import sys
 
 import torch
+from torch.autograd.function import once_differentiable
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import block_quantized_moe_gb300 as ft  # noqa: E402
@@ -61,6 +62,7 @@ class _ExpertFFN(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable  # (the kernels' results have no gradients of their own)
     def backward(ctx, dout):
         (x_q, x_s, gu_q, gu_s, route_weights, w_gateup, w_down, expert_ids, offsets, dst2src,
          route2dst) = ctx.saved_tensors

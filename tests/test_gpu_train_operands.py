@@ -44,3 +44,12 @@ def test_strides(change):
     for a, b in zip(other, grads):
         assert torch.equal(a, b)
     assert ft.ftmoe_read_error_flags() == 0
+
+
+def test_second_derivatives_are_refused():
+    args, ids = operands()
+    args = [t.detach().requires_grad_() for t in args]
+    out = expert_ffn(*args, ids).float()
+    dx, = torch.autograd.grad(out.square().sum(), args[0], create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        (dx.float().square().sum() + args[0].float().square().sum()).backward()
