@@ -69,10 +69,9 @@ class _ExpertFFN(torch.autograd.Function):
         dout = dout.contiguous()
         (T, H), (E, _, inter), dev = dout.shape, w_down.shape, dout.device
         routes, active = dst2src.shape[0], offsets[E:]
-        grouped = route2dst.long().clamp(min=0)
-        used = (route2dst >= 0).float()
-        # the weight of each grouped row (inactive routes add nothing to row 0)
-        row_weights = torch.zeros(routes, device=dev).index_add_(0, grouped, route_weights.reshape(-1) * used)
+        grouped, used = route2dst.long().clamp(min=0), route2dst >= 0
+        # the weight of each grouped row (inactive routes add nothing to row 0, whatever their weight)
+        row_weights = torch.zeros(routes, device=dev).index_add_(0, grouped, route_weights.reshape(-1).where(used, 0.0))
 
         dy = torch.empty(routes, H, dtype=dout.dtype, device=dev)
         ft.ftmoe_gather_rows_scales(dout, None, dst2src, dy, None, n_dst_dev=active)
@@ -96,7 +95,7 @@ class _ExpertFFN(torch.autograd.Function):
         ft.ftmoe_gather_rows_scales(x_q, x_s, dst2src, rows_q, rows_s, n_dst_dev=active)
         dw_gateup = torch.empty_like(w_gateup)
         ft.ftmoe_grouped_matmul_wgrad_saved(dgu, rows_q, rows_s, offsets, dw_gateup)
-        dweights = (drow[grouped] * used).view_as(route_weights)
+        dweights = drow[grouped].where(used, 0.0).view_as(route_weights)
         return dx, dweights, dw_gateup, dw_down, None
 
 

@@ -53,3 +53,24 @@ def test_second_derivatives_are_refused():
     dx, = torch.autograd.grad(out.square().sum(), args[0], create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         (dx.float().square().sum() + args[0].float().square().sum()).backward()
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_weights_of_inactive_routes_are_not_used(value):
+    """What an inactive route's weight holds changes nothing, and its own gradient is zero; also where
+    the first grouped row's is not finite."""
+    args, ids = operands(active=[k % 4 for k in range(T)])
+    inactive = ids < 0
+    assert inactive.any() and not inactive.all()
+    dout = synth.activations_bf16(T, H, 9, DEV)
+    want, grads = step(args, ids, dout)
+    weights = args[1].masked_fill(inactive, value)
+    got, other = step([args[0], weights, *args[2:]], ids, dout)
+    assert torch.equal(got, want)
+    for a, b in zip(other, grads):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
+    assert (other[1][inactive] == 0).all()
+    first = int(torch.nonzero(ids == ids[ids >= 0].min())[0, 0])  # the token of the first grouped row
+    dout[first] = value
+    _, other = step([args[0], weights, *args[2:]], ids, dout)
+    assert (other[1][inactive] == 0).all() and not torch.isfinite(other[1][first][~inactive[first]]).any()
