@@ -67,6 +67,8 @@ class _ExpertFFN(torch.autograd.Function):
         (x_q, x_s, gu_q, gu_s, route_weights, w_gateup, w_down, expert_ids, offsets, dst2src,
          route2dst) = ctx.saved_tensors
         dout = dout.contiguous()
+        need_x, _, need_gateup, need_down, _ = ctx.needs_input_grad  # (a frozen bank has no gradient to compute)
+        dx = dw_gateup = dw_down = None
         (T, H), (E, _, inter), dev = dout.shape, w_down.shape, dout.device
         routes, active = dst2src.shape[0], offsets[E:]
         grouped, used = route2dst.long().clamp(min=0), route2dst >= 0
@@ -78,23 +80,24 @@ class _ExpertFFN(torch.autograd.Function):
         dh = torch.empty(routes, inter, dtype=dout.dtype, device=dev)
         ft.ftmoe_grouped_matmul(dy, offsets, w_down, dh, input_grad=True)
         dgu = torch.empty(routes, 2 * inter, dtype=dout.dtype, device=dev)
-        hw = torch.empty_like(dh)
+        hw = torch.empty_like(dh) if need_down else None
         drow = torch.zeros(routes, device=dev)
         ft.ftmoe_silu_mul_backward(gu_q, gu_s, dh, dgu, hw=hw, row_weights=row_weights, dweights=drow,
                                    fmt=ft.FMT_MXFP8, rows_dev=active)
-        dw_down = torch.empty_like(w_down)
-        ft.ftmoe_grouped_matmul_wgrad(dy, hw, offsets, dw_down)
-
-        dx_rows = torch.empty(routes, H, dtype=torch.float32, device=dev)
-        ft.ftmoe_grouped_matmul(dgu, offsets, w_gateup, dx_rows, input_grad=True)
-        dx = torch.empty_like(dout)
-        ft.ftmoe_combine(dx_rows, expert_ids, torch.ones_like(route_weights), dx, route2dst=route2dst)
-
-        rows_q = torch.empty(routes, H, dtype=torch.uint8, device=dev)
-        rows_s = torch.empty(routes, H // 32, dtype=torch.uint8, device=dev)
-        ft.ftmoe_gather_rows_scales(x_q, x_s, dst2src, rows_q, rows_s, n_dst_dev=active)
-        dw_gateup = torch.empty_like(w_gateup)
-        ft.ftmoe_grouped_matmul_wgrad_saved(dgu, rows_q, rows_s, offsets, dw_gateup)
+        if need_down:
+            dw_down = torch.empty_like(w_down)
+            ft.ftmoe_grouped_matmul_wgrad(dy, hw, offsets, dw_down)
+        if need_x:
+            dx_rows = torch.empty(routes, H, dtype=torch.float32, device=dev)
+            ft.ftmoe_grouped_matmul(dgu, offsets, w_gateup, dx_rows, input_grad=True)
+            dx = torch.empty_like(dout)
+            ft.ftmoe_combine(dx_rows, expert_ids, torch.ones_like(route_weights), dx, route2dst=route2dst)
+        if need_gateup:
+            rows_q = torch.empty(routes, H, dtype=torch.uint8, device=dev)
+            rows_s = torch.empty(routes, H // 32, dtype=torch.uint8, device=dev)
+            ft.ftmoe_gather_rows_scales(x_q, x_s, dst2src, rows_q, rows_s, n_dst_dev=active)
+            dw_gateup = torch.empty_like(w_gateup)
+            ft.ftmoe_grouped_matmul_wgrad_saved(dgu, rows_q, rows_s, offsets, dw_gateup)
         dweights = drow[grouped].where(used, 0.0).view_as(route_weights)
         return dx, dweights, dw_gateup, dw_down, None
 

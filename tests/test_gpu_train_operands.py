@@ -74,3 +74,21 @@ def test_weights_of_inactive_routes_are_not_used(value):
     dout[first] = value
     _, other = step([args[0], weights, *args[2:]], ids, dout)
     assert (other[1][inactive] == 0).all() and not torch.isfinite(other[1][first][~inactive[first]]).any()
+
+
+@pytest.mark.parametrize("needs", [(True, False, False, False), (False, True, False, False), (False, False, True, False),
+                                   (False, False, False, True), (True, True, False, False)])
+def test_gradients_that_are_not_needed_are_not_computed(needs, monkeypatch):
+    args, ids = operands()
+    dout = synth.activations_bf16(T, H, 9, DEV)
+    _, want = step(args, ids, dout)
+    made = []
+    for name in ("ftmoe_grouped_matmul_wgrad", "ftmoe_grouped_matmul_wgrad_saved"):
+        def call(*a, _f=getattr(ft, name), _name=name, **kw):
+            made.append(_name)
+            return _f(*a, **kw)
+        monkeypatch.setattr(ft, name, call)
+    _, got = step(args, ids, dout, needs)
+    for need, a, b in zip(needs, got, want):
+        assert torch.equal(a, b) if need else a is None
+    assert made == ["ftmoe_grouped_matmul_wgrad"] * needs[3] + ["ftmoe_grouped_matmul_wgrad_saved"] * needs[2]
