@@ -54,7 +54,8 @@ class _ExpertFFN(torch.autograd.Function):
         y = torch.empty(routes, H, dtype=torch.float32, device=dev)
         ft.ftmoe_grouped_matmul(h, offsets, w_down, y)
         out = torch.empty_like(x)
-        ft.ftmoe_combine(y, expert_ids, route_weights, out, route2dst=route2dst)
+        if T:  # (the other calls take no rows as nothing to do)
+            ft.ftmoe_combine(y, expert_ids, route_weights, out, route2dst=route2dst)
 
         x_q, x_s, _ = ft.quantize_act(x, ft.FMT_MXFP8)
         ctx.save_for_backward(x_q, x_s, gu_q, gu_s, route_weights, w_gateup, w_down, expert_ids, offsets, dst2src,
@@ -91,7 +92,8 @@ class _ExpertFFN(torch.autograd.Function):
             dx_rows = torch.empty(routes, H, dtype=torch.float32, device=dev)
             ft.ftmoe_grouped_matmul(dgu, offsets, w_gateup, dx_rows, input_grad=True)
             dx = torch.empty_like(dout)
-            ft.ftmoe_combine(dx_rows, expert_ids, torch.ones_like(route_weights), dx, route2dst=route2dst)
+            if T:
+                ft.ftmoe_combine(dx_rows, expert_ids, torch.ones_like(route_weights), dx, route2dst=route2dst)
         if need_gateup:
             rows_q = torch.empty(routes, H, dtype=torch.uint8, device=dev)
             rows_s = torch.empty(routes, H // 32, dtype=torch.uint8, device=dev)

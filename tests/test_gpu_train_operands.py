@@ -92,3 +92,12 @@ def test_gradients_that_are_not_needed_are_not_computed(needs, monkeypatch):
     for need, a, b in zip(needs, got, want):
         assert torch.equal(a, b) if need else a is None
     assert made == ["ftmoe_grouped_matmul_wgrad"] * needs[3] + ["ftmoe_grouped_matmul_wgrad_saved"] * needs[2]
+
+
+def test_no_tokens():
+    args, ids = operands()
+    got, grads = step([args[0][:0], args[1][:0], *args[2:]], ids[:0], args[0][:0])
+    assert got.shape == (0, H)
+    for g, a in zip(grads, [args[0][:0], args[1][:0], *args[2:]]):
+        assert g.shape == a.shape and (g == 0).all()
+    assert ft.ftmoe_read_error_flags() == 0
