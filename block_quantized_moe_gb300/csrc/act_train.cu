@@ -36,7 +36,9 @@ using Pair = F32Pair;
 // exp(-x) = 2^t (1 + ln2 (T - t)) with T = -x log2(e) and t its fp32 rounding: the difference T - t,
 // from the residual of the product, log2(e)'s low part and r, keeps the exponential to a few units
 // in the last place however large |g| is (the rounding of t alone would cost |g| of them). The
-// factor is applied as a factor, so that an infinite 2^t stays infinite. 1 + e is scaled by 2^-24
+// factor is applied as a factor, so that an infinite 2^t stays infinite; it is near 1 unless t has left
+// fp32's range, where T - t is infinite or NaN: cut at 2 it leaves a 2^t of zero zero (x above 2.36e38
+// has the sigmoid 1, like all x above 17). 1 + e is scaled by 2^-24
 // before the reciprocal, which would flush to zero from 2^126 on, and its result again. (Where
 // exp(-x) passes fp32's range, x < -88.7, the sigmoid is 0; its value there is below 1e-38.)
 constexpr float kLog2e = 1.44269502f, kLog2eLow = 1.92596303e-8f, kLn2 = 0.693147182f, kDown = 0x1p-24f;
@@ -49,7 +51,9 @@ __device__ __forceinline__ Pair sigmoid(Pair g, Pair r) {
   t.get(t_lo, t_hi);
   asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(t_lo));
   asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(t_hi));
-  const Pair e = Pair(t_lo, t_hi) * fma2(rest, Pair(kLn2), Pair(1.0f));
+  float f_lo, f_hi;
+  fma2(rest, Pair(kLn2), Pair(1.0f)).get(f_lo, f_hi);
+  const Pair e = Pair(t_lo, t_hi) * Pair(fminf(f_lo, 2.0f), fminf(f_hi, 2.0f));
   float y_lo, y_hi;
   fma2(e, Pair(kDown), Pair(kDown)).get(y_lo, y_hi);
   asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(y_lo));
@@ -166,9 +170,8 @@ __global__ void __launch_bounds__(256, 4) silu_save_kernel(
     load(g_next, u_next);
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
-      // (the sigmoid is 1 long before 128, and the product with an infinite g has no residual)
-      const Pair x(fminf(g[i], 128.0f), fminf(g[i + 1], 128.0f));
-      (Pair(g[i], g[i + 1]) * sigmoid<false>(x, x) * Pair(u[i], u[i + 1])).get(a[i], a[i + 1]);
+      const Pair x(g[i], g[i + 1]);
+      (x * sigmoid<false>(x, x) * Pair(u[i], u[i + 1])).get(a[i], a[i + 1]);
     }
     float sg, su;
     uint8_t bg, bu;
