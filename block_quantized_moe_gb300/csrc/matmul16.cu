@@ -163,14 +163,22 @@ cudaError_t launch_matmul16_general(const Matmul16Args& a, cudaStream_t st) {
   return mm16::run(p, a.dtype, a.out_dtype, false, (cdiv(a.rows, 64) + w.num_experts) * cdiv(p.n, 64), st);
 }
 
-// The streaming kernel where the tensor-core kernel would have at most 38 units of 256 weight
-// rows, half of what fills the GPU. Measured on GB300 (streaming, tensor cores, microseconds):
-// two rows over two experts, 1536 x 2048 (12 units) 5.5, 12.9; one row, 4096 x 7168 (16 units)
-// 19, 33; from there on the units suffice: eight rows over eight experts, 1536 x 2048 (48) 14.3,
-// 14.4; over eight experts, 2048 x 4096 (64) 33, 30; four rows of one expert, 4096 x 7168 46, 33.
+// The streaming kernel where its rows, times units of 256 weight rows, are at most a quarter of the
+// SMs (38), and an expert has at most the four rows that one pass over its weights takes, on average. It
+// fills the GPU whatever the number of units, but its time grows with every row; the tensor-core
+// kernel's is that of one unit until the units are more than half of the CTA pairs. Measured on GB300,
+// one launch after another (streaming, tensor cores, us):
+//   1 expert, 1536 x 2048:  1 row 4.0, 10.8;  2 rows 5.7, 10.9;  4 rows 9.2, 11.1;  5 rows 11.3, 11.1
+//   1 expert, 2048 x 4096:  1 row 7.1, 18.5;  4 rows 17.2, 18.6;  8 rows 31.5, 18.9
+//   1 expert, 4096 x 7168:  1 row 19.6, 30.0;  2 rows 31.0, 30.0;  4 rows 53.1, 30.0;  16 rows 198, 30.5
+//   rows spread over 8 experts, 512 x 7168:  4 rows 11.7, 29.5;  8 rows 18.7, 30.2;  16 rows 30.0, 30.2
+//   over 8 experts, 1536 x 2048:  5 rows 9.8, 12.1;  8 rows 15.0, 13.4;  16 rows 23.8, 13.5
+//   over 2 experts, 1536 x 2048:  5 rows 8.4, 11.4;  12 rows 14.3, 11.4
+// (16 rows that all go to one of 8 experts, 512 x 7168, take 102 where the tensor cores would take 26:
+// the host does not know where they go.)
 static bool prefer_stream(const Matmul16Args& a) {
-  const int64_t hit = a.rows < a.w.num_experts ? a.rows : a.w.num_experts;
-  return a.rows <= 16 && hit * cdiv(a.w.n, 256) <= 38 && stream_matmul16_ok(a);
+  return a.rows <= 16 && a.rows <= 4 * (int64_t)a.w.num_experts && a.rows * cdiv(a.w.n, 256) <= sm_count_once() / 4 &&
+         stream_matmul16_ok(a);
 }
 
 cudaError_t launch_matmul16(const Matmul16Args& a, cudaStream_t st) {
