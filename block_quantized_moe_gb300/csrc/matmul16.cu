@@ -52,7 +52,8 @@ __global__ void __launch_bounds__(256) general_kernel(Params p) {
     int64_t lo, hi;
     segment(p, e, lo, hi);
     const int64_t m = p.ragged_m ? hi - lo : p.m, len = p.ragged_m ? p.l : hi - lo;
-    const int64_t units = ((m + kT - 1) / kT) * nj;
+    // (nothing to add keeps the old values as they are, zeros of either sign and NaN among them)
+    const int64_t units = p.accumulate && len == 0 ? 0 : ((m + kT - 1) / kT) * nj;
     for (; unit < done + units; unit += gridDim.x) {
       const int64_t local = unit - done;
       const int64_t i0 = local / nj * kT, j0 = local % nj * kT;

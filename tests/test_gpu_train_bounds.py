@@ -41,3 +41,24 @@ def test_bounds_of_any_value(bounds, parts, rows, n, k):
         written[rows + lo:rows + hi] = True
     assert torch.isnan(base[~written]).all()
     assert ft.ftmoe_read_error_flags() == 0
+
+
+@pytest.mark.parametrize("kept", [False, True])
+@pytest.mark.parametrize("n,k,rows", [(64, 64, 5), (33, 47, 5), (64, 64, 0)])
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+def test_experts_without_rows_keep_their_bits(n, k, rows, out, kept):
+    """Accumulating into an expert without rows leaves every bit: zeros of both signs, NaN, subnormals."""
+    k = 64 if kept else k
+    c, x = normal((rows, n), 1.0, torch.bfloat16, 4), normal((rows, k), 1.0, torch.bfloat16, 5)
+    dw = torch.zeros(3, n, k, dtype=out, device=DEV)
+    dw[0, :, ::2], dw[0, 0, 1], dw[2, 0, 3], dw[2, -1], dw[2, 0, 0] = -0.0, float("nan"), 1e-40, -0.0, float("inf")
+    old = dw.clone()
+    off = torch.tensor([0, 0, rows, rows], dtype=torch.int32, device=DEV)
+    if kept:
+        q, s = torch.zeros(rows, k, dtype=torch.uint8, device=DEV), torch.full((rows, k // 32), 127, dtype=torch.uint8, device=DEV)
+        ft.ftmoe_grouped_matmul_wgrad_saved(c, q, s, off, dw, accumulate=True)
+    else:
+        ft.ftmoe_grouped_matmul_wgrad(c, x, off, dw, accumulate=True)
+    bits = torch.int32 if out == torch.float32 else torch.int16
+    for e in (0, 2) if rows else (0, 1, 2):
+        assert torch.equal(dw[e].view(bits), old[e].view(bits)), e
