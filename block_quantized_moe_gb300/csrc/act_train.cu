@@ -1,19 +1,23 @@
 // SiLU-and-mul that keeps its gate/up rows in 8 bits, and its backward pass from them.
 //
 // Forward, per row: h = silu(g) * u with silu(g) = g * s, s = 1 / (1 + exp(-g)); g and u are
-// kept as e4m3 codes with an fp32 scale per 128 (amax times fp32's 1 / 448: the multiplication
-// may differ from the division in the last bit, which a scale that travels with its codes does
-// not notice) or a power of two per 32.
+// kept as e4m3 codes with an fp32 scale per 128 or a power of two per 32. The fp32 scale is amax times
+// fp32's 1 / 448, which is what torch's CUDA kernels make of a division by that constant, so that the
+// codes are those of rows kept by plain torch operations. The quantizers of the forward divide: their
+// scale differs in the last bit for about half of the groups, and a code on a midpoint may then go the
+// other way. The scale travels with its codes, and both leave the same error (2.571% of the norm, for
+// normal values).
 // Backward, with the kept g and u, the gradient dh of the unweighted h and the routing weight w:
 //   d h / d u = g s,   d h / d g = u s (1 + g (1 - s))
 //   dgu = w dh (d h / d g | d h / d u),   hw = w h,   dweight = sum_i dh_i h_i
 // Both passes are elementwise but for the group maxima and dweight. The forward moves 8 bytes per
 // intermediate column (4 read, 2 + 2 written) and 1/16 to 1/32 of scales, the backward 10 (2 codes
 // and 2 of dh read, 4 + 2 written): memory bounds them, closely followed by the issue rate (about
-// 310 and 340 instructions per warp and 8 columns a lane). Keeping gate/up in bf16 would move 4
-// more bytes per column and hold twice the memory between the passes. Measured on GB300, both
-// passes of 24,576 rows of 2,048 columns, bf16, FP8: 154 us, 5.9 TB/s, 88% of the measured copy
-// rate (280 us before packed fp32 pairs, the sigmoid below and the loads ahead).
+// 310 and 340 instructions per warp and 8 columns a lane). Reading the bf16 gate/up rows again instead
+// would move as many bytes (2 less written, 2 more read a column) and hold twice the memory between the
+// passes. Measured on GB300, both passes of 24,576 rows of 2,048 columns, bf16: FP8 156 us (5.8 TB/s, 86%
+// of the measured copy rate), MXFP8 156 us (FP8 280 us before packed fp32 pairs, the sigmoid below and
+// the loads ahead).
 #include <type_traits>
 
 #include "common.cuh"

@@ -336,7 +336,7 @@ struct Maps {
   CUtensorMap a, o, b[8];
 };
 
-// Register splits (setmaxnreg). With kSum 384 threads launch with 168 registers each; the control
+// Register splits (setmaxnreg). Sums in registers: 384 threads launch with 168 each; the control
 // warpgroup keeps 80, the two epilogue warpgroups take 208. From saved rows 768 (long
 // segments: 896) threads launch with 80 (72): control keeps 56, the epilogue takes 96, the decoding
 // warpgroups, a team each, keep 72 (64).

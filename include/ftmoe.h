@@ -446,10 +446,11 @@ typedef struct ftmoe_matrix_bank {
  * for the rows r of every expert e. a and w are bf16 or fp16, both w->dtype; out is
  * out_dtype (that type or any other), rounded to nearest even once from an fp32 sum. (The tensor
  * core's fp32 accumulator cuts low bits off as it adds; after 512 terms for fp32 outputs, 2,048 for
- * 16-bit ones, sums leave it and are added rounding to nearest.) Row strides ld_a, ld_out in elements. Rows at or beyond offsets[E] are neither read nor
- * written. Any sizes and strides are taken; where every base, row stride and expert stride of
- * a and w is a multiple of 16 bytes (and there are at most 1,024 experts) the tensor cores or,
- * for few rows, the streaming kernel run, else a slower general kernel. w is only read. rows == 0 launches nothing. */
+ * 16-bit ones, sums leave it and are added rounding to nearest.) Row strides ld_a, ld_out in
+ * elements. Rows at or beyond offsets[E] are not used and not written. Any sizes and strides are
+ * taken; where every base, row stride and expert stride of a and w is a multiple of 16 bytes (and
+ * there are at most 1,024 experts) the tensor cores or, for few rows, the streaming kernel run, else
+ * a slower general kernel. w is only read. rows == 0 launches nothing. */
 ftmoe_status ftmoe_grouped_matmul(const void* a, int64_t rows, int64_t ld_a, const int32_t* offsets,
                                   const ftmoe_matrix_bank* w, int32_t input_grad, void* out, int64_t ld_out,
                                   int32_t out_dtype, void* stream);
@@ -467,9 +468,10 @@ ftmoe_status ftmoe_grouped_matmul_wgrad(const void* dy, int64_t ld_dy, const voi
 
 /* The same gradient with x kept in 8 bits: x->format is FTMOE_FMT_MXFP8 (rows of k codes and
  * k/32 scale bytes, as ftmoe_quantize_act and ftmoe_gather_rows_scales write them). Codes are
- * decoded in front of the multiply; a code times a power of two is exact in bf16 (and in fp16
- * down to 2^-24), so dw is the gradient for the saved values with no further rounding. Sums leave
- * the accumulator after 1,024 terms (fp32), or 4,096 in calls of more rows than above (16 bits). FP8
+ * decoded in front of the multiply. A code times a power of two is exact in bf16 down to a last bit of
+ * 2^-133, and in fp16 down to one of 2^-24 and up to 65,504 (a larger value is infinite there; rows kept
+ * from fp16 values have none), so dw is the gradient for the saved values with no further rounding.
+ * Sums leave the accumulator after 1,024 terms (fp32), or 4,096 in calls of more rows than above (16 bits). FP8
  * rows (an fp32 scale per group) would have to be rounded to 16 bits first and are refused,
  * like NVFP4, as FTMOE_UNSUPPORTED. x->rows is the row count of dy too. */
 ftmoe_status ftmoe_grouped_matmul_wgrad_saved(const void* dy, int64_t ld_dy, int32_t dtype, const ftmoe_act* x,
@@ -480,7 +482,8 @@ ftmoe_status ftmoe_grouped_matmul_wgrad_saved(const void* dy, int64_t ld_dy, int
  *   h[i] = silu(g[i]) * u[i],  g = gu[row, 0:inter], u = gu[row, inter:2*inter]
  * (fp32, rounded once to h_dtype) from the values of gu themselves, and both halves kept as
  * e4m3 codes, q uint8 [rows][2][inter]. FTMOE_FMT_FP8: per 1x128 group s = amax * (1/448) (an
- * fp32 product; ftmoe_quantize_act divides, which may differ in the last bit), code =
+ * fp32 product, what amax / 448 is in torch's CUDA arithmetic; ftmoe_quantize_act divides, which may
+ * differ in the last bit, and a code on a midpoint with it), code =
  * e4m3_rne_satfinite(x / s), s in scales float [rows][2][ceil(inter/128)]; amax = 0 gives s = 0
  * and zero codes. FTMOE_FMT_MXFP8 (inter % 32 == 0): codes and bytes as ftmoe_quantize_act
  * writes them for a row of `inter` elements, scales E8M0 [rows][2][inter/32]. NVFP4 is
