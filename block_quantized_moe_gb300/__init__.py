@@ -20,6 +20,8 @@ FMT_FP8, FMT_NVFP4, FMT_MXFP8 = 0, 1, 2
 ROUTES_GROUPED, ROUTES_SLOTS = 0, 1
 ERR_EXPERT_ID_RANGE, ERR_MAP_RANGE, ERR_WAIT_TIMEOUT = 0x1, 0x2, 0x4
 OUT_BF16, OUT_FP16, OUT_FP32 = 0, 1, 2
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+MOMENTS_FP32, MOMENTS_8BIT = 0, 1
 _OUT_DTYPES = {torch.bfloat16: OUT_BF16, torch.float16: OUT_FP16, torch.float32: OUT_FP32}
 
 c_i32, c_i64, c_ptr, c_size = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
@@ -64,6 +66,33 @@ class MoeArgs(ctypes.Structure):
 class MatrixBank(ctypes.Structure):
     _fields_ = [("dtype", c_i32), ("num_experts", c_i32), ("n", c_i64), ("k", c_i64), ("ld", c_i64),
                 ("expert_stride", c_i64), ("w", c_ptr)]
+
+
+class Router(ctypes.Structure):
+    _fields_ = [("num_experts", c_i32), ("topk", c_i32), ("score", c_i32), ("renormalize", c_i32), ("groups", c_i32),
+                ("group_topk", c_i32), ("group_best", c_i32), ("scale", ctypes.c_float)]
+
+
+class Grad(ctypes.Structure):
+    _fields_ = [("n", c_i64), ("grad", c_ptr)]
+
+
+class GradList(ctypes.Structure):
+    _fields_ = [("dtype", c_i32), ("count", c_i32), ("grads", ctypes.POINTER(Grad))]
+
+
+class AdamwTensor(ctypes.Structure):
+    _fields_ = [("n", c_i64)] + [(f, c_ptr) for f in ("param", "grad", "m", "v", "m_scales", "v_scales", "copy")]
+
+
+class AdamwList(ctypes.Structure):
+    _fields_ = [("param_dtype", c_i32), ("grad_dtype", c_i32), ("copy_dtype", c_i32), ("moments", c_i32),
+                ("count", c_i32), ("tensors", ctypes.POINTER(AdamwTensor))]
+
+
+class Adamw(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_double) for f in ("lr", "beta1", "beta2", "eps", "weight_decay")] + \
+        [("step", c_i64), ("seed", ctypes.c_uint32), ("lr_dev", c_ptr), ("step_dev", c_ptr), ("grad_scale", c_ptr)]
 
 
 _LAYOUT_FIELDS = ["x_q", "x_scales", "x_gscale", "counts", "offsets", "dst2src", "route2dst",
@@ -114,6 +143,13 @@ _SIGNATURES = [
                                     c_ptr, c_ptr]),
     ("ftmoe_silu_mul_backward", c_i32, [c_ptr, c_ptr, c_i32, c_i64, c_i64, c_ptr, c_ptr, c_i64, c_i32, c_ptr, c_ptr,
                                         c_i64, c_ptr, c_i64, c_ptr, c_ptr]),
+    ("ftmoe_route_tokens", c_i32, [c_ptr, c_i32, c_i64, c_i64, ctypes.POINTER(Router), c_ptr, c_ptr, c_ptr, c_ptr,
+                                   c_ptr]),
+    ("ftmoe_route_tokens_backward", c_i32, [c_ptr, c_i32, c_i64, c_i64, ctypes.POINTER(Router), c_ptr, c_ptr, c_ptr,
+                                            c_ptr, c_i32, c_i64, c_ptr]),
+    ("ftmoe_grad_norm_workspace_bytes", c_size, [ctypes.POINTER(GradList)]),
+    ("ftmoe_grad_norm", c_i32, [ctypes.POINTER(GradList), ctypes.c_float, ctypes.c_float, c_ptr, c_size, c_ptr, c_ptr]),
+    ("ftmoe_adamw_step", c_i32, [ctypes.POINTER(AdamwList), c_ptr, c_ptr]),
     ("ftmoe_selftest_wait_timeout", c_i32, [ctypes.c_uint64, c_ptr, c_ptr]),
     ("ftmoe_selftest_shared_division", c_i32, [c_ptr, c_ptr]),
     ("ftmoe_expert_slots", c_i32, [c_ptr, c_i64, c_ptr, c_ptr, c_i32, c_ptr, c_i32, c_i64, c_i32, c_ptr, c_ptr,
@@ -529,6 +565,163 @@ def ftmoe_silu_mul_backward(q, scales, dh, dgu, hw=None, row_weights=None, dweig
                                        ld_hw, dp, _raw_stream(stream, dev))
     if st:
         raise FtmoeError("ftmoe_silu_mul_backward", st)
+
+
+def make_router(num_experts, topk, score=SCORE_SOFTMAX, renormalize=True, groups=1, group_topk=None, group_best=1,
+                scale=1.0):
+    """How tokens are routed (ftmoe_router). group_topk: None keeps every group."""
+    return Router(num_experts, topk, score, int(renormalize), groups, groups if group_topk is None else group_topk,
+                  group_best, scale)
+
+
+def ftmoe_route_tokens(logits, router, expert_ids, weights, bias=None, tokens_dev=None, stream=None):
+    """expert_ids int32 [T, topk] and weights fp32 [T, topk] from logits [T, E] (bf16, fp16 or
+    fp32); bias fp32 [E]; tokens_dev int32: tokens at and beyond it get inactive routes."""
+    dev = 0 if _one_device else _device_of(logits, "logits")
+    T, E, k = logits.shape[0], router.num_experts, router.topk
+    ld = _rows_of(logits, "logits", T, E, dev)
+    ids, w = _dense_of(expert_ids, "expert_ids", (T, k), torch.int32, dev), _dense_of(weights, "weights", (T, k), torch.float32, dev)
+    bp = None if bias is None else _dense_of(bias, "bias", (E,), torch.float32, dev)
+    st = lib().ftmoe_route_tokens(logits.data_ptr(), _dtype_code(logits, "logits"), T, ld, router, bp,
+                                  _count_of(tokens_dev, "tokens_dev", dev), ids, w, _raw_stream(stream, dev))
+    if st:
+        raise FtmoeError("ftmoe_route_tokens", st)
+
+
+def ftmoe_route_tokens_backward(logits, router, expert_ids, weights, dweights, dlogits, stream=None):
+    """dlogits [T, E] (bf16, fp16 or fp32) for the gradient dweights fp32 [T, topk] of the weights
+    that ftmoe_route_tokens gave with expert_ids."""
+    dev = 0 if _one_device else _device_of(logits, "logits")
+    T, E, k = logits.shape[0], router.num_experts, router.topk
+    ld, ld_d = _rows_of(logits, "logits", T, E, dev), _rows_of(dlogits, "dlogits", T, E, dev)
+    ids, w = _dense_of(expert_ids, "expert_ids", (T, k), torch.int32, dev), _dense_of(weights, "weights", (T, k), torch.float32, dev)
+    dw = _dense_of(dweights, "dweights", (T, k), torch.float32, dev)
+    st = lib().ftmoe_route_tokens_backward(logits.data_ptr(), _dtype_code(logits, "logits"), T, ld, router, ids, w, dw,
+                                           dlogits.data_ptr(), _dtype_code(dlogits, "dlogits"), ld_d,
+                                           _raw_stream(stream, dev))
+    if st:
+        raise FtmoeError("ftmoe_route_tokens_backward", st)
+
+
+def _flat_of(t, name, dev, dtypes):
+    """Elements of a contiguous tensor (any shape) on CUDA device dev."""
+    if not t.is_cuda or t.get_device() != dev:
+        _refuse(t, name, tuple(t.shape), None, dev)
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} is {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+    return t.numel()
+
+
+class _List:
+    """Tensors handed to a call by address: the C list, its entries, and the tensors that it keeps alive."""
+
+    def __init__(self, c_list, entries, tensors, device):
+        self.c_list, self.entries, self.tensors, self.device = c_list, entries, tensors, device
+
+
+def _same_place(addresses, what):
+    if len(set(addresses)) != len(addresses):
+        raise ValueError(f"{what}: a tensor occurs twice")
+
+
+def make_grad_list(grads):
+    """The gradients of ftmoe_grad_norm: contiguous CUDA tensors of one dtype (bf16, fp16 or
+    fp32) on the current device. The list holds their addresses: make a new one for other tensors."""
+    grads = list(grads)
+    dev, dtype = (_device_of(grads[0], "grads[0]"), grads[0].dtype) if grads else (_current_device(), torch.float32)
+    if grads:
+        _dtype_code(grads[0], "grads[0]")
+    entries = (Grad * max(1, len(grads)))()
+    for i, g in enumerate(grads):
+        entries[i] = Grad(_flat_of(g, f"grads[{i}]", dev, (dtype,)), g.data_ptr())
+    return _List(GradList(_OUT_DTYPES[dtype], len(grads), entries), entries, grads, dev)
+
+
+def _on_list_device(tensors):
+    if tensors.device != _current_device():
+        raise ValueError(f"the list's tensors are on cuda:{tensors.device}, the current device is cuda:{_current_device()}")
+    return tensors.device
+
+
+def ftmoe_grad_norm_workspace_bytes(grads):
+    return int(lib().ftmoe_grad_norm_workspace_bytes(grads.c_list))
+
+
+def ftmoe_grad_norm(grads, result, workspace, scale=1.0, max_norm=float("inf"), stream=None):
+    """result fp32 [2]: the norm of scale times all gradients of the list, and the factor scale *
+    min(1, max_norm / (norm + 1e-6)) that ftmoe_adamw_step takes as grad_scale."""
+    dev = _on_list_device(grads)
+    rp = _dense_of(result, "result", (2,), torch.float32, dev)
+    size = _flat_of(workspace, "workspace", dev, (torch.uint8, torch.float64)) * workspace.element_size()
+    st = lib().ftmoe_grad_norm(grads.c_list, scale, max_norm, workspace.data_ptr(), size, rp, _raw_stream(stream, dev))
+    if st:
+        raise FtmoeError("ftmoe_grad_norm", st)
+
+
+def make_adamw_list(params, grads, m, v, m_scales=None, v_scales=None, copies=None):
+    """The tensors of ftmoe_adamw_step: for each parameter its gradient and moments (contiguous
+    CUDA tensors of the same size on the current device, any shape; one dtype of each kind).
+    m and v are fp32, or kept in 8 bits: m as uint8 or float8_e4m3fn, v as uint8 or float8_e5m2
+    codes, m_scales and v_scales uint8 or float8_e8m0fnu with a byte per 32 elements. copies:
+    16-bit tensors that receive the new parameters. The list holds addresses: make a new one for other tensors."""
+    params, kinds = list(params), {}
+    for name, given in (("grads", grads), ("m", m), ("v", v), ("m_scales", m_scales), ("v_scales", v_scales), ("copies", copies)):
+        kinds[name] = None if given is None else list(given)
+        if given is not None and len(kinds[name]) != len(params):
+            raise ValueError(f"{len(kinds[name])} {name} for {len(params)} params")
+    if (m_scales is None) != (v_scales is None):
+        raise ValueError("m_scales and v_scales belong together")
+    narrow = m_scales is not None
+    dev = _device_of(params[0], "params[0]") if params else _current_device()
+    p_dtype, g_dtype = (params[0].dtype, kinds["grads"][0].dtype) if params else (torch.float32, torch.float32)
+    c_dtype = kinds["copies"][0].dtype if params and copies is not None else None
+    if params:
+        _dtype_code(params[0], "params[0]")
+        _dtype_code(kinds["grads"][0], "grads[0]")
+        if c_dtype not in (None, torch.bfloat16, torch.float16):
+            raise ValueError(f"copies[0] is {c_dtype}, expected torch.bfloat16 or torch.float16")
+    scale_types = (torch.uint8, torch.float8_e8m0fnu)
+    types = {"grads": (g_dtype,), "copies": (c_dtype,), "m_scales": scale_types, "v_scales": scale_types,
+             "m": (torch.uint8, torch.float8_e4m3fn) if narrow else (torch.float32,),
+             "v": (torch.uint8, torch.float8_e5m2) if narrow else (torch.float32,)}
+    entries, written = (AdamwTensor * max(1, len(params)))(), []
+    for i, p in enumerate(params):
+        n = _flat_of(p, f"params[{i}]", dev, (p_dtype,))
+        at = {"params": p.data_ptr()}
+        for name, tensors in kinds.items():
+            at[name] = None
+            if tensors is not None:
+                want = cdiv(n, 32) if name.endswith("scales") else n
+                if _flat_of(tensors[i], f"{name}[{i}]", dev, types[name]) != want:
+                    raise ValueError(f"{name}[{i}] has {tensors[i].numel()} elements, expected {want}")
+                at[name] = tensors[i].data_ptr()
+        if n:
+            written += [a for name, a in at.items() if a is not None]
+        entries[i] = AdamwTensor(n, at["params"], at["grads"], at["m"], at["v"], at["m_scales"], at["v_scales"], at["copies"])
+    _same_place(written, "make_adamw_list")
+    c_list = AdamwList(_OUT_DTYPES[p_dtype], _OUT_DTYPES[g_dtype], -1 if c_dtype is None else _OUT_DTYPES[c_dtype],
+                       MOMENTS_8BIT if narrow else MOMENTS_FP32, len(params), entries)
+    return _List(c_list, entries, (params, kinds), dev)
+
+
+_pack_adamw = struct.Struct("@dddddqI4xPPP").pack  # the fields of Adamw
+
+
+def ftmoe_adamw_step(tensors, step=1, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=1e-2, grad_scale=None, seed=0,
+                     lr_dev=None, step_dev=None, stream=None):
+    """One AdamW step on every tensor of the list (make_adamw_list), in place. step counts from 1.
+    grad_scale, lr_dev fp32 [1] and step_dev int64 [1]: values on the device, the last two in place of lr and step;
+    nothing is written where grad_scale is NaN or infinite. seed: of the rounding of 8-bit moments."""
+    dev = _on_list_device(tensors)
+    at = [0 if t is None else _dense_of(t, name, (1,), dtype, dev)
+          for name, t, dtype in (("lr_dev", lr_dev, torch.float32), ("step_dev", step_dev, torch.int64),
+                                 ("grad_scale", grad_scale, torch.float32))]
+    opt = _pack_adamw(lr, beta1, beta2, eps, weight_decay, step, seed, *at)
+    st = lib().ftmoe_adamw_step(tensors.c_list, opt, _raw_stream(stream, dev))
+    if st:
+        raise FtmoeError("ftmoe_adamw_step", st)
 
 
 def ftmoe_selftest_wait_timeout(timeout_ns, elapsed_ns=None, stream=None):

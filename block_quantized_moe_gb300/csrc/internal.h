@@ -340,6 +340,50 @@ cudaError_t launch_stream_matmul16(const Matmul16Args& a, cudaStream_t s);
 cudaError_t launch_tc_matmul16(const Matmul16Args& a, cudaStream_t s, int* unsupported);
 uint32_t read_err_tc_matmul16();
 
+// route.cu: routing of tokens to experts, and its gradient
+struct RouteArgs {
+  const void* logits;
+  int32_t dtype;           // ftmoe_out_dtype
+  int64_t tokens, ld;
+  ftmoe_router router;
+  const float* bias;
+  const int32_t* tokens_dev;
+  int32_t* ids_out;
+  float* weights_out;
+  // backward
+  const int32_t* ids;
+  const float* weights;
+  const float* dweights;
+  void* dlogits;
+  int32_t dlogits_dtype;
+  int64_t ld_dlogits;
+  // set by the launchers
+  bool vec, vec_out;       // rows may be read (written) in vectors of eight elements
+  int group_lanes;         // lanes of a warp that hold a group, 0: not whole lanes or no power of two
+};
+constexpr int32_t kRouteMaxExperts = 1024, kRouteMaxTopk = 32, kRouteMaxGroups = 32;
+cudaError_t launch_route(RouteArgs a, cudaStream_t s);
+cudaError_t launch_route_backward(RouteArgs a, cudaStream_t s);
+uint32_t read_err_route();
+
+// adamw.cu: an AdamW step over many tensors
+struct AdamwConstants {
+  float lr, beta1, beta2, rest1, rest2, eps, weight_decay;  // rest: 1 - beta
+  float ln_beta1, ln_beta2;                                 // for corrections by a step on the device
+  float correction1, correction2;                           // 1 / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
+  uint32_t seed;
+  int64_t step;
+  const float* lr_dev;
+  const int64_t* step_dev;
+  const float* grad_scale;
+};
+cudaError_t launch_adamw(const ftmoe_adamw_list& list, const AdamwConstants& c, cudaStream_t s);
+
+// grad_norm.cu: global norm of many gradients
+size_t grad_norm_workspace(const ftmoe_grad_list& list);
+cudaError_t launch_grad_norm(const ftmoe_grad_list& list, float scale, float max_norm, double* parts, float* result,
+                             cudaStream_t s);
+
 // selftest.cu
 uint32_t read_err_selftest();
 

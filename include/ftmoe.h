@@ -511,6 +511,145 @@ ftmoe_status ftmoe_silu_mul_backward(const uint8_t* q, const void* scales, int32
                                      int32_t dtype, const float* row_weights, void* dgu, int64_t ld_dgu, void* hw,
                                      int64_t ld_hw, float* dweights, void* stream);
 
+/* ------------------------------------------------------------------------------------
+ * Around the experts' products (no counterpart in the pages; services of this library): the
+ * router that makes expert_ids and weights from its logits, with its gradient, and what uses
+ * the gradients of a training step: their global norm and an AdamW step. The logits are a
+ * product of ftmoe_grouped_matmul with one expert, whose matrix is the router's.
+ * ------------------------------------------------------------------------------------ */
+
+typedef enum ftmoe_score { FTMOE_SCORE_SOFTMAX = 0, FTMOE_SCORE_SIGMOID = 1 } ftmoe_score;
+
+/* How tokens are routed. num_experts <= 1024, topk <= 32, groups <= 32 (larger:
+ * FTMOE_UNSUPPORTED). */
+typedef struct ftmoe_router {
+  int32_t num_experts;
+  int32_t topk;         /* experts per token, at most group_topk * num_experts / groups */
+  int32_t score;        /* ftmoe_score */
+  int32_t renormalize;  /* 1: the weights of a token sum to scale */
+  int32_t groups;       /* divides num_experts: groups of consecutive experts; 1: none */
+  int32_t group_topk;   /* groups a token may choose from, 1..groups */
+  int32_t group_best;   /* a group's score: the sum of its 1 or 2 best values (groups > 1) */
+  float scale;          /* of the weights, > 0 and finite */
+} ftmoe_router;
+
+/* Routing: for each token, with x its logits,
+ *   s[e] = softmax(x)[e] or 1 / (1 + exp(-x[e])),   value[e] = s[e] + bias[e]
+ * (without bias: s[e]); with groups > 1 only the experts of the group_topk groups of the largest
+ * scores can be chosen; the topk experts of the largest values are, largest first, and
+ *   weights[i] = scale * s[id_i]             or, with renormalize,
+ *   weights[i] = scale * s[id_i] / sum_j s[id_j].
+ * Ties go to the lower group and the lower expert. The order is that of the values in 64 bits;
+ * without bias that of the logits. An expert whose logit or bias is -inf or NaN is never chosen
+ * (a NaN or -inf logit counts as exp(x) = 0 in the softmax), +inf counts as the largest finite number;
+ * where fewer than topk experts are left the last slots are inactive routes, id -1 and weight 0. The
+ * weights are exact to fp32's rounding, also where every chosen sigmoid underflows.
+ * logits: [tokens][num_experts], dtype an ftmoe_out_dtype, row stride ld. bias: float
+ * [num_experts] or NULL. tokens_dev: optional device int32 count; the tokens at and beyond it get
+ * inactive routes (ids -1, weights 0) and their logits are not read. expert_ids int32
+ * [tokens][topk] and weights float [tokens][topk], as ftmoe_segment_routes, ftmoe_moe_forward and
+ * ftmoe_combine take them. */
+ftmoe_status ftmoe_route_tokens(const void* logits, int32_t dtype, int64_t tokens, int64_t ld,
+                                const ftmoe_router* router, const float* bias, const int32_t* tokens_dev,
+                                int32_t* expert_ids, float* weights, void* stream);
+
+/* Gradient of the logits for the gradient dweights float [tokens][topk] of the weights, from what
+ * ftmoe_route_tokens gave (the choice itself has none). With c = scale, w = weights,
+ * r_i = w_i dweights_i, R = sum_i r_i and s as above:
+ *   softmax, renormalize:   dlogits[id_i] = r_i - w_i R / c          others 0
+ *   softmax:                dlogits[e] = (e = id_i ? r_i : 0) - s[e] R
+ *   sigmoid, renormalize:   dlogits[id_i] = (1 - s[id_i]) (r_i - w_i R / c)    others 0
+ *   sigmoid:                dlogits[id_i] = (1 - s[id_i]) r_i                  others 0
+ * Inactive routes (id < 0) take no part, whatever their weight and gradient; a token without an
+ * active route gets zeros and its logits are not read. An id that occurs twice in a token gets the
+ * sum; one >= num_experts raises FTMOE_ERR_EXPERT_ID_RANGE and takes no part. dlogits
+ * [tokens][num_experts] is dlogits_dtype with row stride ld_dlogits; every element is written. */
+ftmoe_status ftmoe_route_tokens_backward(const void* logits, int32_t dtype, int64_t tokens, int64_t ld,
+                                         const ftmoe_router* router, const int32_t* expert_ids, const float* weights,
+                                         const float* dweights, void* dlogits, int32_t dlogits_dtype,
+                                         int64_t ld_dlogits, void* stream);
+
+/* A gradient: n consecutive elements of the list's dtype. n = 0: nothing (grad may be NULL). */
+typedef struct ftmoe_grad {
+  int64_t n;
+  const void* grad;
+} ftmoe_grad;
+
+/* Many gradients. `grads` is a HOST array of count entries, read during the call only. */
+typedef struct ftmoe_grad_list {
+  int32_t dtype; /* ftmoe_out_dtype */
+  int32_t count;
+  const ftmoe_grad* grads;
+} ftmoe_grad_list;
+
+/* Bytes of the workspace that ftmoe_grad_norm needs for this list (0: the list is not valid). */
+size_t ftmoe_grad_norm_workspace_bytes(const ftmoe_grad_list* list);
+
+/* Global norm of the gradients after scaling by `scale` (e.g. one over a loss scale), and the
+ * factor that takes the unscaled gradients to scaled and clipped ones:
+ *   result[0] = norm = scale * sqrt(sum of squares of every element of every gradient)
+ *   result[1] = scale * min(1, max_norm / (norm + 1e-6));  NaN where the norm is not finite
+ * result: device float[2]; result + 1 is a grad_scale for ftmoe_adamw_step, which takes no step for
+ * a NaN. max_norm > 0 (INFINITY: no clipping), scale > 0 and finite. Squares are summed in fp32
+ * over a few elements and from there in fp64; where they leave fp32's range they are taken in
+ * fp64, so that gradients of any finite size have their norm. The order of the sums is fixed by the
+ * sizes: the same bits every time. The workspace (8-byte aligned; contents need not be set) is
+ * used until the call's work completes, by one call at a time. */
+ftmoe_status ftmoe_grad_norm(const ftmoe_grad_list* list, float scale, float max_norm, void* workspace,
+                             size_t workspace_bytes, float* result, void* stream);
+
+/* How AdamW's moments are kept. 8BIT: per 32 consecutive elements of a tensor (the last group may
+ * be shorter) an E8M0 byte b for 2^(b - 127), and codes: e4m3 for the first moment m, e5m2 for
+ * the second, v; value = code * 2^(b - 127). The power is the smallest of at least 2^-127 for which the group's
+ * largest magnitude is at most the format's largest (448; 57,344). Codes are rounded
+ * stochastically: up with the probability of what is cut off (to 16 bits), so that moments
+ * which change by less than half a step still move, on average by what they should. A v above zero
+ * is never rounded to zero (its code is at least 1). NaN and infinite moments are kept as NaN (m)
+ * and infinity (v). The random bits are a hash of (seed, step, tensor's place in the list,
+ * element). */
+typedef enum ftmoe_moments { FTMOE_MOMENTS_FP32 = 0, FTMOE_MOMENTS_8BIT = 1 } ftmoe_moments;
+
+/* One tensor of an AdamW step: n consecutive elements of each array. n = 0: nothing. */
+typedef struct ftmoe_adamw_tensor {
+  int64_t n;
+  void* param;       /* param_dtype */
+  const void* grad;  /* grad_dtype */
+  void* m;           /* float, or e4m3 codes */
+  void* v;           /* float, or e5m2 codes */
+  void* m_scales;    /* 8BIT: uint8 [ceil(n / 32)] */
+  void* v_scales;
+  void* copy;        /* copy_dtype: receives the new parameters, rounded to nearest even */
+} ftmoe_adamw_tensor;
+
+/* Many tensors of the same types. `tensors` is a HOST array of count entries, read during the
+ * call only. No array may overlap another one of the call, of the same or another tensor. */
+typedef struct ftmoe_adamw_list {
+  int32_t param_dtype; /* ftmoe_out_dtype; 16-bit parameters are rounded to nearest even at each step */
+  int32_t grad_dtype;  /* ftmoe_out_dtype */
+  int32_t copy_dtype;  /* FTMOE_OUT_BF16 or FTMOE_OUT_FP16; -1: no copies */
+  int32_t moments;     /* ftmoe_moments */
+  int32_t count;
+  const ftmoe_adamw_tensor* tensors;
+} ftmoe_adamw_list;
+
+typedef struct ftmoe_adamw {
+  double lr, beta1, beta2, eps, weight_decay; /* eps >= 1e-30; 0 <= beta < 1 */
+  int64_t step;            /* t, counted from 1 */
+  uint32_t seed;           /* of the 8-bit moments' rounding */
+  const float* lr_dev;     /* optional device float[1] in place of lr */
+  const int64_t* step_dev; /* optional device int64[1] in place of step (a value below 1 counts as 1) */
+  const float* grad_scale; /* optional device float[1]: gradients are multiplied by it first */
+} ftmoe_adamw;
+
+/* One AdamW step (decoupled weight decay) on every tensor:
+ *   g = grad_scale * grad,  m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
+ *   param = param (1 - lr weight_decay) - lr m / (1 - beta1^t) / (sqrt(v / (1 - beta2^t)) + eps)
+ * in fp32 (the products and sums of m and v each rounded to nearest), the update from the moments before
+ * they are rounded to 8 bits. Where *grad_scale is NaN or infinite no step is taken: nothing
+ * is written. lr_dev, step_dev and grad_scale let a captured graph be replayed as training
+ * goes on. Arrays of any alignment are taken; 16 bytes (8 for codes) is fastest. */
+ftmoe_status ftmoe_adamw_step(const ftmoe_adamw_list* list, const ftmoe_adamw* opt, void* stream);
+
 /* Self-test of the bounded pipeline waits (failure detection; the pages have no counterpart).
  * Every wait of the TMA/tensor-core pipelines gives up after a time limit (4 s), raises
  * FTMOE_ERR_WAIT_TIMEOUT in the device error word and lets its kernel return normally, so a
