@@ -74,13 +74,10 @@ __device__ __forceinline__ float inverse_scale(uint32_t byte) {
   return byte >= 254u ? __uint_as_float(0x00400000u) : __uint_as_float((254u - byte) << 23);
 }
 
-__device__ __forceinline__ uint32_t group_max(uint32_t v) {
-  v = max(v, __shfl_xor_sync(0xffffffffu, v, 1));
-  return max(v, __shfl_xor_sync(0xffffffffu, v, 2));
-}
-
-__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  return a | (b << 8) | (c << 16) | (d << 24);
+// the largest of the four lanes of a group
+__device__ __forceinline__ float group_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
 }
 
 // eight bytes at p, or the first n of them
@@ -104,13 +101,12 @@ __device__ __forceinline__ void store_codes(uint8_t* p, bool vec, int n, uint2 c
 
 // the values of eight codes
 template <__nv_fp8_interpretation_t kFormat>
-__device__ __forceinline__ void decode8(uint2 c, float scale, float (&v)[8]) {
+__device__ __forceinline__ void decode8(uint2 c, float scale, F32Pair (&v)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t two = (i < 2 ? c.x : c.y) >> (16 * (i & 1));
     const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xffffu), kFormat)));
-    v[2 * i] = __fmul_rn(f.x, scale);
-    v[2 * i + 1] = __fmul_rn(f.y, scale);
+    v[i] = F32Pair(f.x, f.y) * F32Pair(scale);
   }
 }
 
@@ -119,10 +115,174 @@ __device__ __forceinline__ float square_root(float x) {
   asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// (of a number from eps to 2^126)
 __device__ __forceinline__ float reciprocal(float x) {
   float r;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+
+// what a step needs of its constants
+struct Step {
+  float grad_scale, beta1, beta2, rest1, rest2, eps;
+  float decay;       // lr * weight decay
+  float rate;        // lr / (1 - beta1^t)
+  float correction;  // 1 / sqrt(1 - beta2^t)
+  float one;         // 1, which the compiler does not know: x * one + y is a sum that it cannot fuse with the product x
+};
+
+// the step on eight elements
+__device__ __forceinline__ void update8(const Step& s, float (&p)[8], const float (&grad)[8], F32Pair (&m)[4], F32Pair (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const F32Pair g = F32Pair(grad[2 * i], grad[2 * i + 1]) * F32Pair(s.grad_scale);
+    m[i] = fma2(m[i] * F32Pair(s.beta1), F32Pair(s.one), g * F32Pair(s.rest1));
+    v[i] = fma2(v[i] * F32Pair(s.beta2), F32Pair(s.one), g * g * F32Pair(s.rest2));
+    float a, b;
+    v[i].get(a, b);
+    fma2(F32Pair(square_root(a), square_root(b)), F32Pair(s.correction), F32Pair(s.eps)).get(a, b);
+    const F32Pair old(p[2 * i], p[2 * i + 1]);
+    const F32Pair less = fma2(m[i] * F32Pair(reciprocal(a), reciprocal(b)), F32Pair(s.rate), old * F32Pair(s.decay));
+    fma2(less, F32Pair(-1.0f), old).get(p[2 * i], p[2 * i + 1]);
+  }
+}
+
+// Codes of eight elements' moments; the lanes of a group call together, its other elements are theirs.
+// h: random bits of the chunk.
+__device__ __forceinline__ void encode8(const F32Pair (&m)[4], const F32Pair (&v)[4], uint32_t base, uint2& mc, uint2& vc,
+                                        uint32_t& m_byte, uint32_t& v_byte) {
+  float m_top = 0.0f, v_top = 0.0f;
+  F32Pair zero(0.0f);  // NaN where an element is not finite
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    zero = fma2(m[i], F32Pair(0.0f), fma2(v[i], F32Pair(0.0f), zero));
+    m[i].get(a, b);
+    m_top = fmaxf(fmaxf(m_top, fabsf(a)), fabsf(b));
+    v[i].get(a, b);
+    v_top = fmaxf(fmaxf(v_top, a), b);
+  }
+  m_byte = scale_byte<8>(__float_as_uint(group_max(m_top)));
+  v_byte = scale_byte<15>(__float_as_uint(group_max(v_top)));
+  const F32Pair mf(inverse_scale(m_byte)), vf(inverse_scale(v_byte));
+  uint32_t h[8];
+  noise8(base, h);
+  uint32_t mq[4], vq[4];  // two codes each
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b, va, vb;
+    (m[i] * mf * F32Pair(0x1p-120f)).get(a, b);
+    a = __uint_as_float((__float_as_uint(a) + ((h[2 * i] & 0xffffu) << 4)) & 0xfff00000u);
+    b = __uint_as_float((__float_as_uint(b) + ((h[2 * i + 1] & 0xffffu) << 4)) & 0xfff00000u);
+    (F32Pair(a, b) * F32Pair(0x1p120f)).get(a, b);
+    mq[i] = f2_to_e4m3x2(a, b);
+    (v[i] * vf * F32Pair(0x1p-112f)).get(a, b);
+    v[i].get(va, vb);
+    uint32_t x = (__float_as_uint(a) + ((h[2 * i] >> 16) << 5)) & 0xffe00000u;
+    uint32_t y = (__float_as_uint(b) + ((h[2 * i + 1] >> 16) << 5)) & 0xffe00000u;
+    if (va > 0.0f) x = max(x, 0x00200000u);
+    if (vb > 0.0f) y = max(y, 0x00200000u);
+    (F32Pair(__uint_as_float(x), __uint_as_float(y)) * F32Pair(0x1p112f)).get(a, b);
+    vq[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E5M2);
+  }
+  mc = make_uint2(mq[0] | (mq[1] << 16), mq[2] | (mq[3] << 16));
+  vc = make_uint2(vq[0] | (vq[1] << 16), vq[2] | (vq[3] << 16));
+  float a, b;
+  zero.get(a, b);
+  if (!(a + b == 0.0f)) {  // (random bits make any number of a NaN)
+    mc = make_uint2(0u, 0u);
+    vc = make_uint2(0u, 0u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float x[2], y[2];
+      m[i].get(x[0], x[1]);
+      v[i].get(y[0], y[1]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t sign = (__float_as_uint(x[j]) >> 24) & 0x80u;
+        uint32_t mb = (mq[i] >> (8 * j)) & 0xffu, vb = (vq[i] >> (8 * j)) & 0xffu;
+        if (!(fabsf(x[j]) < INFINITY)) mb = sign | (x[j] != x[j] ? 0x7fu : 0x7eu);
+        if (!(y[j] < INFINITY)) vb = y[j] != y[j] ? 0x7fu : 0x7bu;
+        (i < 2 ? mc.x : mc.y) |= mb << (16 * (i & 1) + 8 * j);
+        (i < 2 ? vc.x : vc.y) |= vb << (16 * (i & 1) + 8 * j);
+      }
+    }
+  }
+}
+
+// eight elements as they lie in memory
+template <typename P, typename G, bool k8>
+struct Chunk {
+  Raw8<P> p;
+  Raw8<G> g;
+  Raw8<ElemF32> m, v;
+  __device__ __forceinline__ void load(const Entry& t, int64_t at, bool vec, int n) {
+    p = raw_load8<P>(static_cast<const typename P::T*>(t.param) + at, vec, n);
+    g = raw_load8<G>(static_cast<const typename G::T*>(t.grad) + at, vec, n);
+    m = raw_load8<ElemF32>(static_cast<const float*>(t.m) + at, vec, n);
+    v = raw_load8<ElemF32>(static_cast<const float*>(t.v) + at, vec, n);
+  }
+  __device__ __forceinline__ void moments(F32Pair (&a)[4], F32Pair (&b)[4]) const {
+    float x[8];
+    raw_get8<ElemF32>(m, x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = F32Pair(x[2 * i], x[2 * i + 1]);
+    raw_get8<ElemF32>(v, x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = F32Pair(x[2 * i], x[2 * i + 1]);
+  }
+};
+template <typename P, typename G>
+struct Chunk<P, G, true> {
+  Raw8<P> p;
+  Raw8<G> g;
+  uint2 m, v;
+  uint8_t m_byte, v_byte;
+  __device__ __forceinline__ void load(const Entry& t, int64_t at, bool vec, int n) {
+    p = raw_load8<P>(static_cast<const typename P::T*>(t.param) + at, vec, n);
+    g = raw_load8<G>(static_cast<const typename G::T*>(t.grad) + at, vec, n);
+    m = load_codes(static_cast<const uint8_t*>(t.m) + at, vec, n);
+    v = load_codes(static_cast<const uint8_t*>(t.v) + at, vec, n);
+    m_byte = n > 0 ? t.m_scales[at >> 5] : (uint8_t)0;
+    v_byte = n > 0 ? t.v_scales[at >> 5] : (uint8_t)0;
+  }
+  __device__ __forceinline__ void moments(F32Pair (&a)[4], F32Pair (&b)[4]) const {
+    decode8<__NV_E4M3>(m, e8m0_to_f(m_byte), a);
+    decode8<__NV_E5M2>(v, e8m0_to_f(v_byte), b);
+  }
+};
+
+template <typename P, typename G, bool k8>
+__device__ __forceinline__ void step8(const Step& s, const Entry& t, const Chunk<P, G, k8>& c, int64_t at, bool vec, int n,
+                                      uint32_t key, int copy_dtype) {
+  float p[8], g[8];
+  F32Pair m[4], v[4];
+  raw_get8<P>(c.p, p);
+  raw_get8<G>(c.g, g);
+  c.moments(m, v);
+  update8(s, p, g, m, v);
+  elem_store8<P>(static_cast<typename P::T*>(t.param) + at, vec, n, p);
+  if (copy_dtype == FTMOE_OUT_BF16) elem_store8<ElemBf16>(static_cast<uint16_t*>(t.copy) + at, vec, n, p);
+  else if (copy_dtype == FTMOE_OUT_FP16) elem_store8<ElemF16>(static_cast<uint16_t*>(t.copy) + at, vec, n, p);
+  if constexpr (k8) {
+    uint2 mc, vc;
+    uint32_t m_byte, v_byte;
+    encode8(m, v, mix(key + (uint32_t)(at >> 3)), mc, vc, m_byte, v_byte);
+    store_codes(static_cast<uint8_t*>(t.m) + at, vec, n, mc);
+    store_codes(static_cast<uint8_t*>(t.v) + at, vec, n, vc);
+    if ((threadIdx.x & 3) == 0 && n > 0) {
+      t.m_scales[at >> 5] = (uint8_t)m_byte;
+      t.v_scales[at >> 5] = (uint8_t)v_byte;
+    }
+  } else {
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i].get(x[2 * i], x[2 * i + 1]);
+    elem_store8<ElemF32>(static_cast<float*>(t.m) + at, vec, n, x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i].get(x[2 * i], x[2 * i + 1]);
+    elem_store8<ElemF32>(static_cast<float*>(t.v) + at, vec, n, x);
+  }
 }
 
 template <typename P, typename G, bool k8, int kMax>
@@ -131,88 +291,55 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   pdl_wait();
   pdl_trigger();
   const int which = table.find(blockIdx.x);
-  const Entry& t = table.entry[which];
+  const Entry t = table.entry[which];
   const int64_t start = (int64_t)((int)blockIdx.x - table.first[which]) * kUnit;
 
-  const float grad_scale = c.grad_scale != nullptr ? *c.grad_scale : 1.0f;
-  if (!(fabsf(grad_scale) < INFINITY)) return;  // no step
+  Step s = {c.grad_scale != nullptr ? *c.grad_scale : 1.0f, c.beta1, c.beta2, c.rest1, c.rest2, c.eps};
+  if (!(fabsf(s.grad_scale) < INFINITY)) return;  // no step
   const float lr = c.lr_dev != nullptr ? *c.lr_dev : c.lr;
-  float correction1 = c.correction1, correction2 = c.correction2;
+  float correction1 = c.correction1;
+  s.correction = c.correction2;
   int64_t step = c.step;
   if (c.step_dev != nullptr) {
     step = max(*c.step_dev, (int64_t)1);
     correction1 = -1.0f / expm1f((float)step * c.ln_beta1);
-    correction2 = rsqrtf(-expm1f((float)step * c.ln_beta2));
+    s.correction = rsqrtf(-expm1f((float)step * c.ln_beta2));
   }
-  const float decay = lr * c.weight_decay, rate = lr * correction1;
+  s.decay = lr * c.weight_decay;
+  s.rate = lr * correction1;
+  s.one = c.one;
   uint32_t key = 0;
   if constexpr (k8) {
     key = mix(mix(mix(c.seed) + (uint32_t)step) + (uint32_t)t.index);
     key = mix(key + (uint32_t)((uint64_t)(start >> 3) >> 32));
   }
 
+  const int64_t first = start + (int64_t)threadIdx.x * 8;
+  if constexpr (k8) {
+    if (t.vec && start + kUnit <= t.n) {
+      // whole vectors: the next chunk is on its way while this one is worked on (with fp32 moments a chunk
+      // is up to 32 registers, and enough warps fit to do without: unrolled like this they lose 6%)
+      Chunk<P, G, true> now, next;
+      now.load(t, first, true, 8);
+#pragma unroll
+      for (int pass = 0; pass < kPasses; ++pass) {
+        const int64_t at = first + pass * (kThreads * 8);
+        if (pass + 1 < kPasses) next.load(t, at + kThreads * 8, true, 8);
+        step8<P, G, true>(s, t, now, at, true, 8, key, copy_dtype);
+        now = next;
+      }
+      return;
+    }
+  }
 #pragma unroll 1
   for (int pass = 0; pass < kPasses; ++pass) {
-    const int64_t at = start + (int64_t)(pass * kThreads + threadIdx.x) * 8;
-    const int64_t left = t.n - at;
-    // (lanes past the end stay for the exchange between the four lanes of a group)
+    const int64_t at = first + pass * (kThreads * 8), left = t.n - at;
+    // (lanes past the end stay for the exchange between the four lanes of a group; their elements are zeros)
     if (__all_sync(0xffffffffu, left <= 0)) break;
     const int n = left >= 8 ? 8 : left > 0 ? (int)left : 0;
-    const bool vec = t.vec != 0;
-    float p[8], g[8], m[8], v[8];
-    raw_get8<P>(raw_load8<P>(static_cast<const typename P::T*>(t.param) + at, vec, n), p);
-    raw_get8<G>(raw_load8<G>(static_cast<const typename G::T*>(t.grad) + at, vec, n), g);
-    if constexpr (k8) {
-      const uint2 mc = load_codes(static_cast<const uint8_t*>(t.m) + at, vec, n);
-      const uint2 vc = load_codes(static_cast<const uint8_t*>(t.v) + at, vec, n);
-      const float ms = n > 0 ? e8m0_to_f(t.m_scales[at >> 5]) : 0.0f, vs = n > 0 ? e8m0_to_f(t.v_scales[at >> 5]) : 0.0f;
-      decode8<__NV_E4M3>(mc, ms, m);
-      decode8<__NV_E5M2>(vc, vs, v);
-    } else {
-      raw_get8<ElemF32>(raw_load8<ElemF32>(static_cast<const float*>(t.m) + at, vec, n), m);
-      raw_get8<ElemF32>(raw_load8<ElemF32>(static_cast<const float*>(t.v) + at, vec, n), v);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      g[i] = __fmul_rn(g[i], grad_scale);
-      m[i] = __fadd_rn(__fmul_rn(m[i], c.beta1), __fmul_rn(g[i], c.rest1));
-      v[i] = __fadd_rn(__fmul_rn(v[i], c.beta2), __fmul_rn(__fmul_rn(g[i], g[i]), c.rest2));
-      const float d = fmaf(square_root(v[i]), correction2, c.eps);
-      p[i] -= fmaf(rate, m[i] * reciprocal(d), p[i] * decay);
-    }
-    elem_store8<P>(static_cast<typename P::T*>(t.param) + at, vec, n, p);
-    if (copy_dtype == FTMOE_OUT_BF16) elem_store8<ElemBf16>(static_cast<uint16_t*>(t.copy) + at, vec, n, p);
-    else if (copy_dtype == FTMOE_OUT_FP16) elem_store8<ElemF16>(static_cast<uint16_t*>(t.copy) + at, vec, n, p);
-    if constexpr (k8) {
-      uint32_t m_top = 0u, v_top = 0u;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        m_top = i < n ? max(m_top, __float_as_uint(m[i]) & 0x7fffffffu) : m_top;
-        v_top = i < n ? max(v_top, __float_as_uint(v[i]) & 0x7fffffffu) : v_top;
-      }
-      const uint32_t mb = scale_byte<8>(group_max(m_top)), vb = scale_byte<15>(group_max(v_top));
-      const float mf = inverse_scale(mb), vf = inverse_scale(vb);
-      uint32_t h[8], mq[8], vq[8];
-      noise8(mix(key + (uint32_t)(at >> 3)), h);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t sign = (__float_as_uint(m[i]) >> 24) & 0x80u;
-        const uint32_t mbits = __float_as_uint(__fmul_rn(__fmul_rn(fabsf(m[i]), mf), 0x1p-120f));
-        const uint32_t vbits = __float_as_uint(__fmul_rn(__fmul_rn(v[i], vf), 0x1p-112f)) & 0x7fffffffu;
-        mq[i] = min((mbits + ((h[i] & 0xffffu) << 4)) >> 20, 0x7fu) | sign;
-        vq[i] = min((vbits + ((h[i] >> 16) << 5)) >> 21, 0x7cu);
-        if (v[i] > 0.0f) vq[i] = max(vq[i], 1u);
-      }
-      store_codes(static_cast<uint8_t*>(t.m) + at, vec, n, make_uint2(pack4(mq[0], mq[1], mq[2], mq[3]), pack4(mq[4], mq[5], mq[6], mq[7])));
-      store_codes(static_cast<uint8_t*>(t.v) + at, vec, n, make_uint2(pack4(vq[0], vq[1], vq[2], vq[3]), pack4(vq[4], vq[5], vq[6], vq[7])));
-      if ((threadIdx.x & 3) == 0 && n > 0) {
-        t.m_scales[at >> 5] = (uint8_t)mb;
-        t.v_scales[at >> 5] = (uint8_t)vb;
-      }
-    } else {
-      elem_store8<ElemF32>(static_cast<float*>(t.m) + at, vec, n, m);
-      elem_store8<ElemF32>(static_cast<float*>(t.v) + at, vec, n, v);
-    }
+    Chunk<P, G, k8> now;
+    now.load(t, at, t.vec != 0, n);
+    step8<P, G, k8>(s, t, now, at, t.vec != 0, n, key, copy_dtype);
   }
 }
 

@@ -145,6 +145,7 @@ ftmoe_status ftmoe_adamw_step(const ftmoe_adamw_list* list, const ftmoe_adamw* o
     c.correction1 = (float)(1.0 / (1.0 - std::pow(opt->beta1, (double)opt->step)));
     c.correction2 = (float)(1.0 / std::sqrt(1.0 - std::pow(opt->beta2, (double)opt->step)));
   }
+  c.one = 1.0f;
   c.seed = opt->seed;
   c.step = opt->step;
   c.lr_dev = opt->lr_dev;

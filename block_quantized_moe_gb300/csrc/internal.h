@@ -371,6 +371,7 @@ struct AdamwConstants {
   float lr, beta1, beta2, rest1, rest2, eps, weight_decay;  // rest: 1 - beta
   float ln_beta1, ln_beta2;                                 // for corrections by a step on the device
   float correction1, correction2;                           // 1 / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
+  float one;                                                // 1
   uint32_t seed;
   int64_t step;
   const float* lr_dev;

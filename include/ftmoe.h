@@ -604,8 +604,8 @@ ftmoe_status ftmoe_grad_norm(const ftmoe_grad_list* list, float scale, float max
  * largest magnitude is at most the format's largest (448; 57,344). Codes are rounded
  * stochastically: up with the probability of what is cut off (to 16 bits), so that moments
  * which change by less than half a step still move, on average by what they should. A v above zero
- * is never rounded to zero (its code is at least 1). NaN and infinite moments are kept as NaN (m)
- * and infinity (v). The random bits are a hash of (seed, step, tensor's place in the list,
+ * is never rounded to zero (its code is at least 1). NaN and infinite moments stay so (an
+ * infinite one as the largest code of a group whose value of it is infinite in fp32). The random bits are a hash of (seed, step, tensor's place in the list,
  * element). */
 typedef enum ftmoe_moments { FTMOE_MOMENTS_FP32 = 0, FTMOE_MOMENTS_8BIT = 1 } ftmoe_moments;
 
