@@ -25,7 +25,7 @@ namespace adamw {
 
 using many::kPasses;
 using many::kThreads;
-using many::kUnit;
+using many::kPass;
 
 struct Entry {
   int64_t n;
@@ -287,12 +287,12 @@ __device__ __forceinline__ void step8(const Step& s, const Entry& t, const Chunk
 
 template <typename P, typename G, bool k8, int kMax>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ many::Table<Entry, kMax> table,
-                                                         const AdamwConstants c, const int copy_dtype) {
+                                                         const AdamwConstants c, const int copy_dtype, const int passes) {
   pdl_wait();
   pdl_trigger();
   const int which = table.find(blockIdx.x);
   const Entry t = table.entry[which];
-  const int64_t start = (int64_t)((int)blockIdx.x - table.first[which]) * kUnit;
+  const int64_t start = (int64_t)((int)blockIdx.x - table.first[which]) * (passes * kPass);
 
   Step s = {c.grad_scale != nullptr ? *c.grad_scale : 1.0f, c.beta1, c.beta2, c.rest1, c.rest2, c.eps};
   if (!(fabsf(s.grad_scale) < INFINITY)) return;  // no step
@@ -316,15 +316,15 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
 
   const int64_t first = start + (int64_t)threadIdx.x * 8;
   if constexpr (k8) {
-    if (t.vec && start + kUnit <= t.n) {
+    if (passes == kPasses && t.vec && start + kPasses * kPass <= t.n) {
       // whole vectors: the next chunk is on its way while this one is worked on (with fp32 moments a chunk
       // is up to 32 registers, and enough warps fit to do without: unrolled like this they lose 6%)
       Chunk<P, G, true> now, next;
       now.load(t, first, true, 8);
 #pragma unroll
       for (int pass = 0; pass < kPasses; ++pass) {
-        const int64_t at = first + pass * (kThreads * 8);
-        if (pass + 1 < kPasses) next.load(t, at + kThreads * 8, true, 8);
+        const int64_t at = first + pass * kPass;
+        if (pass + 1 < kPasses) next.load(t, at + kPass, true, 8);
         step8<P, G, true>(s, t, now, at, true, 8, key, copy_dtype);
         now = next;
       }
@@ -332,8 +332,8 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     }
   }
 #pragma unroll 1
-  for (int pass = 0; pass < kPasses; ++pass) {
-    const int64_t at = first + pass * (kThreads * 8), left = t.n - at;
+  for (int pass = 0; pass < passes; ++pass) {
+    const int64_t at = first + pass * kPass, left = t.n - at;
     // (lanes past the end stay for the exchange between the four lanes of a group; their elements are zeros)
     if (__all_sync(0xffffffffu, left <= 0)) break;
     const int n = left >= 8 ? 8 : left > 0 ? (int)left : 0;
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
 }
 
 template <typename P, typename G, bool k8, int kMax>
-cudaError_t launch_some(const ftmoe_adamw_list& list, int from, int to, const AdamwConstants& c, cudaStream_t st) {
+cudaError_t launch_some(const ftmoe_adamw_list& list, int from, int to, int passes, const AdamwConstants& c, cudaStream_t st) {
   many::Table<Entry, kMax> table = {};
   int units = 0;
   for (int i = from; i < to; ++i) {
@@ -356,33 +356,21 @@ cudaError_t launch_some(const ftmoe_adamw_list& list, int from, int to, const Ad
     const uintptr_t all8 = (uintptr_t)t.m | (uintptr_t)t.v;
     e.vec = all16 % 16 == 0 && all8 % 8 == 0;
     table.first[table.count++] = units;
-    units += (int)cdiv(t.n, kUnit);
+    units += (int)cdiv(t.n, passes * kPass);
   }
   table.first[table.count] = units;
-  if (units == 0) return cudaSuccess;
   return launch_kernel(adamw_kernel<P, G, k8, kMax>, dim3((unsigned)units), dim3(kThreads), 0, st, true, table, c,
-                       (int)list.copy_dtype);
+                       (int)list.copy_dtype, passes);
 }
 
 // A launch takes kMany tensors (kFew where that is all of them) and 2^30 units at most.
 template <typename P, typename G, bool k8>
 cudaError_t launch_all(const ftmoe_adamw_list& list, const AdamwConstants& c, cudaStream_t st) {
-  for (int from = 0; from < list.count;) {
-    int to = from, taken = 0;
-    int64_t units = 0;
-    while (to < list.count && taken < kMany) {
-      const int64_t n = list.tensors[to].n, more = cdiv(n, kUnit);
-      if (taken > 0 && units + more > ((int64_t)1 << 30)) break;
-      units += more;
-      taken += n > 0;
-      ++to;
-    }
-    const cudaError_t e = taken <= kFew ? launch_some<P, G, k8, kFew>(list, from, to, c, st)
-                                        : launch_some<P, G, k8, kMany>(list, from, to, c, st);
-    if (e != cudaSuccess) return e;
-    from = to;
-  }
-  return cudaSuccess;
+  return many::for_launches(list.count, kMany, [&](int i) { return list.tensors[i].n; },
+                            [&](int from, int to, int taken, int passes) {
+                              return taken <= kFew ? launch_some<P, G, k8, kFew>(list, from, to, passes, c, st)
+                                                   : launch_some<P, G, k8, kMany>(list, from, to, passes, c, st);
+                            });
 }
 
 }  // namespace adamw

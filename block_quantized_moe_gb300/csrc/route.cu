@@ -554,77 +554,116 @@ __global__ void __launch_bounds__(kThreads, kPer <= 8 ? kBlocksPerSm : 2) route_
   }
 }
 
+// what a lane reads of a token's routes: its slot
+struct Slot {
+  int id;
+  float w, dw;
+  __device__ __forceinline__ void load(const RouteArgs& a, int64_t token, int lane, int topk) {
+    id = -1;
+    w = dw = 0.0f;
+    if (lane < topk) {
+      const int64_t at = token * topk + lane;
+      id = a.ids[at];
+      w = a.weights[at];
+      dw = a.dweights[at];
+    }
+  }
+};
+
 template <typename Elem, typename Out, int kPer>
-__global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kThreads) route_backward_kernel(const __grid_constant__ RouteArgs a) {
+  extern __shared__ float4 rows[];
   pdl_wait();
   pdl_trigger();
-  extern __shared__ float rows[];
   const int lane = threadIdx.x & 31;
-  const int64_t token = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (token >= a.tokens) return;
-  const int E = a.router.num_experts, topk = a.router.topk;
-  float* part = rows + (threadIdx.x >> 5) * (32 * kPer);
-  const typename Elem::T* row = static_cast<const typename Elem::T*>(a.logits) + token * a.ld;
-  const bool softmax = a.router.score == FTMOE_SCORE_SOFTMAX;
-
-  int id = lane < topk ? a.ids[token * topk + lane] : -1;
-  if (id >= E) {
-    raise_error(FTMOE_ERR_EXPERT_ID_RANGE);
-    id = -1;
+  const int E = a.router.num_experts, topk = a.router.topk, e0 = lane * kPer;
+  float* const part = reinterpret_cast<float*>(rows) + (threadIdx.x >> 5) * (32 * kPer);
+  const bool softmax = a.router.score == FTMOE_SCORE_SOFTMAX, whole = softmax && !a.router.renormalize;
+  const float per_scale = 1.0f / a.router.scale;
+  const int64_t stride = (int64_t)gridDim.x * kWarps;
+  int64_t token = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  Row<Elem, kPer> next_row;
+  Slot next;
+  if (token < a.tokens) {
+    next.load(a, token, lane, topk);
+    if (whole) next_row.load(static_cast<const typename Elem::T*>(a.logits) + token * a.ld, lane, E, a.vec);
   }
-  const float w = id >= 0 ? a.weights[token * topk + lane] : 0.0f, dw = id >= 0 ? a.dweights[token * topk + lane] : 0.0f;
-  float r = w * dw;
-  const float total = warp_sum(r);
-  if (a.router.renormalize) r = r - w * (total / a.router.scale);
-  if (!softmax && id >= 0) r *= 1.0f / (1.0f + expf(taken(Elem::get(row[id]))));
-  // an id that occurs twice: the first of its lanes gets the sum
-  const uint32_t same = __match_any_sync(kFull, id);
-  if (__any_sync(kFull, id >= 0 && (same & (same - 1u)) != 0u)) {
-    float all = 0.0f;
-    for (int t = 0; t < topk; ++t) {
-      const float other = __shfl_sync(kFull, r, t);
-      all += (same >> t) & 1u ? other : 0.0f;
+  for (; token < a.tokens; token += stride) {
+    const typename Elem::T* row = static_cast<const typename Elem::T*>(a.logits) + token * a.ld;
+    Slot s = next;
+    const Row<Elem, kPer> this_row = next_row;
+    if (token + stride < a.tokens) {
+      next.load(a, token + stride, lane, topk);
+      if (whole) next_row.load(row + stride * a.ld, lane, E, a.vec);
     }
-    r = all;
-  }
-  const bool lead = id >= 0 && (same & ((1u << lane) - 1u)) == 0u;
+    if (s.id >= E) raise_error(FTMOE_ERR_EXPERT_ID_RANGE);
+    if (s.id < 0 || s.id >= E) s.id = -1, s.w = 0.0f, s.dw = 0.0f;
+    float r = s.w * s.dw;
+    const float total = warp_sum(r);
+    if (a.router.renormalize) r = fmaf(-s.w, total * per_scale, r);
+    if (!softmax && s.id >= 0) r *= 1.0f / (1.0f + expf(taken(Elem::get(row[s.id]))));
+    // an id that occurs twice: the first of its lanes gets the sum
+    const uint32_t same = __match_any_sync(kFull, s.id);
+    if (__any_sync(kFull, s.id >= 0 && (same & (same - 1u)) != 0u)) {
+      float all = 0.0f;
+      for (int t = 0; t < topk; ++t) {
+        const float other = __shfl_sync(kFull, r, t);
+        all += (same >> t) & 1u ? other : 0.0f;
+      }
+      r = all;
+    }
+    const bool lead = s.id >= 0 && (same & ((1u << lane) - 1u)) == 0u;
 
+    float d[kPer];
+    if constexpr (kPer >= 4) {
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) part[lane + 32 * j] = 0.0f;
-  __syncwarp();
-  if (lead) part[id] = r;
-  __syncwarp();
-
-  const int e0 = lane * kPer;
-  float d[kPer];
+      for (int j = 0; j < kPer; j += 4) *reinterpret_cast<float4*>(part + e0 + j) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    } else {
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) d[j] = part[e0 + j];
-  if (softmax && !a.router.renormalize && __any_sync(kFull, id >= 0)) {
-    float x[kPer], top, sum;
-    Row<Elem, kPer> raw;
-    raw.load(row, lane, E, a.vec);
-    raw.get(lane, E, x);
-    softmax_stats(x, top, sum);
-    const float f = total / sum;
-    if (top > -INFINITY) {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) d[j] -= expf(x[j] - top) * f;
+      for (int j = 0; j < kPer; ++j) part[e0 + j] = 0.0f;
     }
-  }
-  typename Out::T* out = static_cast<typename Out::T*>(a.dlogits) + token * a.ld_dlogits;
-  if constexpr (kPer >= 8) {
+    __syncwarp();
+    if (lead) part[s.id] = r;
+    __syncwarp();
+    if constexpr (kPer >= 4) {
 #pragma unroll
-    for (int c = 0; c < kPer; c += 8) {
-      float v[8];
+      for (int j = 0; j < kPer; j += 4) {
+        const float4 q = *reinterpret_cast<const float4*>(part + e0 + j);
+        d[j] = q.x, d[j + 1] = q.y, d[j + 2] = q.z, d[j + 3] = q.w;
+      }
+    } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = d[c + j];
-      const int n = E - e0 - c;
-      if (n > 0) elem_store8<Out>(out + e0 + c, a.vec_out, n, v);
+      for (int j = 0; j < kPer; ++j) d[j] = part[e0 + j];
     }
-  } else {
+    if (whole && __any_sync(kFull, s.id >= 0)) {
+      float x[kPer], top = -INFINITY, sum = 0.0f;
+      this_row.get(lane, E, x);
 #pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (e0 + j < E) out[e0 + j] = Out::put(d[j]);
+      for (int j = 0; j < kPer; ++j) top = fmaxf(top, x[j]);
+      top = warp_top(top);
+      if (top > -INFINITY) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) sum += x[j] = exp2_fast((x[j] - top) * kLog2e);
+        const float f = total / warp_sum(sum);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) d[j] = fmaf(-x[j], f, d[j]);
+      }
+    }
+    typename Out::T* out = static_cast<typename Out::T*>(a.dlogits) + token * a.ld_dlogits;
+    if constexpr (kPer >= 8) {
+#pragma unroll
+      for (int c = 0; c < kPer; c += 8) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = d[c + j];
+        const int n = E - e0 - c;
+        if (n > 0) elem_store8<Out>(out + e0 + c, a.vec_out, n, v);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (e0 + j < E) out[e0 + j] = Out::put(d[j]);
+    }
   }
 }
 
@@ -668,8 +707,8 @@ cudaError_t launch_route_backward(RouteArgs a, cudaStream_t st) {
       return with_per(a.router.num_experts, [&](auto per) {
         constexpr int kPer = decltype(per)::value;
         return launch_kernel(route_backward_kernel<decltype(elem), decltype(out), kPer>,
-                             dim3((unsigned)cdiv(a.tokens, kWarps)), dim3(kThreads), kWarps * 32 * kPer * sizeof(float), st,
-                             true, a);
+                             dim3((unsigned)std::min<int64_t>(cdiv(a.tokens, kWarps), 152 * kBlocksPerSm)), dim3(kThreads),
+                             kWarps * 32 * kPer * sizeof(float), st, true, a);
       });
     });
   });

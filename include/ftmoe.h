@@ -591,7 +591,7 @@ size_t ftmoe_grad_norm_workspace_bytes(const ftmoe_grad_list* list);
  *   result[1] = scale * min(1, max_norm / (norm + 1e-6));  NaN where the norm is not finite
  * result: device float[2]; result + 1 is a grad_scale for ftmoe_adamw_step, which takes no step for
  * a NaN. max_norm > 0 (INFINITY: no clipping), scale > 0 and finite. Squares are summed in fp32
- * over a few elements and from there in fp64; where they leave fp32's range they are taken in
+ * over eight elements and from there in pairs of fp32 numbers and in fp64; where they leave fp32's range they are taken in
  * fp64, so that gradients of any finite size have their norm. The order of the sums is fixed by the
  * sizes: the same bits every time. The workspace (8-byte aligned; contents need not be set) is
  * used until the call's work completes, by one call at a time. */
