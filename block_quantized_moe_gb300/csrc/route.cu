@@ -79,31 +79,61 @@ __device__ __forceinline__ float tolerance(float largest_score, float v) {
   return 0x1p-19f * largest_score + 0x1p-21f * fabsf(v);
 }
 
-// a lane's logits as they lie in memory
+// a lane's logits as they lie in memory (-inf past the last expert), in pieces of up to 16 bytes
 template <typename Elem, int kPer>
 struct Row {
-  Raw8<Elem> raw[kPer >= 8 ? kPer / 8 : 1];
-  __device__ __forceinline__ void load(const typename Elem::T* row, int lane, int E, bool vec) {
-    const int e0 = lane * kPer;
-    if constexpr (kPer >= 8) {
+  using T = typename Elem::T;
+  static constexpr int kBytes = kPer * (int)sizeof(T), kPiece = kBytes < 16 ? kBytes : 16;  // (the piece of one 16-bit logit: 2)
+  static constexpr int kWords = kBytes < 4 ? 1 : kBytes / 4;
+  static constexpr uint32_t kNone = sizeof(T) == 4 ? 0xff800000u : std::is_same<Elem, ElemBf16>::value ? 0xff80ff80u : 0xfc00fc00u;
+  uint32_t raw[kWords];
+  __device__ __forceinline__ Row() {
 #pragma unroll
-      for (int c = 0; c < kPer; c += 8) raw[c / 8] = raw_load8<Elem>(row + e0 + c, vec, E - e0 - c);
+    for (int i = 0; i < kWords; ++i) raw[i] = kNone;
+  }
+  // whether rows at base, ld elements apart, can be read in pieces
+  static bool vec_ok(const void* base, int64_t ld, int E) {
+    return (uintptr_t)base % kPiece == 0 && ld * (int64_t)sizeof(T) % kPiece == 0 && E * (int)sizeof(T) % kPiece == 0;
+  }
+  __device__ __forceinline__ void load(const T* row, int lane, int E, bool vec) {
+    const int e0 = lane * kPer;
+    if (vec) {
+#pragma unroll
+      for (int c = 0; c < kBytes / kPiece; ++c) {
+        const T* from = row + e0 + c * (kPiece / (int)sizeof(T));
+        if (e0 + c * (kPiece / (int)sizeof(T)) < E) {
+          if constexpr (kPiece == 16) {
+            const uint4 q = *reinterpret_cast<const uint4*>(from);
+            raw[4 * c] = q.x, raw[4 * c + 1] = q.y, raw[4 * c + 2] = q.z, raw[4 * c + 3] = q.w;
+          } else if constexpr (kPiece == 8) {
+            const uint2 q = *reinterpret_cast<const uint2*>(from);
+            raw[0] = q.x, raw[1] = q.y;
+          } else if constexpr (kPiece == 4) {
+            raw[0] = *reinterpret_cast<const uint32_t*>(from);
+          } else {
+            raw[0] = *reinterpret_cast<const uint16_t*>(from);
+          }
+        }
+      }
     } else {
-      raw[0] = raw_load8<Elem>(row + e0, false, min(E - e0, kPer));
+      const uint32_t* words = reinterpret_cast<const uint32_t*>(row);
+      if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          if (e0 + j < E) raw[j] = words[e0 + j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          if (e0 + j < E) raw[j / 2] = (raw[j / 2] & (j % 2 ? 0x0000ffffu : 0xffff0000u)) | (uint32_t)row[e0 + j] << (16 * (j % 2));
+      }
     }
   }
-  // -inf for experts that take no part, and past the last
-  __device__ __forceinline__ void get(int lane, int E, float (&x)[kPer]) const {
+  // -inf for experts that take no part
+  __device__ __forceinline__ void get(float (&x)[kPer]) const {
 #pragma unroll
-    for (int c = 0; c < kPer; c += 8) {
-      float v[8];
-      raw_get8<Elem>(raw[c / 8], v);
-#pragma unroll
-      for (int j = c; j < kPer && j < c + 8; ++j) x[j] = taken(v[j - c]);
-    }
-    if (lane * kPer + kPer > E) {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) x[j] = lane * kPer + j < E ? x[j] : -INFINITY;
+    for (int j = 0; j < kPer; ++j) {
+      if constexpr (sizeof(T) == 4) x[j] = taken(__uint_as_float(raw[j]));
+      else x[j] = taken(Elem::get((uint16_t)(raw[j / 2] >> (16 * (j % 2)))));
     }
   }
 };
@@ -135,6 +165,10 @@ __device__ __forceinline__ void scores(const float (&x)[kPer], bool softmax, flo
   }
 }
 
+__device__ __forceinline__ float score_fast(float x, bool softmax, float top, float largest) {
+  return softmax ? exp2_fast((x - top) * kLog2e) * largest : sigmoid_fast(x);
+}
+
 // the two largest of two pairs
 __device__ __forceinline__ void merge2(float& a1, float& a2, float b1, float b2) {
   a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
@@ -146,16 +180,6 @@ __device__ __forceinline__ void add2(float& a1, float& a2, float v) {
 }
 __device__ __forceinline__ float group_score(float a1, float a2, int best) {
   return best == 2 && a2 > -INFINITY ? a1 + a2 : a1;
-}
-
-// The group's score on each of its lanes, where `lanes` whole lanes (a power of two) make up a group.
-template <int kPer>
-__device__ __forceinline__ float lane_group_scores(const float (&v)[kPer], int lane, int groups, int lanes, int best) {
-  float a1 = -INFINITY, a2 = -INFINITY;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) add2(a1, a2, v[j]);
-  for (int o = 1; o < lanes; o <<= 1) merge2(a1, a2, __shfl_xor_sync(kFull, a1, o), __shfl_xor_sync(kFull, a2, o));
-  return lane < groups * lanes ? group_score(a1, a2, best) : -INFINITY;
 }
 
 // Group g's score on lane g, groups of any size.
@@ -177,19 +201,19 @@ __device__ __forceinline__ float any_group_scores(const float (&v)[kPer], int la
 }
 
 // Whether this lane's group is among the `keep` best (lanes of a group next to each other, `lanes` of
-// them); how far the worst of those is from the best of the others (infinite where there is none).
-__device__ __forceinline__ bool keep_groups(float mine, int lane, int lanes, int keep, float& gap) {
-  float last = -INFINITY;
+// them); the scores of the worst of those and of the best of the others (-inf where there is none).
+__device__ __forceinline__ bool keep_groups(float mine, int lane, int lanes, int keep, float& last, float& next) {
   bool in = false;
+  const uint32_t below = (1u << (lane & ~(lanes - 1))) - 1u;  // the lanes of lower groups
   for (int t = 0; t < keep; ++t) {
-    const float most = warp_top(mine);
-    if (!(most > -INFINITY)) break;
-    const int first = __ffs(__ballot_sync(kFull, mine == most)) - 1;
+    const float most = warp_top(mine);  // (-inf: groups of no expert that could be chosen)
     last = most;
-    if ((uint32_t)(lane - first) < (uint32_t)lanes) in = true, mine = -INFINITY;
+    const uint32_t all = __ballot_sync(kFull, mine == most);  // (by every lane, so not behind a condition)
+    const bool is = mine == most && (all & below) == 0u;
+    in = in || is;
+    mine = is ? -INFINITY : mine;
   }
-  const float next = warp_top(mine);
-  gap = next > -INFINITY && last > -INFINITY ? last - next : INFINITY;
+  next = warp_top(mine);
   return in;
 }
 
@@ -294,11 +318,150 @@ __device__ __noinline__ int route_exact(const RouteArgs& a, const typename Elem:
   return mine;
 }
 
+// the three largest of a lane's values (of a lane of fewer, -inf for the others)
+struct Best3 {
+  float a, b, c;
+};
+template <int kPer>
+__device__ __forceinline__ Best3 best3(const float (&v)[kPer]) {
+  Best3 t = {v[0], -INFINITY, -INFINITY};
+#pragma unroll
+  for (int j = 1; j < kPer; ++j) {
+    if (j > 1) t.c = fmaxf(t.c, fminf(t.b, v[j]));
+    t.b = fmaxf(t.b, fminf(t.a, v[j]));
+    t.a = fmaxf(t.a, v[j]);
+  }
+  return t;
+}
+
+// a chosen expert and its value
+struct Slot2 {
+  int32_t expert;
+  float v;
+};
+
+// Top-k from the lanes' three best values: each step takes the largest of the lanes' best, and its lane's
+// next moves up. slots[t] gets the expert of slot t (-1: none); rest: the best value left.
+// false: a lane gave three, and what it has left is not known (5% of tokens for 8 of 256 experts), or
+// there are not enough (-inf comes from the lowest lane again and again).
+// (A step is a maximum and a vote over the warp, 24 cycles each; selects rather than branches, and
+// no first-set-bit, which runs at a quarter of the vote's rate.)
+template <int kPer>
+__device__ __forceinline__ bool choose_top(const float (&v)[kPer], Best3 t, int topk, int lane, Slot2* slots, float& rest) {
+  const Best3 all = t;
+  const uint32_t below = (1u << lane) - 1u;
+  uint32_t order = 0u;  // a byte for each value that this lane gives: its slot, from 1; the last in the lowest byte
+#pragma unroll 4
+  for (int n = 1; n <= topk; ++n) {
+    const float most = warp_top(t.a);
+    const bool is = t.a == most;
+    const uint32_t alike = __ballot_sync(kFull, is);  // (by every lane, so not behind a condition)
+    const bool first = is && (alike & below) == 0u;
+    order = first ? order << 8 | (uint32_t)n : order;
+    t.a = first ? t.b : t.a;
+    t.b = first ? t.c : t.b;  // (what follows the third value is never used: see below)
+  }
+  if (__any_sync(kFull, order > 0xffffu)) return false;
+  rest = warp_top(t.a);
+  __syncwarp();  // (the last token's slots have been read)
+  if (order != 0u) {
+    // equal values were taken in the experts' order: the first equal to each
+    int at = kPer;
+#pragma unroll
+    for (int j = kPer - 1; j >= 0; --j) at = v[j] == all.a ? j : at;
+    slots[(order > 0xffu ? order >> 8 : order) - 1u] = {all.a > -INFINITY ? lane * kPer + at : -1, all.a};
+    if (order > 0xffu) {
+      const int before = at;
+#pragma unroll
+      for (int j = kPer - 1; j >= 0; --j) at = v[j] == all.b && (all.b != all.a || j > before) ? j : at;
+      slots[(order & 0xffu) - 1u] = {all.b > -INFINITY ? lane * kPer + at : -1, all.b};
+    }
+  }
+  __syncwarp();
+  return true;
+}
+
 // an expert that may be among the chosen, a lane each
 struct Candidate {
   float v, x, b;
   int32_t expert;
 };
+
+// Writes this lane's candidates, the elements j with bit j of `mask`, behind those of the lanes below; how many
+// there are in all (nothing is written where there are more than 32).
+__device__ __forceinline__ int gather_candidates(uint32_t mask, int lane, int first, int32_t* experts) {
+  const int count = __popc(mask);
+  const uint32_t below = (1u << lane) - 1u;
+  int at = 0, total = 0;
+#pragma unroll
+  for (int bit = 0; bit < 6; ++bit) {
+    const uint32_t lanes = __ballot_sync(kFull, (count >> bit) & 1);
+    at += __popc(lanes & below) << bit;
+    total += __popc(lanes) << bit;
+  }
+  __syncwarp();  // (the last ones have been read)
+  if (total <= 32) {
+    for (; mask != 0u; mask &= mask - 1u) experts[at++] = first + __ffs(mask) - 1;
+  }
+  __syncwarp();
+  return total;
+}
+
+template <int kPer>
+__device__ __forceinline__ double softmax_sum64(const float (&x)[kPer], float top) {
+  double sum = 0.0;
+#pragma unroll 1
+  for (int j = 0; j < kPer; ++j) sum += x[j] > -INFINITY ? exp((double)x[j] - (double)top) : 0.0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+  return sum;
+}
+
+// The groups to keep where scores at the border (`last` the worst kept, `next` the best of the others) are nearer than
+// `near`: the groups that near to the border are compared by their best values in 64 bits, taken of
+// every expert that may be one of them. kept: whether this lane's group is. false: they are more than 32.
+template <typename Elem, int kPer>
+__device__ __forceinline__ bool settle_groups(const float (&v)[kPer], const float (&x)[kPer], const RouteArgs& a,
+                                              const typename Elem::T* row, bool softmax, float top, float g1, float g2,
+                                              float mine, float last, float next, float near, int lane, int32_t* experts,
+                                              bool& kept) {
+  const int lanes = a.group_lanes, groups = a.router.groups, best = a.router.group_best;
+  const bool open = mine >= next - near && mine <= last + near;
+  // (the values that make up the score; without a bias they are logits, and the order is theirs)
+  const float least = best == 2 && g2 > -INFINITY ? g2 : g1;
+  const float from = a.bias != nullptr ? least - near : least;
+  uint32_t mask = 0u;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) mask |= (open && v[j] > -INFINITY && v[j] >= from ? 1u : 0u) << j;
+  const int total = gather_candidates(mask, lane, lane * kPer, experts);
+  if (total > 32) return false;
+  const double sum = softmax ? softmax_sum64(x, top) : 1.0;
+  int64_t key = kNever64;
+  int group = -1;
+  if (lane < total) {
+    const int e = experts[lane];
+    key = key_of(score64(softmax, (double)taken(Elem::get(row[e])), (double)top, sum) + (a.bias != nullptr ? (double)taken(a.bias[e]) : 0.0));
+    group = e / (lanes * kPer);
+  }
+  int64_t a1 = kNever64, a2 = kNever64;
+  for (int i = 0; i < total; ++i) {
+    const int64_t other = __shfl_sync(kFull, key, i);
+    const int of = __shfl_sync(kFull, group, i);
+    if (of == lane / lanes) {
+      a2 = max(a2, min(a1, other));
+      a1 = max(a1, other);
+    }
+  }
+  int64_t score = best == 2 && a2 > kNever64 ? key_of(value_of(a1) + value_of(a2)) : a1;
+  if (!open) score = mine > last ? INT64_MAX : kNever64;
+  int rank = 0;
+  for (int g = 0; g < groups; ++g) {
+    const int64_t other = __shfl_sync(kFull, score, g * lanes);
+    rank += other > score || (other == score && g < lane / lanes);
+  }
+  kept = rank < a.router.group_topk;
+  return true;
+}
 
 // Top-k of the values v by up to 32 candidates, in the order of 64 bits. Lane t gets the
 // candidate of slot t (expert -1: none); false: there are more candidates.
@@ -318,24 +481,12 @@ __device__ __forceinline__ bool choose_few(const float (&v)[kPer], const float (
   }
   if (biased) from -= tolerance(largest_score, from);
   from = fmaxf(from, -FLT_MAX);
-  // places of this lane's candidates: after those of the lanes below
-  int count = 0;
+  uint32_t mask = 0u;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) count += v[j] >= from;
-  const uint32_t below = (1u << lane) - 1u;
-  int at = 0, total = 0;
-#pragma unroll
-  for (int bit = 0; (1 << bit) <= kPer; ++bit) {
-    const uint32_t lanes = __ballot_sync(kFull, (count >> bit) & 1);
-    at += __popc(lanes & below) << bit;
-    total += __popc(lanes) << bit;
-  }
-  if (total > 32) return false;
+  for (int j = 0; j < kPer; ++j) mask |= (v[j] >= from ? 1u : 0u) << j;
   int32_t* experts = reinterpret_cast<int32_t*>(shared + 32);
-#pragma unroll
-  for (int j = 0; j < kPer; ++j)
-    if (v[j] >= from) experts[at++] = lane * kPer + j;
-  __syncwarp();
+  const int total = gather_candidates(mask, lane, lane * kPer, experts);
+  if (total > 32) return false;
   mine = {-INFINITY, -INFINITY, 0.0f, -1};
   if (lane < total) {
     mine.expert = experts[lane];
@@ -343,7 +494,7 @@ __device__ __forceinline__ bool choose_few(const float (&v)[kPer], const float (
     mine.v = mine.x;
     if (biased) {
       mine.b = taken(__ldg(a.bias + mine.expert));
-      mine.v = (softmax ? exp2_fast((mine.x - top) * kLog2e) * largest_score : sigmoid_fast(mine.x)) + mine.b;
+      mine.v = score_fast(mine.x, softmax, top, largest_score) + mine.b;
     }
   }
   // a candidate's place: how many are larger, and where values are equal how many of those are lower experts
@@ -359,19 +510,13 @@ __device__ __forceinline__ bool choose_few(const float (&v)[kPer], const float (
   if (lane < total) mine = shared[lane];
   if (biased) {
     const float next = __shfl_down_sync(kFull, mine.v, 1);
-    bool near = lane < topk && lane + 1 < total && mine.v - next <= tolerance(largest_score, mine.v);
+    // (pairs beyond the last slot too: one that is not the same may follow several that are)
+    bool near = lane + 1 < total && mine.v - next <= tolerance(largest_score, mine.v);
     if (__any_sync(kFull, near)) {
       const float next_x = __shfl_down_sync(kFull, mine.x, 1), next_b = __shfl_down_sync(kFull, mine.b, 1);
       near = near && (next_x != mine.x || next_b != mine.b);
       if (__any_sync(kFull, near)) {
-        double sum = 1.0;
-        if (softmax) {
-          sum = 0.0;
-#pragma unroll 1
-          for (int j = 0; j < kPer; ++j) sum += x[j] > -INFINITY ? exp((double)x[j] - (double)top) : 0.0;
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-        }
+        const double sum = softmax ? softmax_sum64(x, top) : 1.0;
         const int64_t key = key_of(score64(softmax, (double)mine.x, (double)top, sum) + (double)mine.b);
         place = 0;
         for (int i = 0; i < total; ++i) {
@@ -429,9 +574,10 @@ __device__ __forceinline__ int choose_many(float (&v)[kPer], bool biased, float 
 
 // A block takes consecutive tokens; its warps take them one by one, so that a token that has to be
 // taken in 64 bits holds up none of the others.
-template <typename Elem, int kPer, bool kFew>
+template <typename Elem, int kPer, bool kFew, bool kBiased>
 __global__ void __launch_bounds__(kThreads, kPer <= 8 ? kBlocksPerSm : 2) route_kernel(const __grid_constant__ RouteArgs a) {
   __shared__ Candidate candidates[kWarps][32 + 8];  // (the last 8: 32 experts)
+  __shared__ Slot2 slots[kWarps][32];
   __shared__ int taken_tokens;
   if (threadIdx.x == 0) taken_tokens = kWarps;
   __syncthreads();
@@ -440,8 +586,10 @@ __global__ void __launch_bounds__(kThreads, kPer <= 8 ? kBlocksPerSm : 2) route_
   using T = typename Elem::T;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int E = a.router.num_experts, topk = a.router.topk;
-  const bool softmax = a.router.score == FTMOE_SCORE_SOFTMAX, biased = a.bias != nullptr;
-  const bool scored_groups = a.router.groups > 1 && (biased || a.router.group_best == 2);
+  const bool softmax = a.router.score == FTMOE_SCORE_SOFTMAX, biased = kFew ? kBiased : a.bias != nullptr;
+  const bool grouped = a.router.groups > 1, lane_groups = a.group_lanes > 0;
+  const bool scored_groups = grouped && (biased || a.router.group_best == 2);
+  const bool all_scores = softmax && (biased || scored_groups || !a.router.renormalize);
   int64_t active_tokens = a.tokens;
   if (a.tokens_dev != nullptr) {
     const int64_t n = *a.tokens_dev;
@@ -451,6 +599,8 @@ __global__ void __launch_bounds__(kThreads, kPer <= 8 ? kBlocksPerSm : 2) route_
   const int tokens = (int)(a.tokens * (blockIdx.x + 1) / gridDim.x - first);
   const int active = (int)(active_tokens <= first ? 0 : active_tokens - first < tokens ? active_tokens - first : tokens);
   const T* const rows = static_cast<const T*>(a.logits) + first * a.ld;
+  int32_t* const ids_out = a.ids_out + first * topk + lane;
+  float* const weights_out = a.weights_out + first * topk + lane;
   float bias[kPer];
 #pragma unroll
   for (int j = 0; j < kPer; ++j) bias[j] = biased && lane * kPer + j < E ? taken(a.bias[lane * kPer + j]) : 0.0f;
@@ -467,15 +617,14 @@ __global__ void __launch_bounds__(kThreads, kPer <= 8 ? kBlocksPerSm : 2) route_
     if (token < active) {
       const T* const row = rows + token * a.ld;
       float x[kPer];
-      next.get(lane, E, x);
+      next.get(x);
       if (after < active) next.load(rows + after * a.ld, lane, E, a.vec);
 
       float top = 0.0f, sum = 1.0f;
-      if (softmax && (biased || scored_groups || !a.router.renormalize)) softmax_stats(x, top, sum);
-      const float largest_score = softmax ? 1.0f / sum : 1.0f;
-      float v[kPer];       // the order of the experts (-inf: never chosen)
-      bool exact = false;  // the token has to be taken in 64 bits
-      if (biased || scored_groups) {
+      if (all_scores) softmax_stats(x, top, sum);
+      const float largest_score = softmax ? reciprocal(sum) : 1.0f;
+      float v[kPer];  // the order of the experts (-inf: never chosen)
+      if (biased) {
         scores(x, softmax, top, largest_score, v);
 #pragma unroll
         for (int j = 0; j < kPer; ++j) v[j] = x[j] > -INFINITY ? v[j] + bias[j] : -INFINITY;
@@ -483,45 +632,74 @@ __global__ void __launch_bounds__(kThreads, kPer <= 8 ? kBlocksPerSm : 2) route_
 #pragma unroll
         for (int j = 0; j < kPer; ++j) v[j] = x[j];
       }
-      if (a.router.groups > 1) {
-        float gap, mine;
-        uint32_t kept;  // bit j: expert j of the lane may be chosen
-        if (a.group_lanes > 0) {
-          mine = lane_group_scores(v, lane, a.router.groups, a.group_lanes, a.router.group_best);
-          kept = keep_groups(mine, lane, a.group_lanes, a.router.group_topk, gap) ? 0xffffffffu : 0u;
-        } else {
-          const int size = E / a.router.groups;
-          mine = any_group_scores(v, lane, a.router.groups, size, a.router.group_best);
-          const uint32_t groups = __ballot_sync(kFull, keep_groups(mine, lane, 1, a.router.group_topk, gap));
-          kept = 0u;
-          int group = lane * kPer / size, rest = lane * kPer - group * size;
+      bool exact = false;    // the token has to be taken in 64 bits
+      bool kept = true;      // this lane's experts may be chosen
+      Best3 best;
+      if (!grouped) {
+        if constexpr (kFew) best = best3(v);
+      } else if (lane_groups) {
+        best = best3(v);
+        float g1 = best.a, g2 = best.b, last, next_best;
+        for (int o = 1; o < a.group_lanes; o <<= 1) merge2(g1, g2, __shfl_xor_sync(kFull, g1, o), __shfl_xor_sync(kFull, g2, o));
+        const bool inside = lane < a.router.groups * a.group_lanes;
+        float mine = group_score(g1, g2, a.router.group_best);
+        if (!biased && scored_groups && g2 > -INFINITY)  // (scores grow with the logits)
+          mine = score_fast(g1, softmax, top, largest_score) + score_fast(g2, softmax, top, largest_score);
+        else if (!biased && scored_groups && g1 > -INFINITY)
+          mine = score_fast(g1, softmax, top, largest_score);
+        if (!inside) mine = -INFINITY;
+        kept = keep_groups(mine, lane, a.group_lanes, a.router.group_topk, last, next_best);
+        const float near = 2.0f * tolerance(largest_score, last);
+        if (scored_groups && next_best > -INFINITY && last - next_best <= near)
+          exact = !settle_groups<Elem, kPer>(v, x, a, row, softmax, top, g1, g2, mine, last, next_best, near, lane,
+                                             reinterpret_cast<int32_t*>(candidates[warp] + 32), kept);
+        if (!kept) best = {-INFINITY, -INFINITY, -INFINITY};
+      } else {
+        const int size = E / a.router.groups;
+        float s[kPer], last, next_best;
+        if (!biased && scored_groups) scores(x, softmax, top, largest_score, s);
 #pragma unroll
-          for (int j = 0; j < kPer; ++j) {
-            kept |= (group < 32 ? (groups >> group) & 1u : 0u) << j;
-            if (++rest == size) rest = 0, ++group;
-          }
+        for (int j = 0; j < kPer; ++j) s[j] = !biased && scored_groups && x[j] > -INFINITY ? s[j] : v[j];
+        const float mine = any_group_scores(s, lane, a.router.groups, size, a.router.group_best);
+        const uint32_t groups = __ballot_sync(kFull, keep_groups(mine, lane, 1, a.router.group_topk, last, next_best));
+        exact = scored_groups && next_best > -INFINITY && last - next_best <= 2.0f * tolerance(largest_score, last);
+        int group = lane * kPer / size, rest = lane * kPer - group * size;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          v[j] = group < 32 && (groups >> group) & 1u ? v[j] : -INFINITY;
+          if (++rest == size) rest = 0, ++group;
         }
-        if (scored_groups) {
-          const float most = warp_top(mine > -INFINITY ? fabsf(mine) : 0.0f);
-          exact = gap <= 2.0f * tolerance(largest_score, most);
-          if (!biased) {
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) v[j] = x[j];
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) v[j] = (kept >> j) & 1u ? v[j] : -INFINITY;
+        best = best3(v);
       }
       float cx = -INFINITY;  // the chosen's logit
       if constexpr (kFew) {
-        Candidate c;
         if (!exact) {
-          exact = !choose_few<Elem, kPer>(v, x, a, row, biased, softmax, top, largest_score, topk, lane, candidates[warp], c);
-          chosen = c.expert;
-          cx = c.x;
+          float rest;
+          bool fine = choose_top(v, best, topk, lane, slots[warp], rest);
+          if (fine) {
+            const Slot2 s = lane < topk ? slots[warp][lane] : Slot2{-1, -INFINITY};
+            chosen = s.expert;
+            cx = s.v;
+            if (biased) {
+              // (a neighbour as near as that, the best of the rest after the last)
+              const float below = __shfl_down_sync(kFull, s.v, 1);
+              if (chosen >= 0) cx = taken(Elem::get(row[chosen]));
+              fine = !__any_sync(kFull, chosen >= 0 && s.v - (lane + 1 < topk ? below : rest) <= tolerance(largest_score, s.v));
+            }
+          }
+          if (!fine) {
+            Candidate c;
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) v[j] = kept ? v[j] : -INFINITY;
+            exact = !choose_few<Elem, kPer>(v, x, a, row, biased, softmax, top, largest_score, topk, lane, candidates[warp], c);
+            chosen = c.expert;
+            cx = c.x;
+          }
         }
       } else {
         bool near;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) v[j] = kept ? v[j] : -INFINITY;
         chosen = choose_many(v, biased, largest_score, topk, lane, near);
         exact = exact || near;
         if (chosen >= 0) cx = taken(Elem::get(row[chosen]));
@@ -540,15 +718,14 @@ __global__ void __launch_bounds__(kThreads, kPer <= 8 ? kBlocksPerSm : 2) route_
         if (chosen >= 0) u = softmax ? exp2_fast((cx - most) * kLog2e) : reciprocal(exp2_fast(t * kLog2e) + exp2_fast((t - cx) * kLog2e));
         weight = u;
         for (int o = 1; o < topk; o <<= 1) u += __shfl_xor_sync(kFull, u, o);
-        weight = chosen >= 0 ? weight * (a.router.scale / u) : 0.0f;
+        weight = chosen >= 0 ? weight * (a.router.scale * reciprocal(u)) : 0.0f;
       } else if (chosen >= 0) {
         weight = a.router.scale * (softmax ? exp2_fast((cx - top) * kLog2e) * largest_score : sigmoid(cx));
       }
     }
     if (lane < topk) {
-      const int64_t at = (first + token) * topk + lane;
-      a.ids_out[at] = chosen;
-      a.weights_out[at] = weight;
+      ids_out[token * topk] = chosen;
+      weights_out[token * topk] = weight;
     }
     token = after;
   }
@@ -637,7 +814,7 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const __grid_c
     }
     if (whole && __any_sync(kFull, s.id >= 0)) {
       float x[kPer], top = -INFINITY, sum = 0.0f;
-      this_row.get(lane, E, x);
+      this_row.get(x);
 #pragma unroll
       for (int j = 0; j < kPer; ++j) top = fmaxf(top, x[j]);
       top = warp_top(top);
@@ -683,7 +860,6 @@ inline cudaError_t with_per(int32_t E, F f) {
 cudaError_t launch_route(RouteArgs a, cudaStream_t st) {
   using namespace route;
   OverlapLaunch overlap;
-  a.vec = elem_vec_ok(a.logits, a.ld, a.dtype == FTMOE_OUT_FP32 ? 4 : 2);
   return with_elem(a.dtype, [&](auto elem) {
     return with_per(a.router.num_experts, [&](auto per) {
       constexpr int kPer = decltype(per)::value;
@@ -691,8 +867,11 @@ cudaError_t launch_route(RouteArgs a, cudaStream_t st) {
       a.group_lanes = size % kPer == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
       // one token a block where there are few, else as many blocks as fit at once, of equal shares
       const unsigned blocks = (unsigned)std::min<int64_t>(a.tokens, 152 * kBlocksPerSm);
-      return launch_kernel(a.router.topk <= kFewTopk ? route_kernel<decltype(elem), kPer, true> : route_kernel<decltype(elem), kPer, false>,
-                           dim3(blocks), dim3(kThreads), 0, st, true, a);
+      using E = decltype(elem);
+      a.vec = Row<E, kPer>::vec_ok(a.logits, a.ld, a.router.num_experts);
+      auto* kernel = a.router.topk > kFewTopk ? route_kernel<E, kPer, false, false>
+                     : a.bias != nullptr ? route_kernel<E, kPer, true, true> : route_kernel<E, kPer, true, false>;
+      return launch_kernel(kernel, dim3(blocks), dim3(kThreads), 0, st, true, a);
     });
   });
 }
@@ -700,12 +879,12 @@ cudaError_t launch_route(RouteArgs a, cudaStream_t st) {
 cudaError_t launch_route_backward(RouteArgs a, cudaStream_t st) {
   using namespace route;
   OverlapLaunch overlap;
-  a.vec = elem_vec_ok(a.logits, a.ld, a.dtype == FTMOE_OUT_FP32 ? 4 : 2);
   a.vec_out = elem_vec_ok(a.dlogits, a.ld_dlogits, a.dlogits_dtype == FTMOE_OUT_FP32 ? 4 : 2);
   return with_elem(a.dtype, [&](auto elem) {
     return with_elem(a.dlogits_dtype, [&](auto out) {
       return with_per(a.router.num_experts, [&](auto per) {
         constexpr int kPer = decltype(per)::value;
+        a.vec = Row<decltype(elem), kPer>::vec_ok(a.logits, a.ld, a.router.num_experts);
         return launch_kernel(route_backward_kernel<decltype(elem), decltype(out), kPer>,
                              dim3((unsigned)std::min<int64_t>(cdiv(a.tokens, kWarps), 152 * kBlocksPerSm)), dim3(kThreads),
                              kWarps * 32 * kPer * sizeof(float), st, true, a);

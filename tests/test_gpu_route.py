@@ -171,6 +171,51 @@ def test_masked_experts(score, biased):
     assert torch.allclose(w[2], torch.full((6,), 1 / 6, device=DEV))
 
 
+@pytest.mark.parametrize("E", [8, 32, 64, 256])
+@pytest.mark.parametrize("biased", [False, True])
+def test_fewer_experts_than_slots(E, biased):
+    """Rows of 0 to 8 experts that can be chosen, next to each other and apart."""
+    x = logits(34, E, "fp32", E)
+    for t in range(17):
+        x[t, t % 9:] = -math.inf
+        mask = torch.ones(E, dtype=torch.bool, device=DEV)
+        mask[torch.arange(t % 9, device=DEV) * (E // 8) % E] = False
+        x[17 + t].masked_fill_(mask, -math.inf)
+    bias = torch.linspace(-0.1, 0.1, E, device=DEV) if biased else None
+    for score in ("softmax", "sigmoid"):
+        check(x, router(E, 8, score), bias)
+        check(x, router(E, 4, score, groups=4, group_topk=2, group_best=2), bias)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True])
+def test_the_best_next_to_each_other(score, biased):
+    """The chosen in one lane's experts, or few lanes'."""
+    x = logits(64, 256, "fp32", 12, std=0.5)
+    for t in range(64):
+        x[t, 3 * t:3 * t + 2 + t % 11] += 6.0
+    bias = torch.linspace(-0.1, 0.1, 256, device=DEV) if biased else None
+    check(x, router(256, 8, score), bias)
+    check(x, router(256, 12, score, groups=8, group_topk=3, group_best=2), bias)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("E,groups,best", [(256, 8, 2), (256, 8, 1), (64, 8, 2), (96, 4, 2), (512, 16, 2)])
+def test_groups_nearer_than_fp32(E, groups, best, biased, score):
+    """Groups of the same logits but for one unit in the last place here and there: their scores differ by
+    less than fp32 holds, or not at all."""
+    size = E // groups
+    x = logits(48, size, "fp32", E + groups, std=0.3).repeat(1, groups)
+    pick = torch.randint(0, E, (48, 3), generator=torch.Generator(device=DEV).manual_seed(E), device=DEV)
+    up = torch.nextafter(x, torch.full_like(x, 9.0))
+    x.scatter_(1, pick, up.gather(1, pick))
+    top = x.view(48, groups, size).argmax(2) + torch.arange(groups, device=DEV) * size  # the best of some groups too
+    x[24:].scatter_(1, top[24:, ::3], up[24:].gather(1, top[24:, ::3]))
+    bias = torch.linspace(-0.1, 0.1, size, device=DEV).repeat(groups) if biased else None
+    check(x, router(E, 6, score, groups=groups, group_topk=groups // 2, group_best=best), bias)
+
+
 def test_masking_biases():
     x = logits(8, 32, "fp32", 4)
     bias = torch.zeros(32, device=DEV)
