@@ -340,7 +340,7 @@ cudaError_t launch_stream_matmul16(const Matmul16Args& a, cudaStream_t s);
 cudaError_t launch_tc_matmul16(const Matmul16Args& a, cudaStream_t s, int* unsupported);
 uint32_t read_err_tc_matmul16();
 
-// route.cu: routing of tokens to experts, and its gradient
+// route*.cu: routing of tokens to experts (a translation unit for each type of logits), and its gradient
 struct RouteArgs {
   const void* logits;
   int32_t dtype;           // ftmoe_out_dtype
@@ -362,7 +362,9 @@ struct RouteArgs {
   int group_lanes;         // lanes of a warp that hold a group, 0: not whole lanes or no power of two
 };
 constexpr int32_t kRouteMaxExperts = 1024, kRouteMaxTopk = 32, kRouteMaxGroups = 32;
-cudaError_t launch_route(RouteArgs a, cudaStream_t s);
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t s);
+cudaError_t launch_route_bf16(const RouteArgs& a, cudaStream_t s);
+cudaError_t launch_route_fp16(const RouteArgs& a, cudaStream_t s);
 cudaError_t launch_route_backward(RouteArgs a, cudaStream_t s);
 uint32_t read_err_route();
 

@@ -1,898 +1,12 @@
-// Routing of tokens to experts from the router's logits, and its gradient.
-//
-// Forward, per token, with x its logits: s = softmax(x) or 1 / (1 + exp(-x)), value = s + bias;
-// groups of consecutive experts are ranked by the sum of their 1 or 2 best values and all but the
-// best groups left out; the top-k values are chosen, largest first, ties to the lower expert; the
-// weights are the chosen s times the scale, renormalised to sum to it where asked.
-//
-// A warp per token, the next token's logits on their way meanwhile; lane l holds the experts
-// [l * kPer, (l + 1) * kPer). Keys are order-preserving integers of fp32 values. Top-k: the k-th largest of
-// the 32 lanes' maxima is a threshold that at least k keys reach, and, for a small k, few more do (8 of 256: 9 or
-// 10 on average); they go to a lane each, in the experts' order, and a count of the larger ones is a key's
-// place. That is 6 instructions a step of the threshold and 4 a candidate, against about 70 for each of k
-// steps that take the largest key out of its lane's registers; the latter is kept for k > kFewTopk,
-// where the candidates would pass 32 too often.
-// Without a bias the logits themselves are the order and nothing is rounded. With one, the order of
-// s + bias is that of 64 bits: fp32 values are off by less than half of tolerance(), so the
-// threshold is lowered by that much, and where two neighbours in the order are nearer than that
-// (and not the same logit and bias, a tie in any precision) the candidates' values are taken again in 64 bits.
-// More candidates than lanes, and group scores nearer than that, take the whole token again (route_exact).
-//
-// Backward: a closed form in the saved weights (see ftmoe_route_tokens_backward), so that only plain
-// softmax reads every logit. A warp per token puts the chosen experts' terms in a row of shared
-// memory and writes the row of dlogits whole.
-#include <algorithm>
-#include <cfloat>
-
-#include "common.cuh"
-#include "elem16.cuh"
-#include "internal.h"
+// Routing of fp32 logits, and the choice by the logits' type (each in a translation unit of its own).
+#include "route_forward.cuh"
 
 namespace ftmoe {
 
-namespace route {
-
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kBlocksPerSm = 4;
-constexpr uint32_t kFull = 0xffffffffu;
-constexpr int kFewTopk = 12;  // 16 of 256 would have 21 candidates on average, 20 of 256 30
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-  return v;
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t st) {
+  if (a.dtype == FTMOE_OUT_BF16) return launch_route_bf16(a, st);
+  if (a.dtype == FTMOE_OUT_FP16) return launch_route_fp16(a, st);
+  return route::launch_as<ElemF32>(a, st);
 }
-__device__ __forceinline__ float warp_top(float v) {
-  float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-  return r;
-}
-
-// NaN and -inf take no part (-inf); +inf counts as the largest finite number
-__device__ __forceinline__ float taken(float x) { return fminf(fmaxf(x, -INFINITY), FLT_MAX); }
-
-__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
-
-// Scores for the order alone, by the hardware's exponential and reciprocal. exp(-x) is off by the
-// argument's rounding (|x| log2(e) 2^-24 ln 2 of it) and 2 units of the exponential: s by s (1 - s) of
-// that, at most 0.23 * 2^-24 + 2^-24, and by 2^-23 s of the sum's rounding and the reciprocal: under 2^-21.5.
-constexpr float kLog2e = 1.44269504f;
-__device__ __forceinline__ float exp2_fast(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float reciprocal(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float sigmoid_fast(float x) { return reciprocal(1.0f + exp2_fast(x * -kLog2e)); }
-
-// How far apart two fp32 values have to be for their order to be that of 64 bits: s is within
-// 2^-21 of the largest score (sigmoid_fast as above, the largest score taken as 1; softmax: exponentials of arguments
-// rounded by |x - top| 2^-23, which times exp(x - top) is below 2^-24 of the largest, and 2 units of
-// the exponential, a sum of 32 terms a lane at most and 5 levels, its reciprocal: 2^-21 of s), the sum with
-// the bias within 2^-24 of itself; twice that for two values, and as much again to spare.
-__device__ __forceinline__ float tolerance(float largest_score, float v) {
-  return 0x1p-19f * largest_score + 0x1p-21f * fabsf(v);
-}
-
-// a lane's logits as they lie in memory (-inf past the last expert), in pieces of up to 16 bytes
-template <typename Elem, int kPer>
-struct Row {
-  using T = typename Elem::T;
-  static constexpr int kBytes = kPer * (int)sizeof(T), kPiece = kBytes < 16 ? kBytes : 16;  // (the piece of one 16-bit logit: 2)
-  static constexpr int kWords = kBytes < 4 ? 1 : kBytes / 4;
-  static constexpr uint32_t kNone = sizeof(T) == 4 ? 0xff800000u : std::is_same<Elem, ElemBf16>::value ? 0xff80ff80u : 0xfc00fc00u;
-  uint32_t raw[kWords];
-  __device__ __forceinline__ Row() {
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) raw[i] = kNone;
-  }
-  // whether rows at base, ld elements apart, can be read in pieces
-  static bool vec_ok(const void* base, int64_t ld, int E) {
-    return (uintptr_t)base % kPiece == 0 && ld * (int64_t)sizeof(T) % kPiece == 0 && E * (int)sizeof(T) % kPiece == 0;
-  }
-  __device__ __forceinline__ void load(const T* row, int lane, int E, bool vec) {
-    const int e0 = lane * kPer;
-    if (vec) {
-#pragma unroll
-      for (int c = 0; c < kBytes / kPiece; ++c) {
-        const T* from = row + e0 + c * (kPiece / (int)sizeof(T));
-        if (e0 + c * (kPiece / (int)sizeof(T)) < E) {
-          if constexpr (kPiece == 16) {
-            const uint4 q = *reinterpret_cast<const uint4*>(from);
-            raw[4 * c] = q.x, raw[4 * c + 1] = q.y, raw[4 * c + 2] = q.z, raw[4 * c + 3] = q.w;
-          } else if constexpr (kPiece == 8) {
-            const uint2 q = *reinterpret_cast<const uint2*>(from);
-            raw[0] = q.x, raw[1] = q.y;
-          } else if constexpr (kPiece == 4) {
-            raw[0] = *reinterpret_cast<const uint32_t*>(from);
-          } else {
-            raw[0] = *reinterpret_cast<const uint16_t*>(from);
-          }
-        }
-      }
-    } else {
-      const uint32_t* words = reinterpret_cast<const uint32_t*>(row);
-      if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int j = 0; j < kPer; ++j)
-          if (e0 + j < E) raw[j] = words[e0 + j];
-      } else {
-#pragma unroll
-        for (int j = 0; j < kPer; ++j)
-          if (e0 + j < E) raw[j / 2] = (raw[j / 2] & (j % 2 ? 0x0000ffffu : 0xffff0000u)) | (uint32_t)row[e0 + j] << (16 * (j % 2));
-      }
-    }
-  }
-  // -inf for experts that take no part
-  __device__ __forceinline__ void get(float (&x)[kPer]) const {
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      if constexpr (sizeof(T) == 4) x[j] = taken(__uint_as_float(raw[j]));
-      else x[j] = taken(Elem::get((uint16_t)(raw[j / 2] >> (16 * (j % 2)))));
-    }
-  }
-};
-
-// largest logit of the row and the sum of exp(x - max) (softmax scores)
-template <int kPer>
-__device__ __forceinline__ void softmax_stats(const float (&x)[kPer], float& top, float& sum) {
-  float m = x[0];
-#pragma unroll
-  for (int j = 1; j < kPer; ++j) m = fmaxf(m, x[j]);
-  top = warp_top(m);
-  float s = 0.0f;
-  if (top > -INFINITY) {
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) s += exp2_fast((x[j] - top) * kLog2e);
-  }
-  sum = warp_sum(s);
-}
-
-// scores for the order (0 where an expert takes no part)
-template <int kPer>
-__device__ __forceinline__ void scores(const float (&x)[kPer], bool softmax, float top, float largest, float (&s)[kPer]) {
-  if (softmax) {
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) s[j] = exp2_fast((x[j] - top) * kLog2e) * largest;
-  } else {
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) s[j] = sigmoid_fast(x[j]);
-  }
-}
-
-__device__ __forceinline__ float score_fast(float x, bool softmax, float top, float largest) {
-  return softmax ? exp2_fast((x - top) * kLog2e) * largest : sigmoid_fast(x);
-}
-
-// the two largest of two pairs
-__device__ __forceinline__ void merge2(float& a1, float& a2, float b1, float b2) {
-  a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
-  a1 = fmaxf(a1, b1);
-}
-__device__ __forceinline__ void add2(float& a1, float& a2, float v) {
-  a2 = fmaxf(a2, fminf(a1, v));
-  a1 = fmaxf(a1, v);
-}
-__device__ __forceinline__ float group_score(float a1, float a2, int best) {
-  return best == 2 && a2 > -INFINITY ? a1 + a2 : a1;
-}
-
-// Group g's score on lane g, groups of any size.
-template <int kPer>
-__device__ __forceinline__ float any_group_scores(const float (&v)[kPer], int lane, int groups, int size, int best) {
-  float mine = -INFINITY;
-  for (int g = 0; g < groups; ++g) {
-    float a1 = -INFINITY, a2 = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int at = lane * kPer + j - g * size;
-      add2(a1, a2, at >= 0 && at < size ? v[j] : -INFINITY);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) merge2(a1, a2, __shfl_xor_sync(kFull, a1, o), __shfl_xor_sync(kFull, a2, o));
-    if (lane == g) mine = group_score(a1, a2, best);
-  }
-  return mine;
-}
-
-// Whether this lane's group is among the `keep` best (lanes of a group next to each other, `lanes` of
-// them); the scores of the worst of those and of the best of the others (-inf where there is none).
-__device__ __forceinline__ bool keep_groups(float mine, int lane, int lanes, int keep, float& last, float& next) {
-  bool in = false;
-  const uint32_t below = (1u << (lane & ~(lanes - 1))) - 1u;  // the lanes of lower groups
-  for (int t = 0; t < keep; ++t) {
-    const float most = warp_top(mine);  // (-inf: groups of no expert that could be chosen)
-    last = most;
-    const uint32_t all = __ballot_sync(kFull, mine == most);  // (by every lane, so not behind a condition)
-    const bool is = mine == most && (all & below) == 0u;
-    in = in || is;
-    mine = is ? -INFINITY : mine;
-  }
-  next = warp_top(mine);
-  return in;
-}
-
-// fp64 -> integer of the same order (-0 and +0 are one): compared without the few fp64 units
-__device__ __forceinline__ int64_t key_of(double v) {
-  const int64_t b = __double_as_longlong(v + 0.0);
-  return b ^ (int64_t)((uint64_t)(b >> 63) >> 1);
-}
-__device__ __forceinline__ double value_of(int64_t key) {
-  return __longlong_as_double(key ^ (int64_t)((uint64_t)(key >> 63) >> 1));
-}
-constexpr int64_t kNever64 = (int64_t)0x800fffffffffffffull;  // key of -inf
-
-__device__ __forceinline__ double score64(bool softmax, double x, double top, double sum) {
-  const double e = exp(softmax ? x - top : -x);
-  return softmax ? e / sum : 1.0 / (1.0 + e);
-}
-
-// The choice of one token with all its values in 64 bits. Lane t gets the expert of slot t, -1 for
-// none. (Any router, any number of equal values; a few microseconds.)
-template <typename Elem, int kPer>
-__device__ __noinline__ int route_exact(const RouteArgs& a, const typename Elem::T* row, int lane) {
-  constexpr int kUnroll = kPer < 4 ? kPer : 4;
-  const int E = a.router.num_experts, size = E / a.router.groups;
-  const bool softmax = a.router.score == FTMOE_SCORE_SOFTMAX;
-  const bool scored = a.bias != nullptr || (a.router.groups > 1 && a.router.group_best == 2);
-  int64_t key[kPer];
-  double sum = 1.0;
-  float top = -INFINITY;
-  if (softmax && scored) {
-    for (int j = 0; j < kPer; ++j) top = fmaxf(top, lane * kPer + j < E ? taken(Elem::get(row[lane * kPer + j])) : -INFINITY);
-    top = warp_top(top);
-    sum = 0.0;
-#pragma unroll(kUnroll)
-    for (int j = 0; j < kPer; ++j) {
-      const float x = lane * kPer + j < E ? taken(Elem::get(row[lane * kPer + j])) : -INFINITY;
-      sum += x > -INFINITY ? exp((double)x - (double)top) : 0.0;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-  }
-#pragma unroll(kUnroll)
-  for (int j = 0; j < kPer; ++j) {
-    const int e = lane * kPer + j;
-    const float x = e < E ? taken(Elem::get(row[e])) : -INFINITY;
-    double v = (double)x;
-    if (scored) v = score64(softmax, v, (double)top, sum) + (a.bias != nullptr && e < E ? (double)taken(a.bias[e]) : 0.0);
-    key[j] = x > -INFINITY && v > -INFINITY ? key_of(v) : kNever64;
-  }
-  if (a.router.groups > 1) {
-    int64_t mine = kNever64;
-    for (int g = 0; g < a.router.groups; ++g) {
-      int64_t a1 = kNever64, a2 = kNever64;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int at = lane * kPer + j - g * size;
-        if (at >= 0 && at < size) {
-          a2 = max(a2, min(a1, key[j]));
-          a1 = max(a1, key[j]);
-        }
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const int64_t b1 = __shfl_xor_sync(kFull, a1, o), b2 = __shfl_xor_sync(kFull, a2, o);
-        a2 = max(min(a1, b1), max(a2, b2));
-        a1 = max(a1, b1);
-      }
-      if (lane == g) mine = a.router.group_best == 2 && a2 > kNever64 ? key_of(value_of(a1) + value_of(a2)) : a1;
-    }
-    int rank = 0;
-    for (int g = 0; g < a.router.groups; ++g) {
-      const int64_t other = __shfl_sync(kFull, mine, g);
-      rank += other > mine || (other == mine && g < lane);
-    }
-    const uint32_t kept = __ballot_sync(kFull, lane < a.router.groups && rank < a.router.group_topk);
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int e = lane * kPer + j;
-      if (e < E && !((kept >> (e / size)) & 1u)) key[j] = kNever64;
-      else if (a.bias == nullptr && key[j] > kNever64) key[j] = key_of((double)taken(Elem::get(row[e])));  // the order is the logits'
-    }
-  }
-  int mine = -1;
-  for (int t = 0; t < a.router.topk; ++t) {
-    int64_t best = kNever64;
-    int at = E;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (key[j] > best) best = key[j], at = lane * kPer + j;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const int64_t other = __shfl_xor_sync(kFull, best, o);
-      const int other_at = __shfl_xor_sync(kFull, at, o);
-      if (other > best || (other == best && other_at < at)) best = other, at = other_at;
-    }
-    if (best <= kNever64) break;
-    if (lane == t) mine = at;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (lane * kPer + j == at) key[j] = kNever64;
-  }
-  return mine;
-}
-
-// the three largest of a lane's values (of a lane of fewer, -inf for the others)
-struct Best3 {
-  float a, b, c;
-};
-template <int kPer>
-__device__ __forceinline__ Best3 best3(const float (&v)[kPer]) {
-  Best3 t = {v[0], -INFINITY, -INFINITY};
-#pragma unroll
-  for (int j = 1; j < kPer; ++j) {
-    if (j > 1) t.c = fmaxf(t.c, fminf(t.b, v[j]));
-    t.b = fmaxf(t.b, fminf(t.a, v[j]));
-    t.a = fmaxf(t.a, v[j]);
-  }
-  return t;
-}
-
-// a chosen expert and its value
-struct Slot2 {
-  int32_t expert;
-  float v;
-};
-
-// Top-k from the lanes' three best values: each step takes the largest of the lanes' best, and its lane's
-// next moves up. slots[t] gets the expert of slot t (-1: none); rest: the best value left.
-// false: a lane gave three, and what it has left is not known (5% of tokens for 8 of 256 experts), or
-// there are not enough (-inf comes from the lowest lane again and again).
-// (A step is a maximum and a vote over the warp, 24 cycles each; selects rather than branches, and
-// no first-set-bit, which runs at a quarter of the vote's rate.)
-template <int kPer>
-__device__ __forceinline__ bool choose_top(const float (&v)[kPer], Best3 t, int topk, int lane, Slot2* slots, float& rest) {
-  const Best3 all = t;
-  const uint32_t below = (1u << lane) - 1u;
-  uint32_t order = 0u;  // a byte for each value that this lane gives: its slot, from 1; the last in the lowest byte
-#pragma unroll 4
-  for (int n = 1; n <= topk; ++n) {
-    const float most = warp_top(t.a);
-    const bool is = t.a == most;
-    const uint32_t alike = __ballot_sync(kFull, is);  // (by every lane, so not behind a condition)
-    const bool first = is && (alike & below) == 0u;
-    order = first ? order << 8 | (uint32_t)n : order;
-    t.a = first ? t.b : t.a;
-    t.b = first ? t.c : t.b;  // (what follows the third value is never used: see below)
-  }
-  if (__any_sync(kFull, order > 0xffffu)) return false;
-  rest = warp_top(t.a);
-  __syncwarp();  // (the last token's slots have been read)
-  if (order != 0u) {
-    // equal values were taken in the experts' order: the first equal to each
-    int at = kPer;
-#pragma unroll
-    for (int j = kPer - 1; j >= 0; --j) at = v[j] == all.a ? j : at;
-    slots[(order > 0xffu ? order >> 8 : order) - 1u] = {all.a > -INFINITY ? lane * kPer + at : -1, all.a};
-    if (order > 0xffu) {
-      const int before = at;
-#pragma unroll
-      for (int j = kPer - 1; j >= 0; --j) at = v[j] == all.b && (all.b != all.a || j > before) ? j : at;
-      slots[(order & 0xffu) - 1u] = {all.b > -INFINITY ? lane * kPer + at : -1, all.b};
-    }
-  }
-  __syncwarp();
-  return true;
-}
-
-// an expert that may be among the chosen, a lane each
-struct Candidate {
-  float v, x, b;
-  int32_t expert;
-};
-
-// Writes this lane's candidates, the elements j with bit j of `mask`, behind those of the lanes below; how many
-// there are in all (nothing is written where there are more than 32).
-__device__ __forceinline__ int gather_candidates(uint32_t mask, int lane, int first, int32_t* experts) {
-  const int count = __popc(mask);
-  const uint32_t below = (1u << lane) - 1u;
-  int at = 0, total = 0;
-#pragma unroll
-  for (int bit = 0; bit < 6; ++bit) {
-    const uint32_t lanes = __ballot_sync(kFull, (count >> bit) & 1);
-    at += __popc(lanes & below) << bit;
-    total += __popc(lanes) << bit;
-  }
-  __syncwarp();  // (the last ones have been read)
-  if (total <= 32) {
-    for (; mask != 0u; mask &= mask - 1u) experts[at++] = first + __ffs(mask) - 1;
-  }
-  __syncwarp();
-  return total;
-}
-
-template <int kPer>
-__device__ __forceinline__ double softmax_sum64(const float (&x)[kPer], float top) {
-  double sum = 0.0;
-#pragma unroll 1
-  for (int j = 0; j < kPer; ++j) sum += x[j] > -INFINITY ? exp((double)x[j] - (double)top) : 0.0;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-  return sum;
-}
-
-// The groups to keep where scores at the border (`last` the worst kept, `next` the best of the others) are nearer than
-// `near`: the groups that near to the border are compared by their best values in 64 bits, taken of
-// every expert that may be one of them. kept: whether this lane's group is. false: they are more than 32.
-template <typename Elem, int kPer>
-__device__ __forceinline__ bool settle_groups(const float (&v)[kPer], const float (&x)[kPer], const RouteArgs& a,
-                                              const typename Elem::T* row, bool softmax, float top, float g1, float g2,
-                                              float mine, float last, float next, float near, int lane, int32_t* experts,
-                                              bool& kept) {
-  const int lanes = a.group_lanes, groups = a.router.groups, best = a.router.group_best;
-  const bool open = mine >= next - near && mine <= last + near;
-  // (the values that make up the score; without a bias they are logits, and the order is theirs)
-  const float least = best == 2 && g2 > -INFINITY ? g2 : g1;
-  const float from = a.bias != nullptr ? least - near : least;
-  uint32_t mask = 0u;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) mask |= (open && v[j] > -INFINITY && v[j] >= from ? 1u : 0u) << j;
-  const int total = gather_candidates(mask, lane, lane * kPer, experts);
-  if (total > 32) return false;
-  const double sum = softmax ? softmax_sum64(x, top) : 1.0;
-  int64_t key = kNever64;
-  int group = -1;
-  if (lane < total) {
-    const int e = experts[lane];
-    key = key_of(score64(softmax, (double)taken(Elem::get(row[e])), (double)top, sum) + (a.bias != nullptr ? (double)taken(a.bias[e]) : 0.0));
-    group = e / (lanes * kPer);
-  }
-  int64_t a1 = kNever64, a2 = kNever64;
-  for (int i = 0; i < total; ++i) {
-    const int64_t other = __shfl_sync(kFull, key, i);
-    const int of = __shfl_sync(kFull, group, i);
-    if (of == lane / lanes) {
-      a2 = max(a2, min(a1, other));
-      a1 = max(a1, other);
-    }
-  }
-  int64_t score = best == 2 && a2 > kNever64 ? key_of(value_of(a1) + value_of(a2)) : a1;
-  if (!open) score = mine > last ? INT64_MAX : kNever64;
-  int rank = 0;
-  for (int g = 0; g < groups; ++g) {
-    const int64_t other = __shfl_sync(kFull, score, g * lanes);
-    rank += other > score || (other == score && g < lane / lanes);
-  }
-  kept = rank < a.router.group_topk;
-  return true;
-}
-
-// Top-k of the values v by up to 32 candidates, in the order of 64 bits. Lane t gets the
-// candidate of slot t (expert -1: none); false: there are more candidates.
-template <typename Elem, int kPer>
-__device__ __forceinline__ bool choose_few(const float (&v)[kPer], const float (&x)[kPer], const RouteArgs& a,
-                                           const typename Elem::T* row, bool biased, bool softmax, float top,
-                                           float largest_score, int topk, int lane, Candidate* shared, Candidate& mine) {
-  // the threshold (equal maxima go together: it is then lower than it need be)
-  float best = v[0];
-#pragma unroll
-  for (int j = 1; j < kPer; ++j) best = fmaxf(best, v[j]);
-  float from = -INFINITY;
-#pragma unroll 2
-  for (int t = 0; t < topk; ++t) {
-    from = warp_top(best);
-    best = best == from ? -INFINITY : best;
-  }
-  if (biased) from -= tolerance(largest_score, from);
-  from = fmaxf(from, -FLT_MAX);
-  uint32_t mask = 0u;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) mask |= (v[j] >= from ? 1u : 0u) << j;
-  int32_t* experts = reinterpret_cast<int32_t*>(shared + 32);
-  const int total = gather_candidates(mask, lane, lane * kPer, experts);
-  if (total > 32) return false;
-  mine = {-INFINITY, -INFINITY, 0.0f, -1};
-  if (lane < total) {
-    mine.expert = experts[lane];
-    mine.x = taken(Elem::get(row[mine.expert]));
-    mine.v = mine.x;
-    if (biased) {
-      mine.b = taken(__ldg(a.bias + mine.expert));
-      mine.v = score_fast(mine.x, softmax, top, largest_score) + mine.b;
-    }
-  }
-  // a candidate's place: how many are larger, and where values are equal how many of those are lower experts
-  int place = 0;
-#pragma unroll 4
-  for (int i = 0; i < total; ++i) place += __shfl_sync(kFull, mine.v, i) > mine.v;
-  const uint32_t places = __reduce_or_sync(kFull, lane < total ? 1u << place : 0u);
-  if (places != (uint32_t)((1ull << total) - 1ull)) {
-    for (int i = 0; i < total; ++i) place += __shfl_sync(kFull, mine.v, i) == mine.v && i < lane;
-  }
-  if (lane < total) shared[place] = mine;
-  __syncwarp();
-  if (lane < total) mine = shared[lane];
-  if (biased) {
-    const float next = __shfl_down_sync(kFull, mine.v, 1);
-    // (pairs beyond the last slot too: one that is not the same may follow several that are)
-    bool near = lane + 1 < total && mine.v - next <= tolerance(largest_score, mine.v);
-    if (__any_sync(kFull, near)) {
-      const float next_x = __shfl_down_sync(kFull, mine.x, 1), next_b = __shfl_down_sync(kFull, mine.b, 1);
-      near = near && (next_x != mine.x || next_b != mine.b);
-      if (__any_sync(kFull, near)) {
-        const double sum = softmax ? softmax_sum64(x, top) : 1.0;
-        const int64_t key = key_of(score64(softmax, (double)mine.x, (double)top, sum) + (double)mine.b);
-        place = 0;
-        for (int i = 0; i < total; ++i) {
-          const int64_t other = __shfl_sync(kFull, key, i);
-          const int expert = __shfl_sync(kFull, mine.expert, i);
-          place += other > key || (other == key && expert < mine.expert);
-        }
-        __syncwarp();
-        if (lane < total) shared[place] = mine;
-        __syncwarp();
-        if (lane < total) mine = shared[lane];
-      }
-    }
-  }
-  if (lane >= topk) mine.expert = -1;
-  return true;
-}
-
-// Top-k a step at a time; `near` where two neighbours in the order have to be taken in 64 bits.
-template <int kPer>
-__device__ __forceinline__ int choose_many(float (&v)[kPer], bool biased, float largest_score, int topk, int lane, bool& near) {
-  int chosen = -1;
-  float slot = -INFINITY, best = v[0];
-#pragma unroll
-  for (int j = 1; j < kPer; ++j) best = fmaxf(best, v[j]);
-  for (int t = 0; t < topk; ++t) {
-    const float most = warp_top(best);
-    if (!(most > -INFINITY)) break;
-    const int owner = __ffs(__ballot_sync(kFull, best == most)) - 1;
-    int at = 0;
-    if (lane == owner) {
-#pragma unroll
-      for (int j = kPer - 1; j >= 0; --j) at = v[j] == most ? j : at;
-      best = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        v[j] = j == at ? -INFINITY : v[j];
-        best = fmaxf(best, v[j]);
-      }
-    }
-    at = __shfl_sync(kFull, at, owner);
-    if (lane == t) chosen = owner * kPer + at, slot = most;
-  }
-  near = false;
-  if (biased) {
-    // pairs of neighbours in the order, and the last chosen against the best of the rest (whatever it is)
-    const int next = __shfl_down_sync(kFull, chosen, 1);
-    const float next_value = __shfl_down_sync(kFull, slot, 1), last = __shfl_sync(kFull, slot, topk - 1);
-    bool close = lane + 1 < topk && next >= 0 && slot - next_value <= tolerance(largest_score, slot);
-    if (last > -INFINITY) close = close || (best > -INFINITY && last - best <= tolerance(largest_score, last));
-    near = __any_sync(kFull, close);
-  }
-  return chosen;
-}
-
-// A block takes consecutive tokens; its warps take them one by one, so that a token that has to be
-// taken in 64 bits holds up none of the others.
-template <typename Elem, int kPer, bool kFew, bool kBiased>
-__global__ void __launch_bounds__(kThreads, kPer <= 8 ? kBlocksPerSm : 2) route_kernel(const __grid_constant__ RouteArgs a) {
-  __shared__ Candidate candidates[kWarps][32 + 8];  // (the last 8: 32 experts)
-  __shared__ Slot2 slots[kWarps][32];
-  __shared__ int taken_tokens;
-  if (threadIdx.x == 0) taken_tokens = kWarps;
-  __syncthreads();
-  pdl_wait();
-  pdl_trigger();
-  using T = typename Elem::T;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int E = a.router.num_experts, topk = a.router.topk;
-  const bool softmax = a.router.score == FTMOE_SCORE_SOFTMAX, biased = kFew ? kBiased : a.bias != nullptr;
-  const bool grouped = a.router.groups > 1, lane_groups = a.group_lanes > 0;
-  const bool scored_groups = grouped && (biased || a.router.group_best == 2);
-  const bool all_scores = softmax && (biased || scored_groups || !a.router.renormalize);
-  int64_t active_tokens = a.tokens;
-  if (a.tokens_dev != nullptr) {
-    const int64_t n = *a.tokens_dev;
-    active_tokens = n < 0 ? 0 : n < active_tokens ? n : active_tokens;
-  }
-  const int64_t first = a.tokens * blockIdx.x / gridDim.x;
-  const int tokens = (int)(a.tokens * (blockIdx.x + 1) / gridDim.x - first);
-  const int active = (int)(active_tokens <= first ? 0 : active_tokens - first < tokens ? active_tokens - first : tokens);
-  const T* const rows = static_cast<const T*>(a.logits) + first * a.ld;
-  int32_t* const ids_out = a.ids_out + first * topk + lane;
-  float* const weights_out = a.weights_out + first * topk + lane;
-  float bias[kPer];
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) bias[j] = biased && lane * kPer + j < E ? taken(a.bias[lane * kPer + j]) : 0.0f;
-
-  int token = warp;
-  Row<Elem, kPer> next;
-  if (token < active) next.load(rows + token * a.ld, lane, E, a.vec);
-  while (token < tokens) {
-    int after = 0;
-    if (lane == 0) after = atomicAdd(&taken_tokens, 1);
-    after = __shfl_sync(kFull, after, 0);
-    int chosen = -1;    // lane t: expert of slot t
-    float weight = 0.0f;
-    if (token < active) {
-      const T* const row = rows + token * a.ld;
-      float x[kPer];
-      next.get(x);
-      if (after < active) next.load(rows + after * a.ld, lane, E, a.vec);
-
-      float top = 0.0f, sum = 1.0f;
-      if (all_scores) softmax_stats(x, top, sum);
-      const float largest_score = softmax ? reciprocal(sum) : 1.0f;
-      float v[kPer];  // the order of the experts (-inf: never chosen)
-      if (biased) {
-        scores(x, softmax, top, largest_score, v);
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) v[j] = x[j] > -INFINITY ? v[j] + bias[j] : -INFINITY;
-      } else {
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) v[j] = x[j];
-      }
-      bool exact = false;    // the token has to be taken in 64 bits
-      bool kept = true;      // this lane's experts may be chosen
-      Best3 best;
-      if (!grouped) {
-        if constexpr (kFew) best = best3(v);
-      } else if (lane_groups) {
-        best = best3(v);
-        float g1 = best.a, g2 = best.b, last, next_best;
-        for (int o = 1; o < a.group_lanes; o <<= 1) merge2(g1, g2, __shfl_xor_sync(kFull, g1, o), __shfl_xor_sync(kFull, g2, o));
-        const bool inside = lane < a.router.groups * a.group_lanes;
-        float mine = group_score(g1, g2, a.router.group_best);
-        if (!biased && scored_groups && g2 > -INFINITY)  // (scores grow with the logits)
-          mine = score_fast(g1, softmax, top, largest_score) + score_fast(g2, softmax, top, largest_score);
-        else if (!biased && scored_groups && g1 > -INFINITY)
-          mine = score_fast(g1, softmax, top, largest_score);
-        if (!inside) mine = -INFINITY;
-        kept = keep_groups(mine, lane, a.group_lanes, a.router.group_topk, last, next_best);
-        const float near = 2.0f * tolerance(largest_score, last);
-        if (scored_groups && next_best > -INFINITY && last - next_best <= near)
-          exact = !settle_groups<Elem, kPer>(v, x, a, row, softmax, top, g1, g2, mine, last, next_best, near, lane,
-                                             reinterpret_cast<int32_t*>(candidates[warp] + 32), kept);
-        if (!kept) best = {-INFINITY, -INFINITY, -INFINITY};
-      } else {
-        const int size = E / a.router.groups;
-        float s[kPer], last, next_best;
-        if (!biased && scored_groups) scores(x, softmax, top, largest_score, s);
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) s[j] = !biased && scored_groups && x[j] > -INFINITY ? s[j] : v[j];
-        const float mine = any_group_scores(s, lane, a.router.groups, size, a.router.group_best);
-        const uint32_t groups = __ballot_sync(kFull, keep_groups(mine, lane, 1, a.router.group_topk, last, next_best));
-        exact = scored_groups && next_best > -INFINITY && last - next_best <= 2.0f * tolerance(largest_score, last);
-        int group = lane * kPer / size, rest = lane * kPer - group * size;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          v[j] = group < 32 && (groups >> group) & 1u ? v[j] : -INFINITY;
-          if (++rest == size) rest = 0, ++group;
-        }
-        best = best3(v);
-      }
-      float cx = -INFINITY;  // the chosen's logit
-      if constexpr (kFew) {
-        if (!exact) {
-          float rest;
-          bool fine = choose_top(v, best, topk, lane, slots[warp], rest);
-          if (fine) {
-            const Slot2 s = lane < topk ? slots[warp][lane] : Slot2{-1, -INFINITY};
-            chosen = s.expert;
-            cx = s.v;
-            if (biased) {
-              // (a neighbour as near as that, the best of the rest after the last)
-              const float below = __shfl_down_sync(kFull, s.v, 1);
-              if (chosen >= 0) cx = taken(Elem::get(row[chosen]));
-              fine = !__any_sync(kFull, chosen >= 0 && s.v - (lane + 1 < topk ? below : rest) <= tolerance(largest_score, s.v));
-            }
-          }
-          if (!fine) {
-            Candidate c;
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) v[j] = kept ? v[j] : -INFINITY;
-            exact = !choose_few<Elem, kPer>(v, x, a, row, biased, softmax, top, largest_score, topk, lane, candidates[warp], c);
-            chosen = c.expert;
-            cx = c.x;
-          }
-        }
-      } else {
-        bool near;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) v[j] = kept ? v[j] : -INFINITY;
-        chosen = choose_many(v, biased, largest_score, topk, lane, near);
-        exact = exact || near;
-        if (chosen >= 0) cx = taken(Elem::get(row[chosen]));
-      }
-      if (exact) {
-        chosen = route_exact<Elem, kPer>(a, row, lane);
-        cx = chosen >= 0 ? taken(Elem::get(row[chosen])) : -INFINITY;
-      }
-      if (chosen < 0) cx = -INFINITY;
-
-      if (a.router.renormalize) {
-        // shares of the chosen scores, scaled so that the largest does not underflow:
-        // softmax exp(x - most), sigmoid exp(-t) s with t = min(most, 0)
-        const float most = warp_top(cx), t = fminf(most, 0.0f);
-        float u = 0.0f;
-        if (chosen >= 0) u = softmax ? exp2_fast((cx - most) * kLog2e) : reciprocal(exp2_fast(t * kLog2e) + exp2_fast((t - cx) * kLog2e));
-        weight = u;
-        for (int o = 1; o < topk; o <<= 1) u += __shfl_xor_sync(kFull, u, o);
-        weight = chosen >= 0 ? weight * (a.router.scale * reciprocal(u)) : 0.0f;
-      } else if (chosen >= 0) {
-        weight = a.router.scale * (softmax ? exp2_fast((cx - top) * kLog2e) * largest_score : sigmoid(cx));
-      }
-    }
-    if (lane < topk) {
-      ids_out[token * topk] = chosen;
-      weights_out[token * topk] = weight;
-    }
-    token = after;
-  }
-}
-
-// what a lane reads of a token's routes: its slot
-struct Slot {
-  int id;
-  float w, dw;
-  __device__ __forceinline__ void load(const RouteArgs& a, int64_t token, int lane, int topk) {
-    id = -1;
-    w = dw = 0.0f;
-    if (lane < topk) {
-      const int64_t at = token * topk + lane;
-      id = a.ids[at];
-      w = a.weights[at];
-      dw = a.dweights[at];
-    }
-  }
-};
-
-template <typename Elem, typename Out, int kPer>
-__global__ void __launch_bounds__(kThreads) route_backward_kernel(const __grid_constant__ RouteArgs a) {
-  extern __shared__ float4 rows[];
-  pdl_wait();
-  pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const int E = a.router.num_experts, topk = a.router.topk, e0 = lane * kPer;
-  float* const part = reinterpret_cast<float*>(rows) + (threadIdx.x >> 5) * (32 * kPer);
-  const bool softmax = a.router.score == FTMOE_SCORE_SOFTMAX, whole = softmax && !a.router.renormalize;
-  const float per_scale = 1.0f / a.router.scale;
-  const int64_t stride = (int64_t)gridDim.x * kWarps;
-  int64_t token = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  Row<Elem, kPer> next_row;
-  Slot next;
-  if (token < a.tokens) {
-    next.load(a, token, lane, topk);
-    if (whole) next_row.load(static_cast<const typename Elem::T*>(a.logits) + token * a.ld, lane, E, a.vec);
-  }
-  for (; token < a.tokens; token += stride) {
-    const typename Elem::T* row = static_cast<const typename Elem::T*>(a.logits) + token * a.ld;
-    Slot s = next;
-    const Row<Elem, kPer> this_row = next_row;
-    if (token + stride < a.tokens) {
-      next.load(a, token + stride, lane, topk);
-      if (whole) next_row.load(row + stride * a.ld, lane, E, a.vec);
-    }
-    if (s.id >= E) raise_error(FTMOE_ERR_EXPERT_ID_RANGE);
-    if (s.id < 0 || s.id >= E) s.id = -1, s.w = 0.0f, s.dw = 0.0f;
-    float r = s.w * s.dw;
-    const float total = warp_sum(r);
-    if (a.router.renormalize) r = fmaf(-s.w, total * per_scale, r);
-    if (!softmax && s.id >= 0) r *= 1.0f / (1.0f + expf(taken(Elem::get(row[s.id]))));
-    // an id that occurs twice: the first of its lanes gets the sum
-    const uint32_t same = __match_any_sync(kFull, s.id);
-    if (__any_sync(kFull, s.id >= 0 && (same & (same - 1u)) != 0u)) {
-      float all = 0.0f;
-      for (int t = 0; t < topk; ++t) {
-        const float other = __shfl_sync(kFull, r, t);
-        all += (same >> t) & 1u ? other : 0.0f;
-      }
-      r = all;
-    }
-    const bool lead = s.id >= 0 && (same & ((1u << lane) - 1u)) == 0u;
-
-    float d[kPer];
-    if constexpr (kPer >= 4) {
-#pragma unroll
-      for (int j = 0; j < kPer; j += 4) *reinterpret_cast<float4*>(part + e0 + j) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    } else {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) part[e0 + j] = 0.0f;
-    }
-    __syncwarp();
-    if (lead) part[s.id] = r;
-    __syncwarp();
-    if constexpr (kPer >= 4) {
-#pragma unroll
-      for (int j = 0; j < kPer; j += 4) {
-        const float4 q = *reinterpret_cast<const float4*>(part + e0 + j);
-        d[j] = q.x, d[j + 1] = q.y, d[j + 2] = q.z, d[j + 3] = q.w;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) d[j] = part[e0 + j];
-    }
-    if (whole && __any_sync(kFull, s.id >= 0)) {
-      float x[kPer], top = -INFINITY, sum = 0.0f;
-      this_row.get(x);
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) top = fmaxf(top, x[j]);
-      top = warp_top(top);
-      if (top > -INFINITY) {
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) sum += x[j] = exp2_fast((x[j] - top) * kLog2e);
-        const float f = total / warp_sum(sum);
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) d[j] = fmaf(-x[j], f, d[j]);
-      }
-    }
-    typename Out::T* out = static_cast<typename Out::T*>(a.dlogits) + token * a.ld_dlogits;
-    if constexpr (kPer >= 8) {
-#pragma unroll
-      for (int c = 0; c < kPer; c += 8) {
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = d[c + j];
-        const int n = E - e0 - c;
-        if (n > 0) elem_store8<Out>(out + e0 + c, a.vec_out, n, v);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        if (e0 + j < E) out[e0 + j] = Out::put(d[j]);
-    }
-  }
-}
-
-// experts per lane: the smallest power of two that covers them
-template <typename F>
-inline cudaError_t with_per(int32_t E, F f) {
-  if (E <= 32) return f(std::integral_constant<int, 1>{});
-  if (E <= 64) return f(std::integral_constant<int, 2>{});
-  if (E <= 128) return f(std::integral_constant<int, 4>{});
-  if (E <= 256) return f(std::integral_constant<int, 8>{});
-  if (E <= 512) return f(std::integral_constant<int, 16>{});
-  return f(std::integral_constant<int, 32>{});
-}
-
-}  // namespace route
-
-cudaError_t launch_route(RouteArgs a, cudaStream_t st) {
-  using namespace route;
-  OverlapLaunch overlap;
-  return with_elem(a.dtype, [&](auto elem) {
-    return with_per(a.router.num_experts, [&](auto per) {
-      constexpr int kPer = decltype(per)::value;
-      const int size = a.router.num_experts / a.router.groups, lanes = size / kPer;
-      a.group_lanes = size % kPer == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
-      // one token a block where there are few, else as many blocks as fit at once, of equal shares
-      const unsigned blocks = (unsigned)std::min<int64_t>(a.tokens, 152 * kBlocksPerSm);
-      using E = decltype(elem);
-      a.vec = Row<E, kPer>::vec_ok(a.logits, a.ld, a.router.num_experts);
-      auto* kernel = a.router.topk > kFewTopk ? route_kernel<E, kPer, false, false>
-                     : a.bias != nullptr ? route_kernel<E, kPer, true, true> : route_kernel<E, kPer, true, false>;
-      return launch_kernel(kernel, dim3(blocks), dim3(kThreads), 0, st, true, a);
-    });
-  });
-}
-
-cudaError_t launch_route_backward(RouteArgs a, cudaStream_t st) {
-  using namespace route;
-  OverlapLaunch overlap;
-  a.vec_out = elem_vec_ok(a.dlogits, a.ld_dlogits, a.dlogits_dtype == FTMOE_OUT_FP32 ? 4 : 2);
-  return with_elem(a.dtype, [&](auto elem) {
-    return with_elem(a.dlogits_dtype, [&](auto out) {
-      return with_per(a.router.num_experts, [&](auto per) {
-        constexpr int kPer = decltype(per)::value;
-        a.vec = Row<decltype(elem), kPer>::vec_ok(a.logits, a.ld, a.router.num_experts);
-        return launch_kernel(route_backward_kernel<decltype(elem), decltype(out), kPer>,
-                             dim3((unsigned)std::min<int64_t>(cdiv(a.tokens, kWarps), 152 * kBlocksPerSm)), dim3(kThreads),
-                             kWarps * 32 * kPer * sizeof(float), st, true, a);
-      });
-    });
-  });
-}
-
-FTMOE_DEFINE_ERR_READER(read_err_route)
 
 }  // namespace ftmoe

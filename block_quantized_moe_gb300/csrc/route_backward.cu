@@ -1,0 +1,150 @@
+// Gradient of the routing weights: a closed form in the saved weights (see
+// ftmoe_route_tokens_backward), so that only plain softmax reads every logit. A warp per token
+// puts the chosen experts' terms in a row of shared memory (zero otherwise, and again after
+// it) and writes the row of dlogits whole. An expert that is chosen twice gets both terms.
+// Measured on GB300: 32,768 tokens of 256 experts, plain softmax, bf16: 12.5 us (36 MB, 5.3 us of memory): about 240
+// instructions a token, and 3 us of launch and ramp.
+#include "route.cuh"
+
+namespace ftmoe {
+
+namespace route {
+
+// what a lane reads of a token's routes: its slot
+struct Slot {
+  int id;
+  float w, dw;
+  __device__ __forceinline__ void load(const RouteArgs& a, int64_t token, int lane, int topk) {
+    id = -1;
+    w = dw = 0.0f;
+    if (lane < topk) {
+      const int64_t at = token * topk + lane;
+      id = a.ids[at];
+      w = a.weights[at];
+      dw = a.dweights[at];
+    }
+  }
+};
+
+template <typename Elem, typename Out, int kPer>
+__global__ void __launch_bounds__(kThreads) route_backward_kernel(const __grid_constant__ RouteArgs a) {
+  extern __shared__ float4 rows[];
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const int E = a.router.num_experts, topk = a.router.topk, e0 = lane * kPer;
+  float* const part = reinterpret_cast<float*>(rows) + (threadIdx.x >> 5) * (32 * kPer);
+  const bool softmax = a.router.score == FTMOE_SCORE_SOFTMAX, whole = softmax && !a.router.renormalize;
+  const float per_scale = 1.0f / a.router.scale;
+  const int64_t stride = (int64_t)gridDim.x * kWarps;
+  int64_t token = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  Row<Elem, kPer> next_row;
+  Slot next;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) part[lane + 32 * j] = 0.0f;  // and again after each token
+  __syncwarp();
+  if (token < a.tokens) {
+    next.load(a, token, lane, topk);
+    if (whole) next_row.load(static_cast<const typename Elem::T*>(a.logits) + token * a.ld, lane, E, a.vec);
+  }
+  for (; token < a.tokens; token += stride) {
+    const typename Elem::T* row = static_cast<const typename Elem::T*>(a.logits) + token * a.ld;
+    Slot s = next;
+    const Row<Elem, kPer> this_row = next_row;
+    if (token + stride < a.tokens) {
+      next.load(a, token + stride, lane, topk);
+      if (whole) next_row.load(row + stride * a.ld, lane, E, a.vec);
+    }
+    if (s.id >= E) raise_error(FTMOE_ERR_EXPERT_ID_RANGE);
+    if (s.id < 0 || s.id >= E) s.id = -1, s.w = 0.0f, s.dw = 0.0f;
+    float r = s.w * s.dw;
+    const float total = warp_sum(r);
+    if (a.router.renormalize) r = fmaf(-s.w, total * per_scale, r);
+    if (!softmax && s.id >= 0) r *= 1.0f / (1.0f + expf(taken(Elem::get(row[s.id]))));
+    // the terms in the row. An id that occurs twice (a lane reads another's number in its place): the
+    // first of its lanes puts the sum there
+    const bool active = s.id >= 0;
+    if (active) part[s.id] = __int_as_float(lane);
+    __syncwarp();
+    const bool second = active && __float_as_int(part[s.id]) != lane;
+    const uint32_t seconds = __ballot_sync(kFull, second);
+    if (seconds != 0u) {
+      const uint32_t same = __match_any_sync(kFull, s.id);
+      float all = 0.0f;
+      for (int t = 0; t < topk; ++t) {
+        const float other = __shfl_sync(kFull, r, t);
+        all += (same >> t) & 1u ? other : 0.0f;
+      }
+      r = all;  // (the same sum on each of them)
+    }
+    __syncwarp();
+    if (active) part[s.id] = r;
+    __syncwarp();
+
+    float d[kPer];
+    if constexpr (kPer >= 4) {
+#pragma unroll
+      for (int j = 0; j < kPer; j += 4) {
+        const float4 q = *reinterpret_cast<const float4*>(part + e0 + j);
+        d[j] = q.x, d[j + 1] = q.y, d[j + 2] = q.z, d[j + 3] = q.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) d[j] = part[e0 + j];
+    }
+    __syncwarp();
+    if (active) part[s.id] = 0.0f;
+    if (whole && __any_sync(kFull, active)) {
+      float x[kPer], top = -INFINITY, sum = 0.0f;
+      this_row.get_taken(x);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) top = fmaxf(top, x[j]);
+      top = warp_top(top);
+      if (top > -INFINITY) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) sum += x[j] = exp2_fast((x[j] - top) * kLog2e);
+        const float f = total * reciprocal(warp_sum(sum));
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) d[j] = fmaf(-x[j], f, d[j]);
+      }
+    }
+    typename Out::T* out = static_cast<typename Out::T*>(a.dlogits) + token * a.ld_dlogits;
+    if constexpr (kPer >= 8) {
+#pragma unroll
+      for (int c = 0; c < kPer; c += 8) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = d[c + j];
+        const int n = E - e0 - c;
+        if (n > 0) elem_store8<Out>(out + e0 + c, a.vec_out, n, v);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (e0 + j < E) out[e0 + j] = Out::put(d[j]);
+    }
+  }
+}
+
+}  // namespace route
+
+cudaError_t launch_route_backward(RouteArgs a, cudaStream_t st) {
+  using namespace route;
+  OverlapLaunch overlap;
+  a.vec_out = elem_vec_ok(a.dlogits, a.ld_dlogits, a.dlogits_dtype == FTMOE_OUT_FP32 ? 4 : 2);
+  return with_elem(a.dtype, [&](auto elem) {
+    return with_elem(a.dlogits_dtype, [&](auto out) {
+      return with_per(a.router.num_experts, [&](auto per) {
+        constexpr int kPer = decltype(per)::value;
+        a.vec = Row<decltype(elem), kPer>::vec_ok(a.logits, a.ld, a.router.num_experts);
+        return launch_kernel(route_backward_kernel<decltype(elem), decltype(out), kPer>,
+                             dim3((unsigned)std::min<int64_t>(cdiv(a.tokens, kWarps), 152 * kBlocksPerSm)), dim3(kThreads),
+                             kWarps * 32 * kPer * sizeof(float), st, true, a);
+      });
+    });
+  });
+}
+
+FTMOE_DEFINE_ERR_READER(read_err_route)
+
+}  // namespace ftmoe
