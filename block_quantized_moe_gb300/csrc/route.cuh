@@ -12,9 +12,6 @@ namespace ftmoe {
 
 namespace route {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kBlocksPerSm = 4;
 constexpr uint32_t kFull = 0xffffffffu;
 
 __device__ __forceinline__ float warp_sum(float v) {

@@ -10,6 +10,9 @@ namespace ftmoe {
 
 namespace route {
 
+constexpr int kThreads = 256, kWarps = kThreads / 32;  // (a row of shared memory a warp: 32 KB for 1,024 experts)
+constexpr int kBlocksPerSm = 4;
+
 // what a lane reads of a token's routes: its slot
 struct Slot {
   int id;

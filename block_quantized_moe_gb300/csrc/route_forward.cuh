@@ -7,7 +7,8 @@
 //
 // A warp per token, the next token's logits on their way meanwhile; lane l holds the experts
 // [l * kPer, (l + 1) * kPer). Top-k (choose_top): each lane keeps its three best values, and each of the k steps
-// takes the largest of the lanes' best. Where a lane gives all three (5% of tokens for 8 of 256) or values
+// takes the largest of the lanes' best. Where a lane gives all three (5% of
+// tokens for 8 of 256, 20% where half of the groups are left; four values a lane cost every token as much as that) or values
 // are too near (below), choose_few takes over: the k-th largest of the lanes' maxima is a threshold that at least k
 // values reach and few more do; they go to a lane each and are ranked by a count. A choice of more than kFewTopk, which
 // both would have too many for, takes the largest out of its lane's registers step by step (choose_many).
@@ -30,6 +31,8 @@ namespace ftmoe {
 
 namespace route {
 
+constexpr int kThreads = 512, kWarps = kThreads / 32;  // at most: see launch_as
+constexpr int kBlocksPerSm = 2;                        // (four of 256 threads are 2 to 5% slower)
 constexpr int kFewTopk = 12;  // 16 of 256 would have 21 candidates on average, 20 of 256 30
 
 // How far apart two fp32 values have to be for their order to be that of 64 bits: s is within
@@ -463,11 +466,11 @@ __device__ __forceinline__ int choose_many(float (&v)[kPer], bool biased, float 
 // A block takes consecutive tokens; its warps take them one by one, so that a token that has to be
 // taken in 64 bits holds up none of the others.
 template <typename Elem, int kPer, bool kFew, bool kBiased>
-__global__ void __launch_bounds__(kThreads, kPer <= 8 ? kBlocksPerSm : 2) route_kernel(const __grid_constant__ RouteArgs a) {
+__global__ void __launch_bounds__(kThreads, kPer <= 8 ? kBlocksPerSm : 1) route_kernel(const __grid_constant__ RouteArgs a) {
   __shared__ Candidate candidates[kWarps][32 + 8];  // (the last 8: 32 experts)
   __shared__ Slot2 slots[kWarps][32];
   __shared__ int taken_tokens;
-  if (threadIdx.x == 0) taken_tokens = kWarps;
+  if (threadIdx.x == 0) taken_tokens = (int)blockDim.x >> 5;
   __syncthreads();
   pdl_wait();
   pdl_trigger();
@@ -629,9 +632,9 @@ cudaError_t launch_as(RouteArgs a, cudaStream_t st) {
     a.vec = Row<Elem, kPer>::vec_ok(a.logits, a.ld, a.router.num_experts);
     auto* kernel = a.router.topk > kFewTopk ? route_kernel<Elem, kPer, false, false>
                    : a.bias != nullptr ? route_kernel<Elem, kPer, true, true> : route_kernel<Elem, kPer, true, false>;
-    // one token a block where there are few, else as many blocks as fit at once, of equal shares
-    const unsigned blocks = (unsigned)std::min<int64_t>(a.tokens, 152 * kBlocksPerSm);
-    return launch_kernel(kernel, dim3(blocks), dim3(kThreads), 0, st, true, a);
+    // as many blocks as fit at once, of equal shares, and a warp for each of their tokens where there are few
+    const int64_t blocks = std::min<int64_t>(a.tokens, 152 * kBlocksPerSm), most = cdiv(a.tokens, blocks);
+    return launch_kernel(kernel, dim3((unsigned)blocks), dim3(32 * (unsigned)std::min<int64_t>(most, kWarps)), 0, st, true, a);
   });
 }
 
