@@ -9,6 +9,7 @@
 // element beyond 2^38, gradients so small that their squares would be subnormal, NaN) are taken in fp64.
 // (One launch for small lists, a cluster of eight blocks whose sums meet in shared memory, was no faster:
 // 4.4 us for 1,000 elements and 7.1 for 262,144, where the two launches take 4.1.)
+// Measured on GB300: 939 M bf16 elements 269 us, 103% of the measured copy rate; 268 M fp32 ones 156 us, 102%.
 #include <algorithm>
 
 #include "common.cuh"
@@ -30,7 +31,13 @@ struct Entry {
 };
 
 constexpr int kFew = 64, kMany = 1024;  // gradients of a launch
-constexpr int kGrid = 152 * 8;          // blocks of a launch at most, one part each
+// Blocks of a launch, one part each: as many as are resident (a block more a SM runs in a second wave: 939 M bf16
+// elements 314 us instead of 269).
+constexpr int kGrid = 152 * 6;  // at most
+template <typename G>
+constexpr int grid_of() {
+  return 152 * (sizeof(typename G::T) == 4 ? 5 : 6);
+}
 
 // a sum and what its roundings left out
 struct Sum {
@@ -164,7 +171,7 @@ cudaError_t launch_some(const ftmoe_grad_list& list, int from, int to, double* p
     units += (int)cdiv(t.n, kPasses * kPass);
   }
   table.first[table.count] = units;
-  blocks = std::min(units, kGrid);
+  blocks = std::min(units, grid_of<G>());
   return launch_kernel(sums_kernel<G, kMax>, dim3(blocks), dim3(kThreads), 0, st, true, table, parts);
 }
 
