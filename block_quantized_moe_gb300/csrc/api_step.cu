@@ -26,7 +26,7 @@ ftmoe_status check_router(const ftmoe_router* r) {
   if (!r || r->num_experts <= 0 || r->topk <= 0 || r->groups <= 0 || r->num_experts % r->groups != 0 ||
       r->group_topk <= 0 || r->group_topk > r->groups || (r->group_best != 1 && r->group_best != 2) ||
       (r->score != FTMOE_SCORE_SOFTMAX && r->score != FTMOE_SCORE_SIGMOID) || (r->renormalize != 0 && r->renormalize != 1) ||
-      !(r->scale > 0.0f) || !(r->scale < INFINITY) || r->topk > (int64_t)r->group_topk * (r->num_experts / r->groups))
+      !(r->scale >= 1e-30f) || !(r->scale <= 1e30f) || r->topk > (int64_t)r->group_topk * (r->num_experts / r->groups))
     return FTMOE_INVALID_ARG;
   if (r->num_experts > kRouteMaxExperts || r->topk > kRouteMaxTopk || r->groups > kRouteMaxGroups) return FTMOE_UNSUPPORTED;
   return FTMOE_OK;

@@ -530,7 +530,7 @@ typedef struct ftmoe_router {
   int32_t groups;       /* divides num_experts: groups of consecutive experts; 1: none */
   int32_t group_topk;   /* groups a token may choose from, 1..groups */
   int32_t group_best;   /* a group's score: the sum of its 1 or 2 best values (groups > 1) */
-  float scale;          /* of the weights, > 0 and finite */
+  float scale;          /* of the weights, 1e-30 to 1e30 */
 } ftmoe_router;
 
 /* Routing: for each token, with x its logits,
@@ -539,11 +539,11 @@ typedef struct ftmoe_router {
  * scores can be chosen; the topk experts of the largest values are, largest first, and
  *   weights[i] = scale * s[id_i]             or, with renormalize,
  *   weights[i] = scale * s[id_i] / sum_j s[id_j].
- * Ties go to the lower group and the lower expert. The order is that of the values in 64 bits;
- * without bias that of the logits. An expert whose logit or bias is -inf or NaN is never chosen
+ * Ties go to the lower group and the lower expert. The order is that of the values in 64 bits
+ * (computed in fp32, and in fp64 wherever fp32 does not settle it); without bias that of the logits. An expert whose logit or bias is -inf or NaN is never chosen
  * (a NaN or -inf logit counts as exp(x) = 0 in the softmax), +inf counts as the largest finite number;
  * where fewer than topk experts are left the last slots are inactive routes, id -1 and weight 0. The
- * weights are exact to fp32's rounding, also where every chosen sigmoid underflows.
+ * weights are fp32, from fp32 exponentials; renormalised ones keep their ratios where every chosen sigmoid underflows.
  * logits: [tokens][num_experts], dtype an ftmoe_out_dtype, row stride ld. bias: float
  * [num_experts] or NULL. tokens_dev: optional device int32 count; the tokens at and beyond it get
  * inactive routes (ids -1, weights 0) and their logits are not read. expert_ids int32

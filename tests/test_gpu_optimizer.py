@@ -35,7 +35,8 @@ def check_norm(grads, scale=1.0, max_norm=math.inf):
     want = scale * math.sqrt(sum(float(g.double().square().sum()) for g in grads))
     factor = scale * min(1.0, max_norm / (want + 1e-6))
     got = norm_of(grads, scale=scale, max_norm=max_norm)
-    # sums of at most 8 + 4 positive terms in fp32, half of which the root keeps, and its rounding
+    # a chain of 8 positive terms in fp32 (the sums of those carry their errors along), half of which the root keeps,
+    # and its rounding
     assert abs(got[0] - want) <= 8 * EPS32 * want + 2.0 ** -150, (got, want)
     assert abs(got[1] - factor) <= 9 * EPS32 * factor, (got, factor)
 
@@ -389,6 +390,37 @@ def test_constants_on_the_device_and_replayed_graphs(narrow):
             else:
                 c, _ = codes_of(np.abs(m).astype(np.float64), (noise(m.size, 9, t, i) & np.uint64(0xFFFF)).astype(np.float64), 8, -6, 3)
                 np.testing.assert_array_equal(s["m"][i].cpu().numpy() & 127, c)
+
+
+def test_more_than_32_bits_of_elements():
+    """2^32 + 1000 elements: the ends and the places around 2^31 and 2^32 against the formulas, codes bit for bit, and the
+    norm of as many gradients."""
+    n = (1 << 32) + 1000
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    g = torch.zeros(n, dtype=torch.bfloat16, device=DEV)
+    p = torch.zeros(n, dtype=torch.bfloat16, device=DEV)
+    m, v = (torch.zeros(n, dtype=torch.uint8, device=DEV) for _ in range(2))
+    ms, vs = (torch.full((-(-n // 32),), b, dtype=torch.uint8, device=DEV) for b in (118, 105))
+    places = [(a, min(a + 2048, n)) for a in (0, (1 << 31) - 1024, (1 << 32) - 1024)]
+    for a, b in places:
+        g[a:b] = (torch.randn(b - a, generator=gen, device=DEV) * 0.1).to(torch.bfloat16)
+        p[a:b] = torch.randn(b - a, generator=gen, device=DEV).to(torch.bfloat16)
+        m[a:b] = torch.randint(0, 255, (b - a,), generator=gen, device=DEV).clamp(max=126).to(torch.uint8)
+        v[a:b] = torch.randint(1, 124, (b - a,), generator=gen, device=DEV).to(torch.uint8)
+    check_norm([g])
+    cut = {k: [t[a:b].clone() for a, b in places] for k, t in (("p", p), ("m", m), ("v", v))}
+    scales = {k: [t[a // 32:-(-b // 32)].clone() for a, b in places] for k, t in (("m", ms), ("v", vs))}
+    step_on({"params": [p], "grads": [g], "m": [m], "v": [v], "m_scales": [ms], "v_scales": [vs]}, step=7, seed=11)
+    for i, (a, b) in enumerate(places):
+        mm, vv = values(cut["m"][i], scales["m"][i], torch.float8_e4m3fn), values(cut["v"][i], scales["v"][i], torch.float8_e5m2)
+        mm, vv = new_moments(mm, vv, g[a:b].float().cpu().numpy(), 1.0)
+        check_params(p[a:b], cut["p"][i].double().cpu().numpy(), mm, vv, 7, "bf16")
+        h = noise(b - a, 11, 7, 0, first=a)
+        c, bytes_ = codes_of(np.abs(mm).astype(np.float64), (h & np.uint64(0xFFFF)).astype(np.float64), 8, -6, 3)
+        np.testing.assert_array_equal(m[a:b].cpu().numpy(), c | (np.signbit(mm).astype(np.uint8) << 7))
+        np.testing.assert_array_equal(ms[a // 32:-(-b // 32)].cpu().numpy(), bytes_)
+        c, _ = codes_of(vv.astype(np.float64), (h >> np.uint64(16)).astype(np.float64), 15, -14, 2)
+        np.testing.assert_array_equal(v[a:b].cpu().numpy(), np.where(vv > 0, np.maximum(c, 1), c))
 
 
 def test_another_stream():

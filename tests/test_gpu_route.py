@@ -355,6 +355,25 @@ def test_zero_tokens():
     ft.ftmoe_route_tokens_backward(x, r, ids, w, w.clone(), x.clone())
 
 
+def test_rows_far_apart():
+    """Rows 2^30 elements apart: offsets beyond 32 bits in elements and bytes."""
+    T, E, ld = 5, 64, 1 << 30
+    wide = torch.zeros((T - 1) * ld + E, dtype=torch.float16, device=DEV)
+    x = torch.as_strided(wide, (T, E), (ld, 1))
+    x.copy_(logits(T, E, "fp16", 40))
+    dense = x.contiguous()
+    for r, bias in ((router(E, 4), None), (router(E, 4, "sigmoid"), torch.linspace(-0.1, 0.1, E, device=DEV))):
+        ids, w = route(x, r, bias)
+        want, ww = route(dense, r, bias)
+        assert torch.equal(ids, want) and torch.equal(w, ww)
+        dwant = torch.empty_like(dense)
+        ft.ftmoe_route_tokens_backward(dense, r, want, ww, torch.ones_like(ww), dwant)
+        wide2 = torch.zeros((T - 1) * ld + E, dtype=torch.float16, device=DEV)
+        d = torch.as_strided(wide2, (T, E), (ld, 1))
+        ft.ftmoe_route_tokens_backward(x, r, ids, w, torch.ones_like(w), d)
+        assert torch.equal(d, dwant)
+
+
 def test_another_stream_and_a_replayed_graph():
     x, r = logits(65, 256, "fp32", 30), router(256, 6, "sigmoid", groups=8, group_topk=4, group_best=2)
     bias = torch.linspace(-0.2, 0.2, 256, device=DEV)

@@ -21,7 +21,7 @@ ROUTER = dict(num_experts=16, topk=2, score=0, renormalize=1, groups=4, group_to
 BAD_ROUTERS = [dict(num_experts=0), dict(num_experts=-1), dict(topk=0), dict(topk=9), dict(score=2), dict(score=-1),
                dict(renormalize=2), dict(groups=0), dict(groups=3), dict(group_topk=0), dict(group_topk=5),
                dict(group_best=0), dict(group_best=3), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("inf")),
-               dict(scale=float("nan"))]
+               dict(scale=float("nan")), dict(scale=1e-31), dict(scale=1e31)]
 LARGE_ROUTERS = [dict(num_experts=1028), dict(num_experts=256, topk=33), dict(num_experts=128, groups=64, group_topk=8)]
 
 
