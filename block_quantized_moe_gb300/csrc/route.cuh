@@ -31,8 +31,8 @@ __device__ __forceinline__ float taken(float x) { return fminf(fmaxf(x, -INFINIT
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
 // Scores for the order alone, by the hardware's exponential and reciprocal. exp(-x) is off by the
-// argument's rounding (|x| log2(e) 2^-24 ln 2 of it) and 2 units of the exponential: s by s (1 - s) of
-// that, at most 0.23 * 2^-24 + 2^-24, and by 2^-23 s of the sum's rounding and the reciprocal: under 2^-21.5.
+// argument's rounding (|x| 2^-23.6 of it) and 4 half steps of the exponential: s by s (1 - s) of that, at
+// most 0.3 * 2^-24 + 2^-24, and by 3 * 2^-24 s of the sum's rounding and the reciprocal: under 2^-21.5.
 constexpr float kLog2e = 1.44269504f;
 __device__ __forceinline__ float exp2_fast(float x) {
   float r;
@@ -102,8 +102,8 @@ struct Row {
       else x[j] = Elem::get((uint16_t)(raw[j / 2] >> (16 * (j % 2))));
     }
   }
-  // the logits as they take part: see taken(). (A token of numbers alone is left as it is: a product and a vote
-  // in place of two comparisons a logit, which run at half the rate.)
+  // the logits as they take part: see taken(). (A token of finite numbers is left as it is: a product
+  // and a vote in place of two comparisons a logit, which run at half the rate.)
   __device__ __forceinline__ void get_taken(float (&x)[kPer]) const {
     get(x);
     float zero = 0.0f;

@@ -1,28 +1,29 @@
-// Routing of tokens to experts from the router's logits, and its gradient.
+// Routing of tokens to experts from the router's logits.
 //
-// Forward, per token, with x its logits: s = softmax(x) or 1 / (1 + exp(-x)), value = s + bias;
+// Per token, with x its logits: s = softmax(x) or 1 / (1 + exp(-x)), value = s + bias;
 // groups of consecutive experts are ranked by the sum of their 1 or 2 best values and all but the
 // best groups left out; the top-k values are chosen, largest first, ties to the lower expert; the
 // weights are the chosen s times the scale, renormalised to sum to it where asked.
 //
 // A warp per token, the next token's logits on their way meanwhile; lane l holds the experts
-// [l * kPer, (l + 1) * kPer). Top-k (choose_top): each lane keeps its three best values, and each of the k steps
-// takes the largest of the lanes' best. Where a lane gives all three (5% of
-// tokens for 8 of 256, 20% where half of the groups are left; four values a lane cost every token as much as that) or values
-// are too near (below), choose_few takes over: the k-th largest of the lanes' maxima is a threshold that at least k
-// values reach and few more do; they go to a lane each and are ranked by a count. A choice of more than kFewTopk, which
-// both would have too many for, takes the largest out of its lane's registers step by step (choose_many).
+// [l * kPer, (l + 1) * kPer). Top-k (choose_top): each lane keeps its three best values, and each of the
+// k steps takes the largest of the lanes' best. Where a lane gives all three (5% of tokens for 8 of 256,
+// 20% where half of the groups are left; four values a lane cost every token as much as that) or
+// values are too near (below), choose_few takes over: the k-th largest of the lanes' maxima is a
+// threshold that at least k values reach and few more do; they go to a lane each and are ranked by a
+// count. A choice of more than kFewTopk, which would have too many for both, takes the largest out of
+// its lane's registers step by step (choose_many).
 // Without a bias the logits themselves are the order and nothing is rounded. With one, the order of
 // s + bias is that of 64 bits: fp32 values are off by less than half of tolerance(), and where two
-// neighbours in the order are nearer than that (and not the same logit and bias, a tie in any precision) the candidates'
-// values are taken again in 64 bits, a lane each; groups at the border likewise (settle_groups). More candidates than
-// lanes take the whole token again (route_exact).
+// neighbours in the order are nearer than that (and not the same logit and bias, a tie in any
+// precision) the candidates' values are taken again in 64 bits, a lane each; groups at the border
+// likewise (settle_groups). More candidates than lanes take the whole token again (route_exact).
 //
-// Measured on GB300, a call among others: 32,768 tokens of 256 experts, top-8 of 4 of 8 groups, sigmoid and bias
-// 29 us; without bias and groups 19 us (k = 1: 13 us), where the logits are 33.5 MB, 5 us of memory. Instructions
-// bound it: 270 a token for k = 1, about 20 more a step, most of them on the half-rate ALU pipe (steps that rescan the
-// owner's registers took 70 each, 94 us in all; the threshold for every token 42 us).
-// One token, or eight: 2 to 3 us, launch and latency.
+// Measured on GB300, a call among others: 32,768 tokens of 256 experts, top-8 of 4 of 8 groups, sigmoid
+// and bias 29 us; without bias and groups 18 us (k = 1: 12 us), where the logits are 33.5 MB, 5 us of
+// memory. Instructions bound it: 270 a token for k = 1, about 20 more a step, most of them on the
+// half-rate ALU pipe (steps that rescan the owner's registers took 70 each, 94 us in all; the
+// threshold for every token 42 us). One token, or eight: 2 to 3 us, launch and latency.
 #pragma once
 
 #include "route.cuh"
@@ -35,14 +36,14 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;  // at most: see launch_as
 constexpr int kBlocksPerSm = 2;                        // (four of 256 threads are 2 to 5% slower)
 constexpr int kFewTopk = 12;  // 16 of 256 would have 21 candidates on average, 20 of 256 30
 
-// How far apart two fp32 values have to be for their order to be that of 64 bits: s is within
-// 2^-21 of the largest score (sigmoid_fast as above, the largest score taken as 1; softmax: exponentials of arguments
-// rounded by |x - top| 2^-23, which times exp(x - top) is below 2^-24 of the largest, and 2 units of
-// the exponential, a sum of 32 terms a lane at most and 5 levels, its reciprocal: 2^-21 of s), the sum with
-// the bias within 2^-24 of itself; twice that for two values, and as much again to spare.
-__device__ __forceinline__ float tolerance(float largest_score, float v) {
-  return 0x1p-19f * largest_score + 0x1p-21f * fabsf(v);
-}
+// How far apart two fp32 values have to be for their order to be that of 64 bits: scores are off by
+// at most 2^-21.5 (sigmoid_fast), or 45 * 2^-24 = 2^-18.5 of the largest (softmax: arguments rounded by
+// |x - top| 2^-23, which times exp(x - top) is below 2^-24 of the largest; 4 half steps of the
+// exponential; 37 of a sum of 32 terms a lane and 5 levels; 3 of its reciprocal and the product),
+// and sums with the bias by 2^-24 of themselves; twice that for two values, and some to spare.
+// unit: see score_unit.
+__device__ __forceinline__ float tolerance(float unit, float v) { return 0x1p-19f * unit + 0x1p-21f * fabsf(v); }
+__device__ __forceinline__ float score_unit(bool softmax, float largest_score) { return softmax ? 4.0f * largest_score : 1.0f; }
 
 // scores for the order (0 where an expert takes no part)
 template <int kPer>
@@ -360,6 +361,7 @@ template <typename Elem, int kPer>
 __device__ __forceinline__ bool choose_few(const float (&v)[kPer], const float (&x)[kPer], const RouteArgs& a,
                                            const typename Elem::T* row, bool biased, bool softmax, float top,
                                            float largest_score, int topk, int lane, Candidate* shared, Candidate& mine) {
+  const float unit = score_unit(softmax, largest_score);
   // the threshold (equal maxima go together: it is then lower than it need be)
   float best = v[0];
 #pragma unroll
@@ -370,7 +372,7 @@ __device__ __forceinline__ bool choose_few(const float (&v)[kPer], const float (
     from = warp_top(best);
     best = best == from ? -INFINITY : best;
   }
-  if (biased) from -= tolerance(largest_score, from);
+  if (biased) from -= tolerance(unit, from);
   from = fmaxf(from, -FLT_MAX);
   uint32_t mask = 0u;
 #pragma unroll
@@ -384,7 +386,7 @@ __device__ __forceinline__ bool choose_few(const float (&v)[kPer], const float (
     mine.x = taken(Elem::get(row[mine.expert]));
     mine.v = mine.x;
     if (biased) {
-      mine.b = taken(__ldg(a.bias + mine.expert));
+      mine.b = taken(a.bias[mine.expert]);
       mine.v = score_fast(mine.x, softmax, top, largest_score) + mine.b;
     }
   }
@@ -402,7 +404,7 @@ __device__ __forceinline__ bool choose_few(const float (&v)[kPer], const float (
   if (biased) {
     const float next = __shfl_down_sync(kFull, mine.v, 1);
     // (pairs beyond the last slot too: one that is not the same may follow several that are)
-    bool near = lane + 1 < total && mine.v - next <= tolerance(largest_score, mine.v);
+    bool near = lane + 1 < total && mine.v - next <= tolerance(unit, mine.v);
     if (__any_sync(kFull, near)) {
       const float next_x = __shfl_down_sync(kFull, mine.x, 1), next_b = __shfl_down_sync(kFull, mine.b, 1);
       near = near && (next_x != mine.x || next_b != mine.b);
@@ -428,7 +430,7 @@ __device__ __forceinline__ bool choose_few(const float (&v)[kPer], const float (
 
 // Top-k a step at a time; `near` where two neighbours in the order have to be taken in 64 bits.
 template <int kPer>
-__device__ __forceinline__ int choose_many(float (&v)[kPer], bool biased, float largest_score, int topk, int lane, bool& near) {
+__device__ __forceinline__ int choose_many(float (&v)[kPer], bool biased, float unit, int topk, int lane, bool& near) {
   int chosen = -1;
   float slot = -INFINITY, best = v[0];
 #pragma unroll
@@ -456,8 +458,8 @@ __device__ __forceinline__ int choose_many(float (&v)[kPer], bool biased, float 
     // pairs of neighbours in the order, and the last chosen against the best of the rest (whatever it is)
     const int next = __shfl_down_sync(kFull, chosen, 1);
     const float next_value = __shfl_down_sync(kFull, slot, 1), last = __shfl_sync(kFull, slot, topk - 1);
-    bool close = lane + 1 < topk && next >= 0 && slot - next_value <= tolerance(largest_score, slot);
-    if (last > -INFINITY) close = close || (best > -INFINITY && last - best <= tolerance(largest_score, last));
+    bool close = lane + 1 < topk && next >= 0 && slot - next_value <= tolerance(unit, slot);
+    if (last > -INFINITY) close = close || (best > -INFINITY && last - best <= tolerance(unit, last));
     near = __any_sync(kFull, close);
   }
   return chosen;
@@ -513,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, kPer <= 8 ? kBlocksPerSm : 1) route_
 
       float top = 0.0f, sum = 1.0f;
       if (all_scores) softmax_stats(x, top, sum);
-      const float largest_score = softmax ? reciprocal(sum) : 1.0f;
+      const float largest_score = softmax ? reciprocal(sum) : 1.0f, unit = score_unit(softmax, largest_score);
       float v[kPer];  // the order of the experts (-inf: never chosen)
       if (biased) {
         scores(x, softmax, top, largest_score, v);
@@ -540,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, kPer <= 8 ? kBlocksPerSm : 1) route_
           mine = score_fast(g1, softmax, top, largest_score);
         if (!inside) mine = -INFINITY;
         kept = keep_groups(mine, lane, a.group_lanes, a.router.group_topk, last, next_best);
-        const float near = 2.0f * tolerance(largest_score, last);
+        const float near = 2.0f * tolerance(unit, last);
         if (scored_groups && next_best > -INFINITY && last - next_best <= near)
           exact = !settle_groups<Elem, kPer>(v, x, a, row, softmax, top, g1, g2, mine, last, next_best, near, lane,
                                              reinterpret_cast<int32_t*>(candidates[warp] + 32), kept);
@@ -553,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, kPer <= 8 ? kBlocksPerSm : 1) route_
         for (int j = 0; j < kPer; ++j) s[j] = !biased && scored_groups && x[j] > -INFINITY ? s[j] : v[j];
         const float mine = any_group_scores(s, lane, a.router.groups, size, a.router.group_best);
         const uint32_t groups = __ballot_sync(kFull, keep_groups(mine, lane, 1, a.router.group_topk, last, next_best));
-        exact = scored_groups && next_best > -INFINITY && last - next_best <= 2.0f * tolerance(largest_score, last);
+        exact = scored_groups && next_best > -INFINITY && last - next_best <= 2.0f * tolerance(unit, last);
         int group = lane * kPer / size, rest = lane * kPer - group * size;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
@@ -575,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, kPer <= 8 ? kBlocksPerSm : 1) route_
               // (a neighbour as near as that, the best of the rest after the last)
               const float below = __shfl_down_sync(kFull, s.v, 1);
               if (chosen >= 0) cx = taken(Elem::get(row[chosen]));
-              fine = !__any_sync(kFull, chosen >= 0 && s.v - (lane + 1 < topk ? below : rest) <= tolerance(largest_score, s.v));
+              fine = !__any_sync(kFull, chosen >= 0 && s.v - (lane + 1 < topk ? below : rest) <= tolerance(unit, s.v));
             }
           }
           if (!fine) {
@@ -591,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, kPer <= 8 ? kBlocksPerSm : 1) route_
         bool near;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) v[j] = kept ? v[j] : -INFINITY;
-        chosen = choose_many(v, biased, largest_score, topk, lane, near);
+        chosen = choose_many(v, biased, unit, topk, lane, near);
         exact = exact || near;
         if (chosen >= 0) cx = taken(Elem::get(row[chosen]));
       }
