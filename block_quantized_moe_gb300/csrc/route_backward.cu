@@ -10,7 +10,7 @@ namespace ftmoe {
 
 namespace route {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;  // (a row of shared memory a warp: 32 KB for 1,024 experts)
+constexpr int kThreads = 256;  // (a row of shared memory a token: 32 KB for 1,024 experts, 16 tokens of 512)
 constexpr int kBlocksPerSm = 4;
 
 // what a lane reads of a token's routes: its slot
@@ -20,7 +20,7 @@ struct Slot {
   __device__ __forceinline__ void load(const RouteArgs& a, int64_t token, int lane, int topk) {
     id = -1;
     w = dw = 0.0f;
-    if (lane < topk) {
+    if (lane < topk && token < a.tokens) {
       const int64_t at = token * topk + lane;
       id = a.ids[at];
       w = a.weights[at];
@@ -29,56 +29,73 @@ struct Slot {
   }
 };
 
-template <typename Elem, typename Out, int kPer>
+// over the kLanes lanes of a token
+template <int kLanes>
+__device__ __forceinline__ float token_sum(float v) {
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+template <int kLanes>
+__device__ __forceinline__ float token_top(float v) {
+  if constexpr (kLanes == 32) {
+    return warp_top(v);
+  } else {
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+  }
+}
+
+template <typename Elem, typename Out, int kPer, int kLanes>
 __global__ void __launch_bounds__(kThreads) route_backward_kernel(const __grid_constant__ RouteArgs a) {
   extern __shared__ float4 rows[];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
+  const int warp_lane = threadIdx.x & 31, first = warp_lane & ~(kLanes - 1);  // the token's first lane
+  const int lane = warp_lane - first;
+  const uint32_t lanes = (kLanes < 32 ? (1u << kLanes) - 1u : kFull) << first;
   const int E = a.router.num_experts, topk = a.router.topk, e0 = lane * kPer;
-  float* const part = reinterpret_cast<float*>(rows) + (threadIdx.x >> 5) * (32 * kPer);
+  float* const part = reinterpret_cast<float*>(rows) + (threadIdx.x / kLanes) * (kLanes * kPer);
   const bool softmax = a.router.score == FTMOE_SCORE_SOFTMAX, whole = softmax && !a.router.renormalize;
   const float per_scale = 1.0f / a.router.scale;
-  const int64_t stride = (int64_t)gridDim.x * kWarps;
-  int64_t token = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int64_t stride = (int64_t)gridDim.x * (kThreads / kLanes);
+  int64_t token = (int64_t)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
   Row<Elem, kPer> next_row;
   Slot next;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) part[lane + 32 * j] = 0.0f;  // and again after each token
+  for (int j = 0; j < kPer; ++j) part[lane + kLanes * j] = 0.0f;  // and again after each token
   __syncwarp();
-  if (token < a.tokens) {
-    next.load(a, token, lane, topk);
-    if (whole) next_row.load(static_cast<const typename Elem::T*>(a.logits) + token * a.ld, lane, E, a.vec);
-  }
-  for (; token < a.tokens; token += stride) {
+  next.load(a, token, lane, topk);
+  if (whole && token < a.tokens) next_row.load(static_cast<const typename Elem::T*>(a.logits) + token * a.ld, lane, E, a.vec);
+  // (the lanes of a warp go round together: its first token is there as long as any is)
+  for (; token - first / kLanes < a.tokens; token += stride) {
+    const bool there = token < a.tokens;
     const typename Elem::T* row = static_cast<const typename Elem::T*>(a.logits) + token * a.ld;
     Slot s = next;
     const Row<Elem, kPer> this_row = next_row;
-    if (token + stride < a.tokens) {
-      next.load(a, token + stride, lane, topk);
-      if (whole) next_row.load(row + stride * a.ld, lane, E, a.vec);
-    }
+    next.load(a, token + stride, lane, topk);
+    if (whole && token + stride < a.tokens) next_row.load(row + stride * a.ld, lane, E, a.vec);
     if (s.id >= E) raise_error(FTMOE_ERR_EXPERT_ID_RANGE);
     if (s.id < 0 || s.id >= E) s.id = -1, s.w = 0.0f, s.dw = 0.0f;
     float r = s.w * s.dw;
-    const float total = warp_sum(r);
+    const float total = token_sum<kLanes>(r);
     if (a.router.renormalize) r = fmaf(-s.w, total * per_scale, r);
     if (!softmax && s.id >= 0) r *= 1.0f / (1.0f + expf(taken(Elem::get(row[s.id]))));
-    // the terms in the row. An id that occurs twice (a lane reads another's number in its place): the
-    // first of its lanes puts the sum there
+    // the terms in the row. An id that occurs twice (a lane reads another's number in its place): each
+    // of its lanes puts their sum there
     const bool active = s.id >= 0;
     if (active) part[s.id] = __int_as_float(lane);
     __syncwarp();
     const bool second = active && __float_as_int(part[s.id]) != lane;
-    const uint32_t seconds = __ballot_sync(kFull, second);
-    if (seconds != 0u) {
-      const uint32_t same = __match_any_sync(kFull, s.id);
+    if (__any_sync(kFull, second)) {
+      const uint32_t same = __match_any_sync(kFull, active ? s.id + (first << 16) : -1);
       float all = 0.0f;
       for (int t = 0; t < topk; ++t) {
-        const float other = __shfl_sync(kFull, r, t);
-        all += (same >> t) & 1u ? other : 0.0f;
+        const float other = __shfl_sync(kFull, r, first + t);
+        all += (same >> (first + t)) & 1u ? other : 0.0f;
       }
-      r = all;  // (the same sum on each of them)
+      r = all;
     }
     __syncwarp();
     if (active) part[s.id] = r;
@@ -98,16 +115,17 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const __grid_c
     __syncwarp();
     if (active) part[s.id] = 0.0f;
     __syncwarp();
-    if (whole && __any_sync(kFull, active)) {
+    const bool any = (__ballot_sync(kFull, active) & lanes) != 0u;
+    if (whole) {
       float x[kPer], top = -INFINITY, sum = 0.0f;
       this_row.get_taken(x);
 #pragma unroll
       for (int j = 0; j < kPer; ++j) top = fmaxf(top, x[j]);
-      top = warp_top(top);
-      if (top > -INFINITY) {
+      top = token_top<kLanes>(top);
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) sum += x[j] = exp2_fast((x[j] - top) * kLog2e);
-        const float f = total * reciprocal(warp_sum(sum));
+      for (int j = 0; j < kPer; ++j) sum += x[j] = exp2_fast((x[j] - top) * kLog2e);
+      const float f = total * reciprocal(token_sum<kLanes>(sum));
+      if (any && top > -INFINITY) {
 #pragma unroll
         for (int j = 0; j < kPer; ++j) d[j] = fmaf(-x[j], f, d[j]);
       }
@@ -119,13 +137,13 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const __grid_c
         float v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = d[c + j];
-        const int n = E - e0 - c;
+        const int n = there ? E - e0 - c : 0;
         if (n > 0) elem_store8<Out>(out + e0 + c, a.vec_out, n, v);
       }
     } else {
 #pragma unroll
       for (int j = 0; j < kPer; ++j)
-        if (e0 + j < E) out[e0 + j] = Out::put(d[j]);
+        if (there && e0 + j < E) out[e0 + j] = Out::put(d[j]);
     }
   }
 }
@@ -136,14 +154,19 @@ cudaError_t launch_route_backward(RouteArgs a, cudaStream_t st) {
   using namespace route;
   OverlapLaunch overlap;
   a.vec_out = elem_vec_ok(a.dlogits, a.ld_dlogits, a.dlogits_dtype == FTMOE_OUT_FP32 ? 4 : 2);
+  // half a warp a token where its slots and experts fit: two tokens share what a warp does once
+  const bool half = a.router.topk <= 16 && a.router.num_experts <= 512;
   return with_elem(a.dtype, [&](auto elem) {
     return with_elem(a.dlogits_dtype, [&](auto out) {
-      return with_per(a.router.num_experts, [&](auto per) {
+      using E = decltype(elem);
+      using Out = decltype(out);
+      return with_per(half ? 2 * a.router.num_experts : a.router.num_experts, [&](auto per) {
         constexpr int kPer = decltype(per)::value;
-        a.vec = Row<decltype(elem), kPer>::vec_ok(a.logits, a.ld, a.router.num_experts);
-        return launch_kernel(route_backward_kernel<decltype(elem), decltype(out), kPer>,
-                             dim3((unsigned)std::min<int64_t>(cdiv(a.tokens, kWarps), 152 * kBlocksPerSm)), dim3(kThreads),
-                             kWarps * 32 * kPer * sizeof(float), st, true, a);
+        a.vec = Row<E, kPer>::vec_ok(a.logits, a.ld, a.router.num_experts);
+        const int64_t tokens = kThreads / (half ? 16 : 32);  // of a block at a time
+        return launch_kernel(half ? route_backward_kernel<E, Out, kPer, 16> : route_backward_kernel<E, Out, kPer, 32>,
+                             dim3((unsigned)std::min<int64_t>(cdiv(a.tokens, tokens), 152 * kBlocksPerSm)), dim3(kThreads),
+                             kThreads * kPer * sizeof(float), st, true, a);
       });
     });
   });

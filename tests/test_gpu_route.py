@@ -264,7 +264,7 @@ def exact_gradient(x, r, ids, dw):
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [False, True])
-@pytest.mark.parametrize("E,k", [(1, 1), (2, 1), (7, 3), (64, 8), (96, 5), (129, 4), (256, 6), (500, 32), (1024, 9)])
+@pytest.mark.parametrize("E,k", [(1, 1), (2, 1), (7, 3), (64, 8), (96, 5), (129, 4), (256, 6), (256, 16), (256, 17), (500, 32), (512, 16), (513, 16), (1024, 9)])
 def test_gradient(E, k, renorm, score):
     for T, dtype, out, pad in ((33, "fp32", "fp32", 0), (5, "bf16", "bf16", 0), (6, "fp16", "fp32", 3), (4, "fp32", "fp16", 8)):
         x = logits(T, E, dtype, E + T, pad=pad)
@@ -334,6 +334,25 @@ def test_gradient_of_repeated_and_wrong_ids():
     assert ((d.double() - want).abs() <= want.abs() * 32 * EPS32).all()
     assert ft.ftmoe_read_error_flags() == ft.ERR_EXPERT_ID_RANGE
     assert ft.ftmoe_read_error_flags() == 0
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 15, 16, 17, 2500, 20001])
+def test_gradients_of_any_number_of_tokens(T):
+    """Whatever the number of tokens, each token's row is that of the token alone, and nothing behind the last is written."""
+    x = logits(T, 64, "fp32", T)
+    for renorm, score in ((False, "softmax"), (True, "sigmoid")):
+        r = router(64, 4, score, renormalize=renorm)
+        ids, w = route(x, r)
+        ids[T // 2] = -1
+        wide = torch.full((T + 20, 64), 7.0, device=DEV)
+        ft.ftmoe_route_tokens_backward(x, r, ids, w, torch.ones_like(w).cumsum(1), wide[:T])
+        assert (wide[T:] == 7.0).all() and (wide[T // 2] == 0).all()
+        for t in {0, T // 3, T - 1}:
+            alone = torch.empty(1, 64, device=DEV)
+            ft.ftmoe_route_tokens_backward(x[t:t + 1], r, ids[t:t + 1], w[t:t + 1], torch.ones_like(w[:1]).cumsum(1), alone)
+            assert torch.equal(alone[0], wide[t])
+        want = exact_gradient(x, r, ids, torch.ones_like(w).cumsum(1))
+        assert ((wide[:T].double() - want).abs() <= 4 * 4 * 200 * EPS32 + want.abs() * EPS32).all()
 
 
 def test_gradient_of_masked_logits():
