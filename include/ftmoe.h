@@ -515,7 +515,9 @@ ftmoe_status ftmoe_silu_mul_backward(const uint8_t* q, const void* scales, int32
  * Around the experts' products (no counterpart in the pages; services of this library): the
  * router that makes expert_ids and weights from its logits, with its gradient, and what uses
  * the gradients of a training step: their global norm and an AdamW step. The logits are a
- * product of ftmoe_grouped_matmul with one expert, whose matrix is the router's.
+ * product of ftmoe_grouped_matmul with one expert, whose matrix is the router's. All of these
+ * calls may be captured into a CUDA graph. One training step of a whole routed layer:
+ * examples/train_layer.py.
  * ------------------------------------------------------------------------------------ */
 
 typedef enum ftmoe_score { FTMOE_SCORE_SOFTMAX = 0, FTMOE_SCORE_SIGMOID = 1 } ftmoe_score;
