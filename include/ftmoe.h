@@ -542,10 +542,11 @@ typedef struct ftmoe_router {
  *   weights[i] = scale * s[id_i]             or, with renormalize,
  *   weights[i] = scale * s[id_i] / sum_j s[id_j].
  * Ties go to the lower group and the lower expert. The order is that of the values in 64 bits
- * (computed in fp32, and in fp64 wherever fp32 does not settle it); without bias that of the logits. An expert whose logit or bias is -inf or NaN is never chosen
- * (a NaN or -inf logit counts as exp(x) = 0 in the softmax), +inf counts as the largest finite number;
- * where fewer than topk experts are left the last slots are inactive routes, id -1 and weight 0. The
- * weights are fp32, from fp32 exponentials; renormalised ones keep their ratios where every chosen sigmoid underflows.
+ * (computed in fp32, and in fp64 wherever fp32 does not settle it); without bias that of the
+ * logits. An expert whose logit or bias is -inf or NaN is never chosen (a NaN or -inf logit counts as
+ * exp(x) = 0 in the softmax), +inf counts as the largest finite number; where fewer than topk
+ * experts are left the last slots are inactive routes, id -1 and weight 0. The weights are fp32, from
+ * fp32 exponentials; renormalised ones keep their ratios where every chosen sigmoid underflows.
  * logits: [tokens][num_experts], dtype an ftmoe_out_dtype, row stride ld. bias: float
  * [num_experts] or NULL. tokens_dev: optional device int32 count; the tokens at and beyond it get
  * inactive routes (ids -1, weights 0) and their logits are not read. expert_ids int32
@@ -592,23 +593,24 @@ size_t ftmoe_grad_norm_workspace_bytes(const ftmoe_grad_list* list);
  *   result[0] = norm = scale * sqrt(sum of squares of every element of every gradient)
  *   result[1] = scale * min(1, max_norm / (norm + 1e-6));  NaN where the norm is not finite
  * result: device float[2]; result + 1 is a grad_scale for ftmoe_adamw_step, which takes no step for
- * a NaN. max_norm > 0 (INFINITY: no clipping), scale > 0 and finite. Squares are summed in fp32
- * over eight elements and from there in pairs of fp32 numbers and in fp64; where they leave fp32's range they are taken in
- * fp64, so that gradients of any finite size have their norm. The order of the sums is fixed by the
- * sizes: the same bits every time. The workspace (8-byte aligned; contents need not be set) is
- * used until the call's work completes, by one call at a time. */
+ * a NaN. max_norm > 0 (INFINITY: no clipping), scale > 0 and finite. Without elements the norm is
+ * 0. Squares are summed in fp32 over eight elements and from there in pairs of fp32 numbers and in
+ * fp64; where they leave fp32's range they are taken in fp64, so that gradients of any finite size
+ * have their norm. The order of the sums is fixed by the sizes: the same bits every time. The
+ * workspace (8-byte aligned; contents need not be set) is used until the call's work completes, by
+ * one call at a time. */
 ftmoe_status ftmoe_grad_norm(const ftmoe_grad_list* list, float scale, float max_norm, void* workspace,
                              size_t workspace_bytes, float* result, void* stream);
 
 /* How AdamW's moments are kept. 8BIT: per 32 consecutive elements of a tensor (the last group may
- * be shorter) an E8M0 byte b for 2^(b - 127), and codes: e4m3 for the first moment m, e5m2 for
- * the second, v; value = code * 2^(b - 127). The power is the smallest of at least 2^-127 for which the group's
- * largest magnitude is at most the format's largest (448; 57,344). Codes are rounded
- * stochastically: up with the probability of what is cut off (to 16 bits), so that moments
- * which change by less than half a step still move, on average by what they should. A v above zero
- * is never rounded to zero (its code is at least 1). NaN and infinite moments stay so (an
- * infinite one as the largest code of a group whose value of it is infinite in fp32). The random bits are a hash of (seed, step, tensor's place in the list,
- * element). */
+ * be shorter) an E8M0 byte b for 2^(b - 127), and codes: e4m3 for the first moment m, e5m2 for the
+ * second, v; value = code * 2^(b - 127). The power is the smallest of at least 2^-127 for which the
+ * group's largest magnitude is at most the format's largest (448; 57,344). Codes are rounded
+ * stochastically: up with the probability of what is cut off (to 16 bits), so that moments which
+ * change by less than half a step still move, on average by what they should. A v above zero is
+ * never rounded to zero (its code is at least 1). NaN and infinite moments stay so (an infinite one
+ * as the largest code of a group whose value of it is infinite in fp32). The random bits are a hash
+ * of (seed, step, the tensor's place in the list, element): another seed or step gives others. */
 typedef enum ftmoe_moments { FTMOE_MOMENTS_FP32 = 0, FTMOE_MOMENTS_8BIT = 1 } ftmoe_moments;
 
 /* One tensor of an AdamW step: n consecutive elements of each array. n = 0: nothing. */
