@@ -168,6 +168,46 @@ def test_router_in_front_of_the_fused_forward():
     assert ft.ftmoe_read_error_flags() == 0
 
 
+def test_calls_from_several_threads():
+    """Four threads with streams and tensors of their own, calling at once: what each gets is what it gets alone."""
+    import threading
+    E, topk, T, n = 256, 6, 700, 50_000
+    router = ft.make_router(E, topk, score=ft.SCORE_SIGMOID, groups=8, group_topk=4, group_best=2)
+
+    def work(seed, stream):
+        gen = torch.Generator(device=DEV).manual_seed(seed)
+        logits, bias = torch.randn(T, E, generator=gen, device=DEV), torch.randn(E, generator=gen, device=DEV) * 0.1
+        ids, weights = torch.empty(T, topk, dtype=torch.int32, device=DEV), torch.empty(T, topk, device=DEV)
+        dlogits, p = torch.empty(T, E, device=DEV), torch.randn(n, generator=gen, device=DEV)
+        m, v = (torch.zeros(n, dtype=torch.uint8, device=DEV) for _ in range(2))
+        ms, vs = (torch.zeros(-(-n // 32), dtype=torch.uint8, device=DEV) for _ in range(2))
+        g = dlogits.view(-1)[:n]
+        grads, tensors = ft.make_grad_list([g]), ft.make_adamw_list([p], [g], [m], [v], [ms], [vs])
+        norm, ws = torch.empty(2, device=DEV), torch.empty(ft.ftmoe_grad_norm_workspace_bytes(grads), dtype=torch.uint8, device=DEV)
+        torch.cuda.synchronize()
+        for t in range(1, 31):
+            ft.ftmoe_route_tokens(logits, router, ids, weights, bias=bias, stream=stream)
+            ft.ftmoe_route_tokens_backward(logits, router, ids, weights, weights, dlogits, stream=stream)
+            ft.ftmoe_grad_norm(grads, norm, ws, max_norm=0.1, stream=stream)
+            ft.ftmoe_adamw_step(tensors, step=t, seed=seed, grad_scale=norm[1:], stream=stream)
+        stream.synchronize()
+        return ids, weights, dlogits, norm, p, m, v, ms, vs
+
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    alone = [work(seed, streams[0]) for seed in range(4)]
+    got = [None] * 4
+
+    def run(i):
+        got[i] = work(i, streams[i])
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for a, b in zip(alone, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 @pytest.mark.parametrize("moments", ["fp32", "8bit"])
 def test_example_runs(moments, monkeypatch):
     import sys
