@@ -226,50 +226,39 @@ __device__ __forceinline__ Best3 best3(const float (&v)[kPer]) {
   return t;
 }
 
-// a chosen expert and its value
-struct Slot2 {
-  int32_t expert;
-  float v;
-};
-
 // Top-k from the lanes' three best values: each step takes the largest of the lanes' best, and its lane's
-// next moves up. slots[t] gets the expert of slot t (-1: none); rest: the best value left.
+// next moves up. Lane t gets the expert of slot t (-1: none) and its value; rest: the best value left.
 // false: a lane gave three, and what it has left is not known (5% of tokens for 8 of 256 experts), or
-// there are not enough (-inf comes from the lowest lane again and again).
+// two that are equal, or there are not enough (-inf comes from the lowest lane again and again).
 // (A step is a maximum and a vote over the warp, 24 cycles each; selects rather than branches, and
-// no first-set-bit, which runs at a quarter of the vote's rate.)
+// no first-set-bit, which runs at a quarter of the vote's rate. The experts' places in their lanes are
+// found at the end, for all slots at once, by an exchange for each of a lane's values.)
 template <int kPer>
-__device__ __forceinline__ bool choose_top(const float (&v)[kPer], Best3 t, int topk, int lane, Slot2* slots, float& rest) {
-  const Best3 all = t;
+__device__ __forceinline__ bool choose_top(const float (&v)[kPer], Best3 t, int topk, int lane, int& expert, float& value, float& rest) {
   const uint32_t below = (1u << lane) - 1u;
-  uint32_t order = 0u;  // a byte for each value that this lane gives: its slot, from 1; the last in the lowest byte
+  const bool twins = t.a == t.b;
+  uint32_t givers = 0u;  // lane t: those whose best was the largest at slot t (the lowest gave it)
+  int given = 0;         // values that this lane gave
+  value = -INFINITY;
 #pragma unroll 4
-  for (int n = 1; n <= topk; ++n) {
+  for (int n = 0; n < topk; ++n) {
     const float most = warp_top(t.a);
     const bool is = t.a == most;
     const uint32_t alike = __ballot_sync(kFull, is);  // (by every lane, so not behind a condition)
     const bool first = is && (alike & below) == 0u;
-    order = first ? order << 8 | (uint32_t)n : order;
+    givers = lane == n ? alike : givers;
+    value = lane == n ? most : value;
+    given += first ? 1 : 0;
     t.a = first ? t.b : t.a;
     t.b = first ? t.c : t.b;  // (what follows the third value is never used: see below)
   }
-  if (__any_sync(kFull, order > 0xffffu)) return false;
+  if (__any_sync(kFull, given > 2 || (given == 2 && twins))) return false;
   rest = warp_top(t.a);
-  __syncwarp();  // (the last token's slots have been read)
-  if (order != 0u) {
-    // equal values were taken in the experts' order: the first equal to each
-    int at = kPer;
+  const int giver = __ffs(givers) - 1;
+  int at = 0;
 #pragma unroll
-    for (int j = kPer - 1; j >= 0; --j) at = v[j] == all.a ? j : at;
-    slots[(order > 0xffu ? order >> 8 : order) - 1u] = {all.a > -INFINITY ? lane * kPer + at : -1, all.a};
-    if (order > 0xffu) {
-      const int before = at;
-#pragma unroll
-      for (int j = kPer - 1; j >= 0; --j) at = v[j] == all.b && (all.b != all.a || j > before) ? j : at;
-      slots[(order & 0xffu) - 1u] = {all.b > -INFINITY ? lane * kPer + at : -1, all.b};
-    }
-  }
-  __syncwarp();
+  for (int j = kPer - 1; j >= 0; --j) at = __shfl_sync(kFull, v[j], giver) == value ? j : at;
+  expert = value > -INFINITY ? giver * kPer + at : -1;
   return true;
 }
 
@@ -470,7 +459,6 @@ __device__ __forceinline__ int choose_many(float (&v)[kPer], bool biased, float 
 template <typename Elem, int kPer, bool kFew, bool kBiased>
 __global__ void __launch_bounds__(kThreads, kPer <= 8 ? kBlocksPerSm : 1) route_kernel(const __grid_constant__ RouteArgs a) {
   __shared__ Candidate candidates[kWarps][32 + 8];  // (the last 8: 32 experts)
-  __shared__ Slot2 slots[kWarps][32];
   __shared__ int taken_tokens;
   if (threadIdx.x == 0) taken_tokens = (int)blockDim.x >> 5;
   __syncthreads();
@@ -568,16 +556,15 @@ __global__ void __launch_bounds__(kThreads, kPer <= 8 ? kBlocksPerSm : 1) route_
       if constexpr (kFew) {
         if (!exact) {
           float rest;
-          bool fine = choose_top(v, best, topk, lane, slots[warp], rest);
+          float value;
+          bool fine = choose_top(v, best, topk, lane, chosen, value, rest);
           if (fine) {
-            const Slot2 s = lane < topk ? slots[warp][lane] : Slot2{-1, -INFINITY};
-            chosen = s.expert;
-            cx = s.v;
+            cx = value;
             if (biased) {
               // (a neighbour as near as that, the best of the rest after the last)
-              const float below = __shfl_down_sync(kFull, s.v, 1);
+              const float below = __shfl_down_sync(kFull, value, 1);
               if (chosen >= 0) cx = taken(Elem::get(row[chosen]));
-              fine = !__any_sync(kFull, chosen >= 0 && s.v - (lane + 1 < topk ? below : rest) <= tolerance(unit, s.v));
+              fine = !__any_sync(kFull, chosen >= 0 && value - (lane + 1 < topk ? below : rest) <= tolerance(unit, value));
             }
           }
           if (!fine) {
