@@ -20,10 +20,10 @@
 // likewise (settle_groups). More candidates than lanes take the whole token again (route_exact).
 //
 // Measured on GB300, a call among others: 32,768 tokens of 256 experts, top-8 of 4 of 8 groups, sigmoid
-// and bias 29 us; without bias and groups 18 us (k = 1: 12 us), where the logits are 33.5 MB, 5 us of
-// memory. Instructions bound it: 270 a token for k = 1, about 20 more a step, most of them on the
-// half-rate ALU pipe (steps that rescan the owner's registers took 70 each, 94 us in all; the
-// threshold for every token 42 us). One token, or eight: 2 to 3 us, launch and latency.
+// and bias 28 us; without bias and groups 18 us (k = 1: 12 us), where the logits are 33.5 MB, 5 us of
+// memory. Instructions bound it (690 and 400 a token, issued at 70% of the rate), most of them on the
+// half-rate ALU pipe; a step is about 15 (steps that rescan the owner's registers took 70 each, 94 us
+// in all; the threshold for every token 42 us). One token, or eight: 2 to 3 us, launch and latency.
 #pragma once
 
 #include "route.cuh"
