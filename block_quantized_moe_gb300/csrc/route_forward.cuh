@@ -17,7 +17,8 @@
 // s + bias is that of 64 bits: fp32 values are off by less than half of tolerance(), and where two
 // neighbours in the order are nearer than that (and not the same logit and bias, a tie in any
 // precision) the candidates' values are taken again in 64 bits, a lane each; groups at the border
-// likewise (settle_groups). More candidates than lanes take the whole token again (route_exact).
+// likewise (settle_groups), where the sizes of their values (not of their sums) leave it open. More
+// candidates than lanes take the whole token again (route_exact).
 //
 // Measured on GB300, a call among others: 32,768 tokens of 256 experts, top-8 of 4 of 8 groups, sigmoid
 // and bias 28 us; without bias and groups 18 us (k = 1: 12 us), where the logits are 33.5 MB, 5 us of
@@ -74,10 +75,19 @@ __device__ __forceinline__ float group_score(float a1, float a2, int best) {
   return best == 2 && a2 > -INFINITY ? a1 + a2 : a1;
 }
 
-// Group g's score on lane g, groups of any size.
+// How far a group's score may be from its score in 64 bits: its values are off by half of tolerance() each, by
+// their own sizes and not by their sum's (which biases of both signs leave small), and the sum by a rounding.
+__device__ __forceinline__ float group_slack(float unit, float a1, float a2, int best) {
+  const float size = best == 2 && a2 > -INFINITY ? fmaxf(fabsf(a1), fabsf(a2)) : fabsf(a1);
+  return a1 > -INFINITY ? tolerance(unit, size) : 0.0f;
+}
+
+// Group g's score on lane g, groups of any size, and its slack.
 template <int kPer>
-__device__ __forceinline__ float any_group_scores(const float (&v)[kPer], int lane, int groups, int size, int best) {
+__device__ __forceinline__ float any_group_scores(const float (&v)[kPer], float unit, int lane, int groups, int size, int best,
+                                                  float& slack) {
   float mine = -INFINITY;
+  slack = 0.0f;
   for (int g = 0; g < groups; ++g) {
     float a1 = -INFINITY, a2 = -INFINITY;
 #pragma unroll
@@ -87,27 +97,35 @@ __device__ __forceinline__ float any_group_scores(const float (&v)[kPer], int la
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) merge2(a1, a2, __shfl_xor_sync(kFull, a1, o), __shfl_xor_sync(kFull, a2, o));
-    if (lane == g) mine = group_score(a1, a2, best);
+    if (lane == g) mine = group_score(a1, a2, best), slack = group_slack(unit, a1, a2, best);
   }
   return mine;
 }
 
-// Whether this lane's group is among the `keep` best (lanes of a group next to each other, `lanes` of
-// them); the scores of the worst of those and of the best of the others (-inf where there is none).
-__device__ __forceinline__ bool keep_groups(float mine, int lane, int lanes, int keep, float& last, float& next) {
+// Whether this lane's group is among the `keep` best (lanes of a group next to each other, `lanes` of them).
+__device__ __forceinline__ bool keep_groups(float mine, int lane, int lanes, int keep) {
   bool in = false;
   const uint32_t below = (1u << (lane & ~(lanes - 1))) - 1u;  // the lanes of lower groups
   for (int t = 0; t < keep; ++t) {
     const float most = warp_top(mine);  // (-inf: groups of no expert that could be chosen)
-    last = most;
     const uint32_t all = __ballot_sync(kFull, mine == most);  // (by every lane, so not behind a condition)
     const bool is = mine == most && (all & below) == 0u;
     in = in || is;
     mine = is ? -INFINITY : mine;
   }
-  next = warp_top(mine);
   return in;
 }
+
+// The border between the groups kept and the others: the least that the score of a kept one may be in 64 bits, and
+// the most that one of the others may be (-inf where there is none).
+struct Border {
+  float low, high;
+  __device__ __forceinline__ Border(float mine, float slack, bool kept) {
+    low = -warp_top(kept ? slack - mine : -INFINITY);
+    high = warp_top(kept ? -INFINITY : mine + slack);
+  }
+  __device__ __forceinline__ bool unsure() const { return high > -INFINITY && low <= high; }
+};
 
 // fp64 -> integer of the same order (-0 and +0 are one): compared without the few fp64 units
 __device__ __forceinline__ int64_t key_of(double v) {
@@ -298,19 +316,19 @@ __device__ __forceinline__ double softmax_sum64(const float (&x)[kPer], float to
   return sum;
 }
 
-// The groups to keep where scores at the border (`last` the worst kept, `next` the best of the others) are nearer than
-// `near`: the groups that near to the border are compared by their best values in 64 bits, taken of
-// every expert that may be one of them. kept: whether this lane's group is. false: they are more than 32.
+// The groups to keep where the border is unsure: a kept group that may be below one of the others and another that may
+// be above a kept one are compared by their best values in 64 bits, taken of every expert that may be
+// one of them. kept: whether this lane's group is, in fp32 and then in 64 bits. false: they are more than 32.
 template <typename Elem, int kPer>
 __device__ __forceinline__ bool settle_groups(const float (&v)[kPer], const float (&x)[kPer], const RouteArgs& a,
-                                              const typename Elem::T* row, bool softmax, float top, float g1, float g2,
-                                              float mine, float last, float next, float near, int lane, int32_t* experts,
+                                              const typename Elem::T* row, bool softmax, float unit, float top, float g1,
+                                              float g2, float mine, float slack, Border border, int lane, int32_t* experts,
                                               bool& kept) {
   const int lanes = a.group_lanes, groups = a.router.groups, best = a.router.group_best;
-  const bool open = mine >= next - near && mine <= last + near;
+  const bool open = kept ? mine - slack <= border.high : mine > -INFINITY && mine + slack >= border.low;
   // (the values that make up the score; without a bias they are logits, and the order is theirs)
   const float least = best == 2 && g2 > -INFINITY ? g2 : g1;
-  const float from = a.bias != nullptr ? least - near : least;
+  const float from = a.bias != nullptr ? least - tolerance(unit, least) : least;
   uint32_t mask = 0u;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) mask |= (open && v[j] > -INFINITY && v[j] >= from ? 1u : 0u) << j;
@@ -334,7 +352,7 @@ __device__ __forceinline__ bool settle_groups(const float (&v)[kPer], const floa
     }
   }
   int64_t score = best == 2 && a2 > kNever64 ? key_of(value_of(a1) + value_of(a2)) : a1;
-  if (!open) score = mine > last ? INT64_MAX : kNever64;
+  if (!open) score = kept ? INT64_MAX : kNever64;
   int rank = 0;
   for (int g = 0; g < groups; ++g) {
     const int64_t other = __shfl_sync(kFull, score, g * lanes);
@@ -520,30 +538,34 @@ __global__ void __launch_bounds__(kThreads, kPer <= 8 ? kBlocksPerSm : 1) route_
         if constexpr (kFew) best = best3(v);
       } else if (lane_groups) {
         best = best3(v);
-        float g1 = best.a, g2 = best.b, last, next_best;
+        float g1 = best.a, g2 = best.b;
         for (int o = 1; o < a.group_lanes; o <<= 1) merge2(g1, g2, __shfl_xor_sync(kFull, g1, o), __shfl_xor_sync(kFull, g2, o));
         const bool inside = lane < a.router.groups * a.group_lanes;
-        float mine = group_score(g1, g2, a.router.group_best);
-        if (!biased && scored_groups && g2 > -INFINITY)  // (scores grow with the logits)
-          mine = score_fast(g1, softmax, top, largest_score) + score_fast(g2, softmax, top, largest_score);
-        else if (!biased && scored_groups && g1 > -INFINITY)
-          mine = score_fast(g1, softmax, top, largest_score);
-        if (!inside) mine = -INFINITY;
-        kept = keep_groups(mine, lane, a.group_lanes, a.router.group_topk, last, next_best);
-        const float near = 2.0f * tolerance(unit, last);
-        if (scored_groups && next_best > -INFINITY && last - next_best <= near)
-          exact = !settle_groups<Elem, kPer>(v, x, a, row, softmax, top, g1, g2, mine, last, next_best, near, lane,
-                                             reinterpret_cast<int32_t*>(candidates[warp] + 32), kept);
+        float h1 = g1, h2 = g2;
+        if (!biased && scored_groups) {  // (scores grow with the logits)
+          h1 = g1 > -INFINITY ? score_fast(g1, softmax, top, largest_score) : -INFINITY;
+          h2 = g2 > -INFINITY ? score_fast(g2, softmax, top, largest_score) : -INFINITY;
+        }
+        const float mine = inside ? group_score(h1, h2, a.router.group_best) : -INFINITY;
+        kept = keep_groups(mine, lane, a.group_lanes, a.router.group_topk);
+        if (scored_groups) {
+          const float slack = inside ? group_slack(unit, h1, h2, a.router.group_best) : 0.0f;
+          const Border border(mine, slack, kept);
+          if (border.unsure())
+            exact = !settle_groups<Elem, kPer>(v, x, a, row, softmax, unit, top, g1, g2, mine, slack, border, lane,
+                                               reinterpret_cast<int32_t*>(candidates[warp] + 32), kept);
+        }
         if (!kept) best = {-INFINITY, -INFINITY, -INFINITY};
       } else {
         const int size = E / a.router.groups;
-        float s[kPer], last, next_best;
+        float s[kPer], slack;
         if (!biased && scored_groups) scores(x, softmax, top, largest_score, s);
 #pragma unroll
         for (int j = 0; j < kPer; ++j) s[j] = !biased && scored_groups && x[j] > -INFINITY ? s[j] : v[j];
-        const float mine = any_group_scores(s, lane, a.router.groups, size, a.router.group_best);
-        const uint32_t groups = __ballot_sync(kFull, keep_groups(mine, lane, 1, a.router.group_topk, last, next_best));
-        exact = scored_groups && next_best > -INFINITY && last - next_best <= 2.0f * tolerance(unit, last);
+        const float mine = any_group_scores(s, unit, lane, a.router.groups, size, a.router.group_best, slack);
+        const bool in = keep_groups(mine, lane, 1, a.router.group_topk);
+        const uint32_t groups = __ballot_sync(kFull, in);
+        exact = scored_groups && Border(mine, slack, in).unsure();
         int group = lane * kPer / size, rest = lane * kPer - group * size;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
