@@ -71,8 +71,9 @@ __device__ __forceinline__ void add2(float& a1, float& a2, float v) {
   a2 = fmaxf(a2, fminf(a1, v));
   a1 = fmaxf(a1, v);
 }
+// (a sum is at least the lowest number: -inf is the score of a group of which nothing can be chosen)
 __device__ __forceinline__ float group_score(float a1, float a2, int best) {
-  return best == 2 && a2 > -INFINITY ? a1 + a2 : a1;
+  return best == 2 && a2 > -INFINITY ? fmaxf(a1 + a2, -FLT_MAX) : a1;
 }
 
 // How far a group's score may be from its score in 64 bits: its values are off by half of tolerance() each, by

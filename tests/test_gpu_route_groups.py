@@ -81,3 +81,24 @@ def test_sums_above_fp32(E, groups):
     for score in (ft.SCORE_SOFTMAX, ft.SCORE_SIGMOID):
         for keep in (1, 2, 3):
             check_ids(logits(300, E, E), ft.make_router(E, 5, score=score, groups=groups, group_topk=keep, group_best=2), bias)
+
+
+@pytest.mark.parametrize("E,groups", [(32, 4), (160, 8), (256, 8)])
+@pytest.mark.parametrize("low", [-LARGEST, -1e38])
+def test_sums_below_fp32(E, groups, low):
+    """Groups masked by the type's lowest value, whose two best sum to less than fp32 holds, are still ahead of groups
+    of which nothing can be chosen."""
+    size = E // groups
+    x, bias = logits(300, E, E), torch.full((E,), low, device=DEV)
+    x[:100, 2 * size:3 * size] = -float("inf")  # nothing left
+    x[100:200, :size] = -float("inf")
+    x[200:250, size:] = -float("inf")
+    x[250:260] = -float("inf")
+    bias[:size] = 0.0
+    if groups > 4:
+        bias[5 * size:6 * size] = low / 2
+    for score in (ft.SCORE_SOFTMAX, ft.SCORE_SIGMOID):
+        for keep in (1, 2, 3):
+            for topk in (4, min(32, keep * size)):
+                r = ft.make_router(E, topk, score=score, groups=groups, group_topk=keep, group_best=2)
+                check_ids(x, r, bias)
