@@ -83,12 +83,10 @@ __device__ __forceinline__ float group_slack(float unit, float a1, float a2, int
   return a1 > -INFINITY ? tolerance(unit, size) : 0.0f;
 }
 
-// Group g's score on lane g, groups of any size, and its slack.
+// Group g's two best values on lane g, groups of any size.
 template <int kPer>
-__device__ __forceinline__ float any_group_scores(const float (&v)[kPer], float unit, int lane, int groups, int size, int best,
-                                                  float& slack) {
-  float mine = -INFINITY;
-  slack = 0.0f;
+__device__ __forceinline__ void any_groups_best(const float (&v)[kPer], int lane, int groups, int size, float& g1, float& g2) {
+  g1 = g2 = -INFINITY;
   for (int g = 0; g < groups; ++g) {
     float a1 = -INFINITY, a2 = -INFINITY;
 #pragma unroll
@@ -98,9 +96,8 @@ __device__ __forceinline__ float any_group_scores(const float (&v)[kPer], float 
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) merge2(a1, a2, __shfl_xor_sync(kFull, a1, o), __shfl_xor_sync(kFull, a2, o));
-    if (lane == g) mine = group_score(a1, a2, best), slack = group_slack(unit, a1, a2, best);
+    if (lane == g) g1 = a1, g2 = a2;
   }
-  return mine;
 }
 
 // Whether this lane's group is among the `keep` best (lanes of a group next to each other, `lanes` of them).
@@ -559,14 +556,15 @@ __global__ void __launch_bounds__(kThreads, kPer <= 8 ? kBlocksPerSm : 1) route_
         if (!kept) best = {-INFINITY, -INFINITY, -INFINITY};
       } else {
         const int size = E / a.router.groups;
-        float s[kPer], slack;
+        float s[kPer], g1, g2;
         if (!biased && scored_groups) scores(x, softmax, top, largest_score, s);
 #pragma unroll
         for (int j = 0; j < kPer; ++j) s[j] = !biased && scored_groups && x[j] > -INFINITY ? s[j] : v[j];
-        const float mine = any_group_scores(s, unit, lane, a.router.groups, size, a.router.group_best, slack);
+        any_groups_best(s, lane, a.router.groups, size, g1, g2);
+        const float mine = group_score(g1, g2, a.router.group_best);
         const bool in = keep_groups(mine, lane, 1, a.router.group_topk);
         const uint32_t groups = __ballot_sync(kFull, in);
-        exact = scored_groups && Border(mine, slack, in).unsure();
+        exact = scored_groups && Border(mine, group_slack(unit, g1, g2, a.router.group_best), in).unsure();
         int group = lane * kPer / size, rest = lane * kPer - group * size;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
