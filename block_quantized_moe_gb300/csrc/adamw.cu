@@ -265,6 +265,10 @@ __device__ __forceinline__ void step8(const Step& s, const Entry& t, const Chunk
   c.moments(m, v);
   update8(s, p, g, m, v);
   elem_store8<P>(static_cast<typename P::T*>(t.param) + at, vec, n, p);
+  if constexpr (sizeof(typename P::T) == 2) {  // the copy is of the parameter as it is kept
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = P::get(P::put(p[i]));
+  }
   if (copy_dtype == FTMOE_OUT_BF16) elem_store8<ElemBf16>(static_cast<uint16_t*>(t.copy) + at, vec, n, p);
   else if (copy_dtype == FTMOE_OUT_FP16) elem_store8<ElemF16>(static_cast<uint16_t*>(t.copy) + at, vec, n, p);
   if constexpr (k8) {

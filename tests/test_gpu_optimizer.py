@@ -451,3 +451,11 @@ def test_betas_of_zero_and_steps_of_a_device_below_one():
 
 def test_no_tensors():
     ft.ftmoe_adamw_step(ft.make_adamw_list([], [], [], []))
+
+
+@pytest.mark.parametrize("narrow", [False, True])
+@pytest.mark.parametrize("gdtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("pdtype,copy", [("bf16", "fp16"), ("fp16", "bf16"), ("bf16", "bf16"), ("fp16", "fp16")])
+def test_copies_of_16_bit_parameters(pdtype, copy, gdtype, narrow):
+    """The copy is the new parameter as it is kept, in the copy's type."""
+    check_step(state((20_000, 33, 7), gdtype, pdtype, narrow, copy), pdtype=pdtype, copy=copy)
