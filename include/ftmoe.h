@@ -564,9 +564,10 @@ ftmoe_status ftmoe_route_tokens(const void* logits, int32_t dtype, int64_t token
  *   sigmoid, renormalize:   dlogits[id_i] = (1 - s[id_i]) (r_i - w_i R / c)    others 0
  *   sigmoid:                dlogits[id_i] = (1 - s[id_i]) r_i                  others 0
  * Inactive routes (id < 0) take no part, whatever their weight and gradient; a token without an
- * active route gets zeros and its logits are not read. An id that occurs twice in a token gets the
- * sum; one >= num_experts raises FTMOE_ERR_EXPERT_ID_RANGE and takes no part. dlogits
- * [tokens][num_experts] is dlogits_dtype with row stride ld_dlogits; every element is written. */
+ * active route gets zeros, whatever its logits are (they may be read all the same: logits holds
+ * every one of the [tokens][num_experts]). An id that occurs twice in a token gets the sum; one >=
+ * num_experts raises FTMOE_ERR_EXPERT_ID_RANGE and takes no part. dlogits [tokens][num_experts] is
+ * dlogits_dtype with row stride ld_dlogits; every element is written. */
 ftmoe_status ftmoe_route_tokens_backward(const void* logits, int32_t dtype, int64_t tokens, int64_t ld,
                                          const ftmoe_router* router, const int32_t* expert_ids, const float* weights,
                                          const float* dweights, void* dlogits, int32_t dlogits_dtype,

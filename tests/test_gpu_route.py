@@ -368,6 +368,24 @@ def test_gradient_of_masked_logits():
             assert torch.isfinite(d).all() and (d[0, ::2] == 0).all() and (d[1, 3:] == 0).all() and (d[2] == 0).all()
 
 
+@pytest.mark.parametrize("value", [0.0, math.nan, math.inf, -math.inf, 3e38])
+@pytest.mark.parametrize("E,k", [(64, 8), (256, 6), (600, 17)])
+def test_logits_of_tokens_without_routes_make_no_difference(E, k, value):
+    """Whatever such rows hold, every row has the same bits, those that share a warp with one too."""
+    x = logits(1000, E, "fp32", E)
+    for score in ("softmax", "sigmoid"):
+        for renorm in (False, True):
+            r = router(E, k, score, renormalize=renorm)
+            ids, w = route(x, r)
+            ids[1::3], ids[500:510] = -1, -1
+            dw = torch.linspace(-1.0, 1.0, k, device=DEV).repeat(1000, 1)
+            want, d = torch.full_like(x, 7.0), torch.full_like(x, 7.0)
+            ft.ftmoe_route_tokens_backward(x, r, ids, w, dw, want)
+            y = torch.where((ids < 0).all(1, keepdim=True), torch.full_like(x, value), x)
+            ft.ftmoe_route_tokens_backward(y, r, ids, w, dw, d)
+            assert torch.equal(d, want) and (d[1::3] == 0).all() and (d[500:510] == 0).all()
+
+
 def test_zero_tokens():
     x, r = torch.empty(0, 64, device=DEV), router(64, 4)
     ids, w = route(x, r)
