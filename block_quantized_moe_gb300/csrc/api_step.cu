@@ -1,5 +1,6 @@
 // C ABI of the operators around the experts' products (routing, gradient norm, AdamW): argument
 // checks on the host, then launches on the caller's stream (no allocation, no synchronisation).
+#include <cfloat>
 #include <cmath>
 
 #include "common.cuh"
@@ -114,7 +115,7 @@ ftmoe_status ftmoe_adamw_step(const ftmoe_adamw_list* list, const ftmoe_adamw* o
       (list->copy_dtype != -1 && !half_dtype(list->copy_dtype)) ||
       (list->moments != FTMOE_MOMENTS_FP32 && list->moments != FTMOE_MOMENTS_8BIT) || (list->count > 0 && !list->tensors))
     return FTMOE_INVALID_ARG;
-  if (!std::isfinite(opt->lr) || !std::isfinite(opt->weight_decay) || !(opt->eps >= 1e-30) || !(opt->eps <= 1e30) ||
+  if (!(std::fabs(opt->lr) <= FLT_MAX) || !(std::fabs(opt->weight_decay) <= FLT_MAX) || !(opt->eps >= 1e-30) || !(opt->eps <= 1e30) ||
       !(opt->beta1 >= 0.0) || !(opt->beta1 < 1.0) || !(opt->beta2 >= 0.0) || !(opt->beta2 < 1.0) ||
       (!opt->step_dev && opt->step < 1))
     return FTMOE_INVALID_ARG;

@@ -638,7 +638,7 @@ typedef struct ftmoe_adamw_list {
 } ftmoe_adamw_list;
 
 typedef struct ftmoe_adamw {
-  double lr, beta1, beta2, eps, weight_decay; /* eps >= 1e-30; 0 <= beta < 1 */
+  double lr, beta1, beta2, eps, weight_decay; /* finite in fp32; eps >= 1e-30; 0 <= beta < 1 */
   int64_t step;            /* t, counted from 1 */
   uint32_t seed;           /* of the 8-bit moments' rounding */
   const float* lr_dev;     /* optional device float[1] in place of lr */

@@ -109,6 +109,15 @@ def test_adamw_refusals(ft):
     assert f(None, None, None) == bad
 
 
+def test_adamw_constants_beyond_fp32_are_refused(ft):
+    """The step is computed in fp32: a rate or decay that is infinite there is an error, not NaN parameters."""
+    no_tensors = ft.AdamwList(2, 0, -1, 0, 0, None)
+    for kw, want in ((dict(lr=3e38), ft.FTMOE_OK), (dict(weight_decay=-3e38), ft.FTMOE_OK), (dict(lr=1e39), ft.FTMOE_INVALID_ARG),
+                     (dict(lr=-1e39), ft.FTMOE_INVALID_ARG), (dict(weight_decay=1e300), ft.FTMOE_INVALID_ARG)):
+        opt = ft.Adamw(**{**dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.1, step=1, seed=0), **kw})
+        assert ft.lib().ftmoe_adamw_step(no_tensors, ctypes.addressof(opt), None) == want, kw
+
+
 def test_packed_options_are_the_structure(ft):
     packed = ft._pack_adamw(1.0, 2.0, 3.0, 4.0, 5.0, 6, 7, 8, 9, 10)
     o = ft.Adamw.from_buffer_copy(packed)
