@@ -5,7 +5,9 @@
 // Elementwise: 24 bytes an element and the gradient with fp32 moments, 12 1/8 and the gradient with
 // 8-bit ones (p 8, codes 4, scales 1/8), and 2 for a 16-bit copy. Memory bounds it. Measured on GB300,
 // 939 M fp32 parameters with bf16 gradients and copies: 3.84 ms with fp32 moments (101% of the measured
-// copy rate), 2.28 ms with 8-bit ones (98%; 52 instructions an element, 56% of the issue slots).
+// copy rate), 2.28 ms with 8-bit ones (98%; 52 instructions an element, 56% of the issue slots). The same in
+// bf16 parameters without copies: 3.00 ms (102%), and 1.65 ms with 8-bit moments (85%: 10 bytes an element
+// under the same instructions).
 //
 // 8-bit moments: per 32 elements a power of two, codes e4m3 (m) and e5m2 (v), stochastically rounded.
 // With beta2 = 0.999 v moves by a thousandth of itself a step, far below half of e5m2's step: rounded

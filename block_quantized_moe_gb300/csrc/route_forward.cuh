@@ -7,12 +7,13 @@
 //
 // A warp per token, the next token's logits on their way meanwhile; lane l holds the experts
 // [l * kPer, (l + 1) * kPer). Top-k (choose_top): each lane keeps its three best values, and each of the
-// k steps takes the largest of the lanes' best. Where a lane gives all three (5% of tokens for 8 of 256,
-// 20% where half of the groups are left; four values a lane cost every token as much as that) or
-// values are too near (below), choose_few takes over: the k-th largest of the lanes' maxima is a
-// threshold that at least k values reach and few more do; they go to a lane each and are ranked by a
-// count. A choice of more than kFewTopk, which would have too many for both, takes the largest out of
-// its lane's registers step by step (choose_many).
+// k steps takes the largest of the lanes' best. Where a lane gives all three (3% of tokens for 8 of 256
+// normal logits, 6 to 10% where half of the groups are left; four values a lane cost every token as much
+// as that) or values are too near (below), choose_few takes over: the k-th largest of the lanes' maxima is
+// a threshold that at least k values reach and few more do; they go to a lane each and are ranked by a
+// count. (Where fewer than k lanes are left, or lanes have equal maxima, the threshold falls, at worst to
+// the lowest number.) A choice of more than kFewTopk, which would have too many for both, takes the
+// largest out of its lane's registers step by step (choose_many).
 // Without a bias the logits themselves are the order and nothing is rounded. With one, the order of
 // s + bias is that of 64 bits: fp32 values are off by less than half of tolerance(), and where two
 // neighbours in the order are nearer than that (and not the same logit and bias, a tie in any
@@ -21,10 +22,15 @@
 // candidates than lanes take the whole token again (route_exact).
 //
 // Measured on GB300, a call among others: 32,768 tokens of 256 experts, top-8 of 4 of 8 groups, sigmoid
-// and bias 28 us; without bias and groups 18 us (k = 1: 12 us), where the logits are 33.5 MB, 5 us of
-// memory. Instructions bound it (690 and 400 a token, issued at 70% of the rate), most of them on the
+// and bias 28 us; without bias and groups 17.5 us (k = 1: 12 us), where the logits are 33.5 MB, 5 us of
+// memory. Instructions bound it (683 and 440 a token, issued in 72% of the cycles), most of them on the
 // half-rate ALU pipe; a step is about 15 (steps that rescan the owner's registers took 70 each, 94 us
 // in all; the threshold for every token 42 us). One token, or eight: 2 to 3 us, launch and latency.
+// Slow are the routers and rows that go to 64 bits whole (32,768 tokens, sigmoid, bias): kept groups of
+// fewer lanes than k that hold more than 32 experts (512 experts, 2 of 8 groups, top-10: 71% of tokens,
+// 0.91 ms; all groups 40 us; 1,024, 1 of 8, top-12: every token, 2.3 ms), rows of more than 32 equal logits
+// under one bias, or with k above kFewTopk of any equal ones (256 experts, top-16, bf16: 0.40 ms; without
+// a bias 54 us).
 #pragma once
 
 #include "route.cuh"
@@ -244,7 +250,7 @@ __device__ __forceinline__ Best3 best3(const float (&v)[kPer]) {
 
 // Top-k from the lanes' three best values: each step takes the largest of the lanes' best, and its lane's
 // next moves up. Lane t gets the expert of slot t (-1: none) and its value; rest: the best value left.
-// false: a lane gave three, and what it has left is not known (5% of tokens for 8 of 256 experts), or
+// false: a lane gave three, and what it has left is not known (3% of tokens for 8 of 256 experts), or
 // two that are equal, or there are not enough (-inf comes from the lowest lane again and again).
 // (A step is a maximum and a vote over the warp, 24 cycles each; selects rather than branches, and
 // no first-set-bit, which runs at a quarter of the vote's rate. The experts' places in their lanes are

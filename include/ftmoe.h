@@ -542,8 +542,8 @@ typedef struct ftmoe_router {
  *   weights[i] = scale * s[id_i]             or, with renormalize,
  *   weights[i] = scale * s[id_i] / sum_j s[id_j].
  * Ties go to the lower group and the lower expert. The order is that of the values in 64 bits
- * (computed in fp32, and in fp64 wherever fp32 does not settle it); without bias that of the
- * logits. An expert whose logit or bias is -inf or NaN is never chosen (a NaN or -inf logit counts as
+ * (computed in fp32, and in fp64 wherever fp32 does not settle it; values that differ by fp64's own
+ * rounding alone may come in either order); without bias that of the logits. An expert whose logit or bias is -inf or NaN is never chosen (a NaN or -inf logit counts as
  * exp(x) = 0 in the softmax), +inf counts as the largest finite number; where fewer than topk
  * experts are left the last slots are inactive routes, id -1 and weight 0. The weights are fp32, from
  * fp32 exponentials; renormalised ones keep their ratios where every chosen sigmoid underflows.
@@ -610,7 +610,8 @@ ftmoe_status ftmoe_grad_norm(const ftmoe_grad_list* list, float scale, float max
  * stochastically: up with the probability of what is cut off (to 16 bits), so that moments which
  * change by less than half a step still move, on average by what they should. A v above zero is
  * never rounded to zero (its code is at least 1). NaN and infinite moments stay so (an infinite one
- * as the largest code of a group whose value of it is infinite in fp32). The random bits are a hash
+ * as the largest code of a group whose value of it is infinite in fp32; finite ones above 1.75 * 2^127
+ * may become infinite). The random bits are a hash
  * of (seed, step, the tensor's place in the list, element): another seed or step gives others. */
 typedef enum ftmoe_moments { FTMOE_MOMENTS_FP32 = 0, FTMOE_MOMENTS_8BIT = 1 } ftmoe_moments;
 
@@ -629,7 +630,8 @@ typedef struct ftmoe_adamw_tensor {
 /* Many tensors of the same types. `tensors` is a HOST array of count entries, read during the
  * call only. No array may overlap another one of the call, of the same or another tensor. */
 typedef struct ftmoe_adamw_list {
-  int32_t param_dtype; /* ftmoe_out_dtype; 16-bit parameters are rounded to nearest even at each step */
+  int32_t param_dtype; /* ftmoe_out_dtype; 16-bit parameters are rounded to nearest even at each step,
+                          so that updates below half a unit in their last place are lost */
   int32_t grad_dtype;  /* ftmoe_out_dtype */
   int32_t copy_dtype;  /* FTMOE_OUT_BF16 or FTMOE_OUT_FP16; -1: no copies */
   int32_t moments;     /* ftmoe_moments */
